@@ -3,7 +3,9 @@
 The table and every operation on it live in the HIP library ``libhkv.so``
 behind the C ABI of ``include/hkv.h``; this package is its Python binding.
 ``HashTable`` owns one table and allocates output tensors; the functions of
-``hash_table_cache_amd._native`` mirror the C entry points one to one.
+``hash_table_cache_amd._native`` mirror the C entry points one to one. The
+training operators (losses on logits, gradient clipping) are functions of
+``hash_table_cache_amd.training`` on the library ``libhkv_train.so``.
 """
 
 from __future__ import annotations
@@ -35,9 +37,19 @@ from ._native import (  # noqa: F401
     hkv_set_outcome_counters,
     hkv_size,
 )
+from .training import (
+    PolicyLoss,
+    PreferenceLoss,
+    clip_grad_norm,
+    policy_loss,
+    preference_loss,
+    token_logprobs,
+    token_logprobs_backward,
+)
 
 __all__ = ["HashTable", "HkvError", "BUCKET_SLOTS", "EMPTY_KEY", "LOCKED_KEY", "HKV_FLAG_SERIAL_INSERT",
-           "HKV_FLAG_RW_LOCK", "HKV_FLAG_UNIQUE_KEYS"]
+           "HKV_FLAG_RW_LOCK", "HKV_FLAG_UNIQUE_KEYS", "PolicyLoss", "PreferenceLoss", "clip_grad_norm",
+           "policy_loss", "preference_loss", "token_logprobs", "token_logprobs_backward"]
 
 
 class HashTable:

@@ -1,5 +1,6 @@
-"""Builds the HIP library ``_lib/libhkv.so`` for gfx950 with hipcc, and the
-multi-threaded mixed-workload driver ``_lib/libhkv_mixed.so`` on top of it.
+"""Builds the HIP library ``_lib/libhkv.so`` for gfx950 with hipcc, the
+multi-threaded mixed-workload driver ``_lib/libhkv_mixed.so`` on top of it,
+and the training operators' library ``_lib/libhkv_train.so``.
 
 Run as ``python -m hash_table_cache_amd.build``. Cross-compiles without a GPU.
 The objects compile in parallel.
@@ -25,6 +26,10 @@ SOURCES = [CSRC / "hkv_kernels.hip", CSRC / "hkv_runtime.cpp"]
 # library of its own on top of the C ABI
 MIXED_SOURCE = CSRC / "hkv_mixed_driver.cpp"
 MIXED_LIB_PATH = PKG / "_lib" / "libhkv_mixed.so"
+# the training operators (include/hkv_train.h), a library of their own: they
+# work on logits and gradients and hold no table
+TRAIN_SOURCES = [CSRC / "hkv_train_kernels.hip", CSRC / "hkv_train.cpp"]
+TRAIN_LIB_PATH = PKG / "_lib" / "libhkv_train.so"
 ARCH = "gfx950"
 
 
@@ -40,7 +45,7 @@ def compile_flags() -> list[str]:
         "-std=c++17",
         "-fPIC",
         "-fvisibility=hidden",
-        # packed fp32 instructions stay off (no float arithmetic here anyway)
+        # packed fp32 instructions stay off
         "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
         "-Wall",
         "-I", str(INCLUDE),
@@ -69,8 +74,8 @@ def _compile(src: pathlib.Path, verbose: bool) -> pathlib.Path:
 def build(verbose: bool = False) -> pathlib.Path:
     BUILD_DIR.mkdir(parents=True, exist_ok=True)
     LIB_PATH.parent.mkdir(parents=True, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=3) as pool:
-        futs = [pool.submit(_compile, src, verbose) for src in (*SOURCES, MIXED_SOURCE)]
+    with concurrent.futures.ThreadPoolExecutor(max_workers=5) as pool:
+        futs = [pool.submit(_compile, src, verbose) for src in (*SOURCES, MIXED_SOURCE, *TRAIN_SOURCES)]
         objs = [f.result() for f in futs]
     tmp = LIB_PATH.with_suffix(".so.tmp")
     _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", str(tmp), *map(str, objs[:2])], verbose)
@@ -79,6 +84,9 @@ def build(verbose: bool = False) -> pathlib.Path:
     _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", str(tmp), str(objs[2]),
           f"-L{LIB_PATH.parent}", "-lhkv", "-Wl,-rpath,$ORIGIN", "-pthread"], verbose)
     tmp.replace(MIXED_LIB_PATH)
+    tmp = TRAIN_LIB_PATH.with_suffix(".so.tmp")
+    _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", str(tmp), *map(str, objs[3:])], verbose)
+    tmp.replace(TRAIN_LIB_PATH)
     return LIB_PATH
 
 

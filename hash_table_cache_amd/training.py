@@ -1,0 +1,322 @@
+"""Training operators between a table's ``find`` and its ``assign``.
+
+ctypes binding of ``libhkv_train.so`` (the C ABI of ``include/hkv_train.h``,
+which states the formulas): every step runs in the HIP library; the functions
+here check their arguments, allocate outputs and workspace and pass pointers.
+There is no fallback implementation.
+
+Logits are two-dimensional [rows, vocab] tensors of float32, bfloat16 or
+float16 whose rows may lie inside wider ones (stride(0) >= vocab, stride(1) ==
+1). Labels are int64; a negative one leaves its row out. Work is enqueued on
+``stream`` (a ``torch.cuda.Stream`` or a handle; torch's current stream by
+default), and what a call allocates belongs to that stream. Gradients are
+returned, not recorded: pass one on with ``logits.backward(grad)``.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import pathlib
+from typing import NamedTuple, Optional
+
+import torch
+
+from ._native import HKV_OK, HkvError
+
+LIB_PATH = pathlib.Path(__file__).resolve().parent / "_lib" / "libhkv_train.so"
+
+# Every entry point declared in include/hkv_train.h.
+EXPORTS = (
+    "hkv_train_workspace_bytes",
+    "hkv_token_logprobs",
+    "hkv_token_logprobs_backward",
+    "hkv_preference_loss",
+    "hkv_policy_loss",
+    "hkv_clip_grad_norm",
+    "hkv_train_last_error",
+)
+
+KINDS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class PreferenceLoss(NamedTuple):
+    loss: torch.Tensor  # [] float32: the mean over pairs
+    losses: torch.Tensor  # [pairs] float32
+    rewards: torch.Tensor  # [2 * pairs] float32
+    logp: torch.Tensor  # [rows] float32
+    grad: Optional[torch.Tensor]  # like logits
+
+
+class PolicyLoss(NamedTuple):
+    loss: torch.Tensor  # [] float32: the weighted sum
+    token_loss: torch.Tensor  # [rows] float32
+    kl: torch.Tensor  # [rows] float32
+    logp: torch.Tensor  # [rows] float32
+    grad: Optional[torch.Tensor]  # like logits
+
+
+def _load() -> ctypes.CDLL:
+    if not LIB_PATH.exists():
+        raise ImportError(
+            f"{LIB_PATH} is missing; build it with `python -m hash_table_cache_amd.build`"
+        )
+    L = ctypes.CDLL(str(LIB_PATH))
+    vp, u64, u32, f32, st = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_float, ctypes.c_int32
+    logits = [u64, u64, u32, vp, u64, vp, f32]
+    L.hkv_train_workspace_bytes.argtypes = [u64, u64, u64]
+    L.hkv_train_workspace_bytes.restype = u64
+    L.hkv_token_logprobs.argtypes = [*logits, vp, vp, vp, u64, vp]
+    L.hkv_token_logprobs.restype = st
+    L.hkv_token_logprobs_backward.argtypes = [*logits, vp, vp, vp, u64, vp]
+    L.hkv_token_logprobs_backward.restype = st
+    L.hkv_preference_loss.argtypes = [*logits, u64, vp, vp, f32, f32, f32, vp, vp, vp, vp, vp, u64, vp, u64, vp]
+    L.hkv_preference_loss.restype = st
+    L.hkv_policy_loss.argtypes = [*logits, vp, vp, vp, vp, f32, f32, f32, f32, vp, vp, vp, vp, vp, u64, vp, u64, vp]
+    L.hkv_policy_loss.restype = st
+    L.hkv_clip_grad_norm.argtypes = [u64, vp, vp, vp, vp, f32, vp, vp, u64, vp]
+    L.hkv_clip_grad_norm.restype = st
+    L.hkv_train_last_error.argtypes = []
+    L.hkv_train_last_error.restype = ctypes.c_char_p
+    return L
+
+
+_LIB = None
+
+
+def load() -> ctypes.CDLL:
+    """The loaded ``libhkv_train.so`` (loaded on the first call)."""
+    global _LIB
+    if _LIB is None:
+        _LIB = _load()
+    return _LIB
+
+
+def _check(status: int) -> None:
+    if status != HKV_OK:
+        raise HkvError(status, load().hkv_train_last_error().decode(errors="replace"))
+
+
+class _On:
+    """The stream of a call: its handle, and the context in which the call's
+    tensors are allocated, so that they belong to that stream."""
+
+    def __init__(self, stream, device):
+        self.ctx = None
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        self.handle = stream.cuda_stream
+        self.ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _logits(x, labels):
+    if x.dtype not in KINDS:
+        raise TypeError(f"logits: dtype {x.dtype} not in {tuple(KINDS)}")
+    if x.dim() != 2:
+        raise ValueError(f"logits must have two dimensions, rows and vocab, not {x.dim()}")
+    if not x.is_cuda:
+        raise ValueError("logits must be on a GPU")
+    rows, vocab = x.shape
+    if vocab == 0:
+        raise ValueError("logits have no columns")
+    _vector(labels, torch.int64, rows, "labels", x.device)
+    return rows, vocab, _row_stride(x, "logits")
+
+
+def _row_stride(x, name):
+    rows, vocab = x.shape
+    s0, s1 = x.stride()
+    if vocab > 1 and s1 != 1:
+        raise ValueError(f"{name}: the elements of a row must be next to each other (stride(1) is {s1})")
+    if rows > 1 and s0 < vocab:
+        raise ValueError(f"{name}: rows overlap (stride(0) is {s0}, vocab {vocab})")
+    return s0 if rows > 1 else vocab
+
+
+def _vector(t, dtype, numel, name, device):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} is not {dtype}")
+    if t.dim() != 1 or t.shape[0] != numel:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs [{numel}]")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, logits on {device}")
+    return t.data_ptr()
+
+
+def _grad(x, grad_out):
+    """The tensor that takes the gradient, and its row stride."""
+    if grad_out is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device), x.shape[1]
+    if grad_out.dtype != x.dtype or grad_out.shape != x.shape or grad_out.device != x.device:
+        raise ValueError(f"grad_out: {grad_out.dtype} {tuple(grad_out.shape)} on {grad_out.device}, "
+                         f"logits are {x.dtype} {tuple(x.shape)} on {x.device}")
+    return grad_out, _row_stride(grad_out, "grad_out")
+
+
+def _workspace(rows, pairs, tensors, device):
+    n = load().hkv_train_workspace_bytes(rows, pairs, tensors)
+    return torch.empty(n, dtype=torch.uint8, device=device), n
+
+
+def token_logprobs(logits, labels, *, temperature: float = 1.0, stream=None):
+    """(logp, lse), both [rows] float32: the log-probability of each row's
+    label under softmax(logits / temperature), and the normaliser."""
+    rows, vocab, stride = _logits(logits, labels)
+    dev = logits.device
+    with _On(stream, dev) as s:
+        out = torch.empty((2, rows), dtype=torch.float32, device=dev)
+        ws, n = _workspace(rows, 0, 0, dev)
+        logp, lse = out.unbind(0)
+        _check(load().hkv_token_logprobs(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride,
+                                         labels.data_ptr(), temperature, logp.data_ptr(), lse.data_ptr(),
+                                         ws.data_ptr(), n, s))
+    return logp, lse
+
+
+def token_logprobs_backward(logits, labels, lse, grad_logp, *, temperature: float = 1.0, grad_out=None, stream=None):
+    """The gradient of (grad_logp * logp).sum() with respect to the logits;
+    grad_out takes it where given (it may be the logits)."""
+    rows, vocab, stride = _logits(logits, labels)
+    dev = logits.device
+    z = _vector(lse, torch.float32, rows, "lse", dev)
+    g = _vector(grad_logp, torch.float32, rows, "grad_logp", dev)
+    with _On(stream, dev) as s:
+        grad_out, gstride = _grad(logits, grad_out)
+        _check(load().hkv_token_logprobs_backward(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride,
+                                                  labels.data_ptr(), temperature, z, g, grad_out.data_ptr(),
+                                                  gstride, s))
+    return grad_out
+
+
+def preference_loss(logits, labels, cu_seqlens, ref_logp=None, *, beta: float = 0.1, label_smoothing: float = 0.0,
+                    temperature: float = 1.0, grad_scale: float = 1.0, with_grad: bool = True, grad_out=None,
+                    stream=None) -> PreferenceLoss:
+    """Preference loss on pairs of sequences: 2p preferred to 2p + 1, each the
+    rows [cu_seqlens[s], cu_seqlens[s + 1]). cu_seqlens: [2 * pairs + 1] int64;
+    ref_logp: [rows] float32 log-probabilities of the reference (token_logprobs
+    of its logits), 0 where not given. grad is grad_scale times the gradient of
+    loss; with_grad=False leaves it out."""
+    rows, vocab, stride = _logits(logits, labels)
+    dev = logits.device
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] % 2 != 1:
+        raise ValueError(f"cu_seqlens has shape {tuple(cu_seqlens.shape)}, needs [2 * pairs + 1]")
+    pairs = cu_seqlens.shape[0] // 2
+    cu = _vector(cu_seqlens, torch.int64, 2 * pairs + 1, "cu_seqlens", dev)
+    ref = None if ref_logp is None else _vector(ref_logp, torch.float32, rows, "ref_logp", dev)
+    with _On(stream, dev) as s:
+        out = torch.empty(1 + 3 * pairs + rows, dtype=torch.float32, device=dev)
+        loss, losses, rewards, logp = out.split((1, pairs, 2 * pairs, rows))
+        gptr, gstride = None, 0
+        if with_grad:
+            grad_out, gstride = _grad(logits, grad_out)
+            gptr = grad_out.data_ptr()
+        else:
+            grad_out = None
+        ws, n = _workspace(rows, pairs, 0, dev)
+        _check(load().hkv_preference_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride,
+                                          labels.data_ptr(), temperature, pairs, cu, ref, beta, label_smoothing,
+                                          grad_scale, loss.data_ptr(), losses.data_ptr(), rewards.data_ptr(),
+                                          logp.data_ptr(), gptr, gstride, ws.data_ptr(), n, s))
+    return PreferenceLoss(loss.view(()), losses, rewards, logp, grad_out)
+
+
+def policy_loss(logits, labels, old_logp, advantages, weights, ref_logp=None, *, clip_low: float = 0.2,
+                clip_high: float = 0.2, kl_coef: float = 0.0, temperature: float = 1.0, grad_scale: float = 1.0,
+                with_grad: bool = True, grad_out=None, stream=None) -> PolicyLoss:
+    """Clipped policy loss with a divergence term. old_logp, advantages,
+    weights (what each row counts in the sum), ref_logp: [rows] float32; a
+    kl_coef needs ref_logp. grad is grad_scale times the gradient of loss;
+    with_grad=False leaves it out."""
+    rows, vocab, stride = _logits(logits, labels)
+    dev = logits.device
+    old = _vector(old_logp, torch.float32, rows, "old_logp", dev)
+    adv = _vector(advantages, torch.float32, rows, "advantages", dev)
+    wts = _vector(weights, torch.float32, rows, "weights", dev)
+    ref = None if ref_logp is None else _vector(ref_logp, torch.float32, rows, "ref_logp", dev)
+    if kl_coef != 0.0 and ref is None:
+        raise ValueError("kl_coef needs ref_logp")
+    with _On(stream, dev) as s:
+        out = torch.empty(1 + 3 * rows, dtype=torch.float32, device=dev)
+        loss, token_loss, kl, logp = out.split((1, rows, rows, rows))
+        gptr, gstride = None, 0
+        if with_grad:
+            grad_out, gstride = _grad(logits, grad_out)
+            gptr = grad_out.data_ptr()
+        else:
+            grad_out = None
+        ws, n = _workspace(rows, 0, 0, dev)
+        _check(load().hkv_policy_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
+                                      temperature, old, adv, wts, ref, clip_low, clip_high, kl_coef, grad_scale,
+                                      loss.data_ptr(), token_loss.data_ptr(), kl.data_ptr(), logp.data_ptr(), gptr,
+                                      gstride, ws.data_ptr(), n, s))
+    return PolicyLoss(loss.view(()), token_loss, kl, logp, grad_out)
+
+
+def _dense(t) -> bool:
+    """Whether t's elements fill one stretch of memory, in whatever order of its axes."""
+    if t.is_contiguous():
+        return True
+    want = 1
+    for size, step in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n != 1), key=lambda p: p[1]):
+        if step != want:
+            return False
+        want *= size
+    return True
+
+
+def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
+    """Scales the gradients (a sequence of tensors, of mixed float types) so
+    that their global 2-norm is at most max_norm; returns the norm that they
+    had ([] float32, on their GPU). out: tensors like the gradients that take
+    the result (by default it replaces them). Each tensor has to fill one
+    stretch of memory; the order of its axes is free, and out's is the same."""
+    grads = list(grads)
+    if not grads:
+        raise ValueError("clip_grad_norm needs at least one tensor")
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"{len(outs)} tensors in out, {len(grads)} gradients")
+    dev = grads[0].device
+    if dev.type != "cuda":
+        raise ValueError("gradients must be on a GPU")
+    n = len(grads)
+    for i, g in enumerate(grads):
+        if g.dtype not in KINDS:
+            raise TypeError(f"gradient {i}: dtype {g.dtype} not in {tuple(KINDS)}")
+        if g.device != dev:
+            raise ValueError(f"gradient {i} is on {g.device}, the first on {dev}")
+        if not _dense(g):
+            raise ValueError(f"gradient {i} does not fill one stretch of memory (strides {g.stride()})")
+    if out is not None:
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if o.dtype != g.dtype or o.shape != g.shape or o.device != dev:
+                raise ValueError(f"out {i}: {o.dtype} {tuple(o.shape)} on {o.device}, its gradient is {g.dtype} "
+                                 f"{tuple(g.shape)} on {dev}")
+            if o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous()):
+                raise ValueError(f"out {i} has strides {o.stride()}, its gradient {g.stride()}")
+    pointers = ctypes.c_void_p * n
+    ptrs = pointers(*[g.data_ptr() for g in grads])
+    optrs = None if out is None else pointers(*[o.data_ptr() for o in outs])
+    numel = (ctypes.c_uint64 * n)(*[g.numel() for g in grads])
+    kinds = bytes([KINDS[g.dtype] for g in grads])
+    with _On(stream, dev) as s:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        ws, nb = _workspace(0, 0, n, dev)
+        _check(load().hkv_clip_grad_norm(n, ptrs, optrs, numel, kinds, max_norm, norm.data_ptr(), ws.data_ptr(), nb,
+                                         s))
+    return norm
