@@ -137,7 +137,8 @@ struct Running {
 #pragma unroll
     for (int i = 1; i < K; ++i) mx = fmaxf(mx, f[i]);
     if (mx > m) {
-      s *= (double)exp2_fast((m - mx) * c.k_hi);
+      const float t = m - mx;
+      s *= (double)exp2_fast(fmaf(t, c.k_hi, t * c.k_lo));
       m = mx;
     }
     const float base = m == -kInf ? 0.0f : m;
