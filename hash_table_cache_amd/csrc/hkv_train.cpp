@@ -119,8 +119,8 @@ hkv_status check_logits(int* device, uint64_t rows, uint64_t vocab, uint32_t dty
   uint64_t es = 0;
   if (!kind_size(dtype, &es)) return fail(HKV_EINVAL, "dtype %u is none of HKV_F32, HKV_BF16, HKV_F16", dtype);
   if (rows >= (1ull << 31)) return fail(HKV_EINVAL, "rows = %llu, the limit is 2^31 - 1", (unsigned long long)rows);
-  if (vocab == 0 || vocab >= (1ull << 31))
-    return fail(HKV_EINVAL, "vocab = %llu is outside 1 .. 2^31 - 1", (unsigned long long)vocab);
+  if (vocab == 0 || vocab >= (1ull << 29))
+    return fail(HKV_EINVAL, "vocab = %llu is outside 1 .. 2^29 - 1", (unsigned long long)vocab);
   if (!(temperature > 0.0f) || !std::isfinite(temperature) || !std::isfinite(1.0f / temperature))
     return fail(HKV_EINVAL, "temperature = %g has to be a positive finite number", (double)temperature);
   if (stride < vocab || stride > (1ull << 40))

@@ -25,6 +25,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kInf = __builtin_inff();
+constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -126,69 +127,100 @@ Scale make_scale(double tau) {
   return c;
 }
 
+// Vectors of a row, read once and not needed again by this kernel. A row's
+// bytes are counted in 32 bits: a scalar base and one register of offset.
+template <typename T>
+__device__ __forceinline__ u32x4 load_vec(const T* row, uint32_t v) {
+  return __builtin_nontemporal_load(
+      reinterpret_cast<const typename Io<T>::V*>(reinterpret_cast<const char*>(row) + v * 16u));
+}
+
+template <typename T>
+__device__ __forceinline__ void store_vec(T* row, uint32_t v, u32x4 x) {
+  __builtin_nontemporal_store(x, reinterpret_cast<typename Io<T>::V*>(reinterpret_cast<char*>(row) + v * 16u));
+}
+
 // Running maximum and sum of the elements a thread has seen.
 struct Running {
   float m = -kInf;
   double s = 0.0;
 
-  template <int K>
+  // N elements: their maximum first, so that the sum is rescaled at most once
+  // for all of them and, after the first few, by hardly any wave.
+  template <int N>
   __device__ __forceinline__ void add(const float* f, const Scale& c) {
     float mx = f[0];
 #pragma unroll
-    for (int i = 1; i < K; ++i) mx = fmaxf(mx, f[i]);
-    if (mx > m) {
-      const float t = m - mx;
+    for (int i = 1; i < N; ++i) mx = fmaxf(mx, f[i]);
+    if (__any(mx > m)) {
+      const float top = fmaxf(m, mx);
+      const float t = top == -kInf ? 0.0f : m - top;
       s *= (double)exp2_fast(fmaf(t, c.k_hi, t * c.k_lo));
-      m = mx;
+      m = top;
     }
     const float base = m == -kInf ? 0.0f : m;
-    float e[K];
+    float e[N];
 #pragma unroll
-    for (int i = 0; i < K; ++i) {
+    for (int i = 0; i < N; ++i) {
       const float t = f[i] - base;
       e[i] = exp2_fast(fmaf(t, c.k_hi, t * c.k_lo));
     }
 #pragma unroll
-    for (int w = K / 2; w > 0; w /= 2)
+    for (int w = N / 2; w > 0; w /= 2)
 #pragma unroll
       for (int i = 0; i < w; ++i) e[i] += e[i + w];
     s += (double)e[0];
   }
 };
 
+// The threads that serve a row: a part of a wave, a wave, or a workgroup.
 template <int NT>
-struct Shared {
-  float m[NT / 64];
-  double s[NT / 64];
+struct Team {
+  static constexpr int kBlock = NT < 256 ? 256 : NT;  // threads of the workgroup
+  static constexpr int kRows = kBlock / NT;           // rows it works on at a time
+  static constexpr int kWaves = NT > 64 ? NT / 64 : 1;
+  struct Shared {
+    float m[kWaves];
+    double s[kWaves];
+    float got[4];
+  };
+  static __device__ __forceinline__ uint32_t thread() { return threadIdx.x % NT; }
+  // This team's row; the same in every lane where a wave has one row, and then
+  // told to the compiler, which keeps addresses in scalar registers.
+  static __device__ __forceinline__ uint32_t row(uint32_t first) {
+    const uint32_t r = first + blockIdx.x * kRows + threadIdx.x / NT;
+    return NT >= 64 ? __builtin_amdgcn_readfirstlane(r) : r;
+  }
 };
 
-__device__ __forceinline__ double shfl_xor(double v, int mask) { return __shfl_xor(v, mask); }
-
-// Joins the threads' running values; every thread gets the workgroup's.
+// Joins the threads' running values; every thread of the team gets them all.
 template <int NT>
-__device__ __forceinline__ void join(Running& r, const Scale& c, Shared<NT>& sh) {
-  float m = r.m;
+__device__ __forceinline__ void join(Running& r, const Scale& c, typename Team<NT>::Shared& sh) {
+  constexpr int W = NT < 64 ? NT : 64;
+  float top = r.m;
 #pragma unroll
-  for (int w = 32; w > 0; w /= 2) m = fmaxf(m, __shfl_xor(m, w));
+  for (int w = W / 2; w > 0; w /= 2) top = fmaxf(top, __shfl_xor(top, w));
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  __syncthreads();  // the last use of `sh` is over
-  if (lane == 0) sh.m[wave] = m;
-  __syncthreads();
-  float top = -kInf;
+  if (NT > 64) {
+    if (lane == 0) sh.m[wave] = top;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NT / 64; ++w) top = fmaxf(top, sh.m[w]);
+    for (int w = 0; w < Team<NT>::kWaves; ++w) top = fmaxf(top, sh.m[w]);
+  }
   const float base = top == -kInf ? 0.0f : top;
   const float t = r.m - base;
   double s = r.s * (double)exp2_fast(fmaf(t, c.k_hi, t * c.k_lo));
 #pragma unroll
-  for (int w = 32; w > 0; w /= 2) s += shfl_xor(s, w);
-  if (lane == 0) sh.s[wave] = s;
-  __syncthreads();
-  double all = 0.0;
+  for (int w = W / 2; w > 0; w /= 2) s += __shfl_xor(s, w);
+  if (NT > 64) {
+    if (lane == 0) sh.s[wave] = s;
+    __syncthreads();
+    s = 0.0;
 #pragma unroll
-  for (int w = 0; w < NT / 64; ++w) all += sh.s[w];
+    for (int w = 0; w < Team<NT>::kWaves; ++w) s += sh.s[w];
+  }
   r.m = top;
-  r.s = all;
+  r.s = s;
 }
 
 struct RowEnd {
@@ -228,59 +260,89 @@ __device__ RowEnd nan_row() {
   return RowEnd{q, q, RowState{q, (float)q, (float)q, (float)q, 1}};
 }
 
-// Running values of one row, the label left out.
-template <typename T, int NT>
-__device__ __forceinline__ Running read_row(const T* row, uint32_t vocab, uint32_t y, const Scale& c) {
+// Adds N vectors of a row, of which vector `at` holds the label in this thread
+// (N or more: none does). The label's own element stays out.
+template <typename T, int N>
+__device__ __forceinline__ void add_vecs(Running& r, const u32x4* raw, uint32_t at, uint32_t y, const Scale& c) {
   constexpr int K = Io<T>::K;
-  const uint32_t nv = vocab / K, yv = y / K;
-  Running r;
-  for (uint32_t v = threadIdx.x; v < nv; v += NT) {
-    float f[K];
-    Io<T>::unpack(*reinterpret_cast<const typename Io<T>::V*>(row + (uint64_t)v * K), f);
-    if (v == yv) {
+  float f[N * K];
 #pragma unroll
-      for (int i = 0; i < K; ++i)
-        if (i == (int)(y % K)) f[i] = -kInf;
-    }
-    r.add<K>(f, c);
+  for (int i = 0; i < N; ++i) Io<T>::unpack(raw[i], f + i * K);
+  if (__any(at < N)) {
+#pragma unroll
+    for (int i = 0; i < N * K; ++i)
+      if (at == i / K && y % K == i % K) f[i] = -kInf;
   }
-  const uint32_t i = nv * K + threadIdx.x;
-  if (i < vocab && i != y) {
-    const float f = (float)row[i];
-    r.add<1>(&f, c);
-  }
-  return r;
+  r.add<N * K>(f, c);
 }
 
-// The row of the gradient: coef = g / (tau * total); at the label g * rest / tau.
-template <typename T, int NT>
-__device__ __forceinline__ void write_row(const T* row, T* out, uint32_t vocab, uint32_t y, float top, float k,
-                                          float coef, float at_label) {
+// A vector of -inf, where a row has no more.
+template <typename T>
+__device__ __forceinline__ u32x4 no_vec() {
+  float f[Io<T>::K];
+#pragma unroll
+  for (int i = 0; i < Io<T>::K; ++i) f[i] = -kInf;
+  return Io<T>::pack(f);
+}
+
+// The elements after a row's last vector, fewer than one vector.
+template <typename T>
+__device__ __forceinline__ void add_tail(Running& r, const T* row, uint32_t vocab, uint32_t y, uint32_t tid,
+                                         const Scale& c) {
+  const uint32_t i = vocab / Io<T>::K * Io<T>::K + tid;
+  float f = -kInf;
+  if (i < vocab && i != y) f = (float)row[i];
+  r.add<1>(&f, c);
+}
+
+// One vector of the gradient: -coef * 2^((x - top) k).
+template <typename T>
+__device__ __forceinline__ u32x4 grad_vec(u32x4 raw, float top, float k, float coef) {
   constexpr int K = Io<T>::K;
-  const uint32_t nv = vocab / K, yv = y / K;
-  for (uint32_t v = threadIdx.x; v < nv; v += NT) {
-    float f[K];
-    Io<T>::unpack(*reinterpret_cast<const typename Io<T>::V*>(row + (uint64_t)v * K), f);
+  float f[K];
+  Io<T>::unpack(raw, f);
 #pragma unroll
-    for (int i = 0; i < K; ++i) f[i] = -coef * exp2_fast((f[i] - top) * k);
-    if (v == yv) {
+  for (int i = 0; i < K; ++i) f[i] = -coef * exp2_fast((f[i] - top) * k);
+  return Io<T>::pack(f);
+}
+
+template <typename T>
+__device__ __forceinline__ void grad_tail(const T* row, T* out, uint32_t vocab, uint32_t tid, float top, float k,
+                                          float coef) {
+  const uint32_t i = vocab / Io<T>::K * Io<T>::K + tid;
+  if (i < vocab) out[i] = (T)(-coef * exp2_fast(((float)row[i] - top) * k));
+}
+
+// The gradient at the label, by the thread that wrote its neighbours before.
+template <typename T, int NT>
+__device__ __forceinline__ void grad_label(T* out, uint32_t vocab, uint32_t y, uint32_t tid, float at_label) {
+  constexpr uint32_t K = Io<T>::K;
+  const uint32_t last = vocab / K * K;
+  if (tid == (y < last ? y / K % NT : y - last)) out[y] = (T)at_label;
+}
+
+// The vectors from `first` of a row's gradient, the row read again. (In place,
+// every vector is read by the thread that writes it.)
+template <typename T, int NT, int U>
+__device__ __forceinline__ void grad_vecs(const T* row, T* out, uint32_t first, uint32_t nv, uint32_t tid, float top,
+                                          float k, float coef) {
+  uint32_t v = first + tid;
+  for (; v + (U - 1) * NT < nv; v += U * NT) {
+    u32x4 raw[U];
 #pragma unroll
-      for (int i = 0; i < K; ++i)
-        if (i == (int)(y % K)) f[i] = at_label;
-    }
-    *reinterpret_cast<typename Io<T>::V*>(out + (uint64_t)v * K) = Io<T>::pack(f);
+    for (int u = 0; u < U; ++u) raw[u] = load_vec(row, v + u * NT);
+#pragma unroll
+    for (int u = 0; u < U; ++u) store_vec(out, v + u * NT, grad_vec<T>(raw[u], top, k, coef));
   }
-  const uint32_t i = nv * K + threadIdx.x;
-  if (i < vocab) out[i] = (T)(i == y ? at_label : -coef * exp2_fast(((float)row[i] - top) * k));
+  for (; v < nv; v += NT) store_vec(out, v, grad_vec<T>(load_vec(row, v), top, k, coef));
 }
 
 template <typename T, int NT>
-__device__ __forceinline__ void zero_row(T* out, uint32_t vocab) {
+__device__ __forceinline__ void zero_row(T* out, uint32_t vocab, uint32_t tid) {
   constexpr int K = Io<T>::K;
   const uint32_t nv = vocab / K;
-  for (uint32_t v = threadIdx.x; v < nv; v += NT)
-    *reinterpret_cast<typename Io<T>::V*>(out + (uint64_t)v * K) = u32x4{0, 0, 0, 0};
-  const uint32_t i = nv * K + threadIdx.x;
+  for (uint32_t v = tid; v < nv; v += NT) store_vec(out, v, u32x4{0, 0, 0, 0});
+  const uint32_t i = nv * K + tid;
   if (i < vocab) out[i] = (T)0.0f;
 }
 
@@ -289,22 +351,27 @@ struct PolicyRow {
   float loss, kl, g;
 };
 
-__device__ PolicyRow policy_row(const Policy& p, uint32_t t, double logp) {
-  const double r = exp(logp - (double)p.old_logp[t]), a = p.advantages[t];
+// What it takes beside the logits, loaded before them.
+struct PolicyIn {
+  float old_logp, advantage, weight, ref;
+};
+
+__device__ PolicyRow policy_row(const Policy& p, const PolicyIn& in, double logp) {
+  const double r = exp(logp - (double)in.old_logp), a = in.advantage;
   const double free = r * a, bound = fmin(fmax(r, p.low), p.high) * a;
   double loss = -(free <= bound ? free : bound);
   double g = free <= bound ? -free : 0.0;
   if (!(free == free)) loss = g = free;
   double kl = 0.0;
   if (p.ref) {
-    const double d = (double)p.ref[t] - logp, e = expm1(d);
+    const double d = (double)in.ref - logp, e = expm1(d);
     kl = e - d;
     if (p.kl_coef != 0.0) {
       loss += p.kl_coef * kl;
       g -= p.kl_coef * e;
     }
   }
-  return PolicyRow{(float)loss, (float)kl, (float)(g * (double)p.weights[t] * p.grad_scale)};
+  return PolicyRow{(float)loss, (float)kl, (float)(g * (double)in.weight * p.grad_scale)};
 }
 
 enum Mode { kLogp, kPairs, kPolicy };
@@ -317,76 +384,136 @@ struct RowsArgs {
   RowState* states;  // kPairs
   float* g;          // kPairs: the rows' coefficients, cleared here
   Policy p;          // kPolicy
+  uint32_t first;    // row of the first team
 };
 
-// One workgroup a row: statistics, and for the policy loss, whose coefficient
-// needs its own row alone, the gradient in the same kernel.
-template <typename T, int NT, Mode MODE>
-__global__ __launch_bounds__(NT) void rows_kernel(const RowsArgs a) {
-  __shared__ Shared<NT> sh;
-  __shared__ float got[4];
-  for (uint32_t t = blockIdx.x; t < a.l.rows; t += gridDim.x) {
-    const T* row = static_cast<const T*>(a.l.x) + (uint64_t)t * a.l.x_stride;
-    const int64_t y = a.l.labels[t];
-    RowEnd e;
-    if (y < 0) {
-      e.logp = e.lse = 0.0;
-      e.state = RowState{0.0, 0.0f, 1.0f, 0.0f, 0};
-    } else if (y >= (int64_t)a.l.vocab) {
-      e = nan_row();
+// Statistics of rows, by a team of NT threads each, and for the policy loss,
+// whose coefficient needs its own row alone, the gradient in the same kernel:
+// the first NV vectors of every thread stay in registers from the one to the
+// other, so that a row of up to 16 * NT * NV bytes is read once. Without a
+// gradient the same registers hold what is in flight.
+template <typename T, int NT, int NV, Mode MODE>
+__global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a) {
+  using Tm = Team<NT>;
+  constexpr int K = Io<T>::K;
+  constexpr int U = NV > 8 ? 2 : 4;  // vectors summed at a time
+  __shared__ typename Tm::Shared sh;
+  const uint32_t tid = Tm::thread(), vocab = a.l.vocab, nv = vocab / K;
+  const uint32_t t = Tm::row(a.first);
+  if (t >= a.l.rows) return;  // a whole team
+  const T* row = static_cast<const T*>(a.l.x) + (uint64_t)t * a.l.x_stride;
+  const int64_t y64 = a.l.labels[t];
+  const uint32_t y = y64 < 0 || y64 >= (int64_t)vocab ? 0u : (uint32_t)y64;
+  PolicyIn in{};
+  if (MODE == kPolicy && tid == 0) {
+    in.old_logp = a.p.old_logp[t];
+    in.advantage = a.p.advantages[t];
+    in.weight = a.p.weights[t];
+    if (a.p.ref) in.ref = a.p.ref[t];
+  }
+  RowEnd e;
+  u32x4 kept[NV];
+  if (y64 < 0) {
+    e.logp = e.lse = 0.0;
+    e.state = RowState{0.0, 0.0f, 1.0f, 0.0f, 0};
+  } else if (y64 >= (int64_t)vocab) {
+    e = nan_row();
+  } else {
+    const float xy = (float)row[y];
+    Running r;
+    // chunks of NT * NV vectors, the first last: it is the one kept
+    const uint32_t chunks = nv ? (nv - 1) / (NT * NV) + 1 : 0;
+    for (uint32_t ch = chunks; ch-- > 0;) {
+      const uint32_t v0 = ch * (NT * NV) + tid;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        kept[i] = no_vec<T>();
+        if (v0 + i * NT < nv) kept[i] = load_vec(row, v0 + i * NT);
+      }
+      const uint32_t at = y / K >= v0 && (y / K - v0) % NT == 0 ? (y / K - v0) / NT : ~0u;
+#pragma unroll
+      for (int i = 0; i < NV; i += U)
+        if (ch * (NT * NV) + i * NT < nv) add_vecs<T, U>(r, kept + i, at - i, y, a.c);
+    }
+    if (nv * K < vocab) add_tail<T>(r, row, vocab, y, tid, a.c);
+    join<NT>(r, a.c, sh);
+    if (tid == 0) e = finish_row(r.m, r.s, xy, a.c.inv_tau);
+  }
+  PolicyRow p{0.0f, 0.0f, 0.0f};
+  if (tid == 0) {
+    a.logp[t] = (float)e.logp;
+    if (MODE == kLogp && a.lse) a.lse[t] = (float)e.lse;
+    if (MODE == kPairs) {
+      a.states[t] = e.state;
+      a.g[t] = 0.0f;
+    }
+    if (MODE == kPolicy) {
+      if (e.state.counts) p = policy_row(a.p, in, e.logp);
+      a.p.token_loss[t] = p.loss;
+      a.p.kl[t] = p.kl;
+    }
+  }
+  if (MODE == kPolicy && a.l.dx) {
+    float g = p.g, top = e.state.top;
+    float coef = (float)(g * a.c.inv_tau / e.state.total), at_label = (float)(g * a.c.inv_tau * e.state.rest);
+    if (NT > 64) {
+      if (tid == 0) {
+        sh.got[0] = g;
+        sh.got[1] = top;
+        sh.got[2] = coef;
+        sh.got[3] = at_label;
+      }
+      __syncthreads();
+      g = sh.got[0];
+      top = sh.got[1];
+      coef = sh.got[2];
+      at_label = sh.got[3];
     } else {
-      Running r = read_row<T, NT>(row, a.l.vocab, (uint32_t)y, a.c);
-      join<NT>(r, a.c, sh);
-      if (threadIdx.x == 0) e = finish_row(r.m, r.s, (float)row[y], a.c.inv_tau);
+      g = __shfl(g, 0, NT);
+      top = __shfl(top, 0, NT);
+      coef = __shfl(coef, 0, NT);
+      at_label = __shfl(at_label, 0, NT);
     }
-    if (threadIdx.x == 0) {
-      a.logp[t] = (float)e.logp;
-      if (MODE == kLogp && a.lse) a.lse[t] = (float)e.lse;
-      if (MODE == kPairs) {
-        a.states[t] = e.state;
-        a.g[t] = 0.0f;
+    T* out = static_cast<T*>(a.l.dx) + (uint64_t)t * a.l.dx_stride;
+    if (g == 0.0f) {
+      zero_row<T, NT>(out, vocab, tid);
+    } else {
+      if (y64 >= (int64_t)vocab) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) kept[i] = u32x4{0, 0, 0, 0};  // NaN comes from the coefficient
       }
-      if (MODE == kPolicy) {
-        PolicyRow p{0.0f, 0.0f, 0.0f};
-        if (e.state.counts) p = policy_row(a.p, t, e.logp);
-        a.p.token_loss[t] = p.loss;
-        a.p.kl[t] = p.kl;
-        got[0] = p.g;
-        got[1] = e.state.top;
-        got[2] = (float)(p.g * a.c.inv_tau / e.state.total);
-        got[3] = (float)(p.g * a.c.inv_tau * e.state.rest);
-      }
-    }
-    if (MODE == kPolicy && a.l.dx) {
-      __syncthreads();
-      const float g = got[0], top = got[1], coef = got[2], at_label = got[3];
-      T* out = static_cast<T*>(a.l.dx) + (uint64_t)t * a.l.dx_stride;
-      if (g == 0.0f)
-        zero_row<T, NT>(out, a.l.vocab);
-      else
-        write_row<T, NT>(row, out, a.l.vocab, y >= (int64_t)a.l.vocab ? 0u : (uint32_t)y, top, a.c.k_hi, coef,
-                         at_label);
-      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (tid + i * NT < nv) store_vec(out, tid + i * NT, grad_vec<T>(kept[i], top, a.c.k_hi, coef));
+      if (nv > NT * NV) grad_vecs<T, NT, 4>(row, out, NT * NV, nv, tid, top, a.c.k_hi, coef);
+      grad_tail<T>(row, out, vocab, tid, top, a.c.k_hi, coef);
+      grad_label<T, NT>(out, vocab, y, tid, at_label);
     }
   }
 }
 
 // The gradient of rows whose coefficients and statistics are known.
 template <typename T, int NT>
-__global__ __launch_bounds__(NT) void grad_kernel(const Logits l, const Scale c, const RowState* states,
-                                                  const float* g_rows) {
-  for (uint32_t t = blockIdx.x; t < l.rows; t += gridDim.x) {
-    const T* row = static_cast<const T*>(l.x) + (uint64_t)t * l.x_stride;
-    T* out = static_cast<T*>(l.dx) + (uint64_t)t * l.dx_stride;
-    const RowState st = states[t];
-    const float g = st.counts ? g_rows[t] : 0.0f;
-    const int64_t y = l.labels[t];
-    if (g == 0.0f)
-      zero_row<T, NT>(out, l.vocab);
-    else
-      write_row<T, NT>(row, out, l.vocab, y >= (int64_t)l.vocab ? 0u : (uint32_t)y, st.top, c.k_hi,
-                       (float)(g * c.inv_tau / st.total), (float)(g * c.inv_tau * st.rest));
+__global__ __launch_bounds__(Team<NT>::kBlock) void grad_kernel(const Logits l, const Scale c, const RowState* states,
+                                                                const float* g_rows, uint32_t first) {
+  using Tm = Team<NT>;
+  const uint32_t tid = Tm::thread();
+  const uint32_t t = Tm::row(first);
+  if (t >= l.rows) return;
+  const T* row = static_cast<const T*>(l.x) + (uint64_t)t * l.x_stride;
+  T* out = static_cast<T*>(l.dx) + (uint64_t)t * l.dx_stride;
+  const RowState st = states[t];
+  const float g = st.counts ? g_rows[t] : 0.0f;
+  const int64_t y64 = l.labels[t];
+  if (g == 0.0f) {
+    zero_row<T, NT>(out, l.vocab, tid);
+    return;
   }
+  const uint32_t y = y64 >= (int64_t)l.vocab ? 0u : (uint32_t)y64;
+  const float coef = (float)(g * c.inv_tau / st.total);
+  grad_vecs<T, NT, 4>(row, out, 0, l.vocab / Io<T>::K, tid, st.top, c.k_hi, coef);
+  grad_tail<T>(row, out, l.vocab, tid, st.top, c.k_hi, coef);
+  grad_label<T, NT>(out, l.vocab, y, tid, (float)(g * c.inv_tau * st.rest));
 }
 
 // x / tau - lse: the first step cancels what the two have in common exactly,
@@ -405,58 +532,58 @@ __device__ __forceinline__ double rest_of_label(float x, const Scale& c, float l
   return -expm1(z > 1.0 ? 1.0 : z);
 }
 
+template <typename T>
+__device__ __forceinline__ u32x4 backward_vec(u32x4 raw, const Scale& c, float lse, float g) {
+  constexpr int K = Io<T>::K;
+  float f[K];
+  Io<T>::unpack(raw, f);
+#pragma unroll
+  for (int i = 0; i < K; ++i) f[i] = -g * exp2_fast(exponent(f[i], c, lse) * kLog2e);
+  return Io<T>::pack(f);
+}
+
 // The gradient of the log-probabilities from the normalisers.
 template <typename T, int NT>
-__global__ __launch_bounds__(NT) void backward_kernel(const Logits l, const Scale c, const float* lse,
-                                                      const float* g_rows) {
-  constexpr int K = Io<T>::K;
-  constexpr float kLog2e = 1.4426950408889634f;
-  for (uint32_t t = blockIdx.x; t < l.rows; t += gridDim.x) {
-    const T* row = static_cast<const T*>(l.x) + (uint64_t)t * l.x_stride;
-    T* out = static_cast<T*>(l.dx) + (uint64_t)t * l.dx_stride;
-    const int64_t yy = l.labels[t];
-    const float z = lse[t];
-    float g = (float)(g_rows[t] * c.inv_tau);
-    if (yy < 0 || z == -kInf || g == 0.0f) {
-      zero_row<T, NT>(out, l.vocab);
-      continue;
-    }
-    if (yy >= (int64_t)l.vocab) g = __builtin_nanf("");
-    const uint32_t y = yy >= (int64_t)l.vocab ? 0u : (uint32_t)yy;
-    const uint32_t nv = l.vocab / K;
-    for (uint32_t v = threadIdx.x; v < nv; v += NT) {
-      float f[K];
-      Io<T>::unpack(*reinterpret_cast<const typename Io<T>::V*>(row + (uint64_t)v * K), f);
-      float fy = 0.0f;
-      if (v == y / K) {
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-          if (i == (int)(y % K)) fy = f[i];
-      }
-#pragma unroll
-      for (int i = 0; i < K; ++i) f[i] = -g * exp2_fast(exponent(f[i], c, z) * kLog2e);
-      if (v == y / K) {
-        const float at_label = (float)((double)g * rest_of_label(fy, c, z));
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-          if (i == (int)(y % K)) f[i] = at_label;
-      }
-      *reinterpret_cast<typename Io<T>::V*>(out + (uint64_t)v * K) = Io<T>::pack(f);
-    }
-    const uint32_t i = nv * K + threadIdx.x;
-    if (i < l.vocab) {
-      const float f = (float)row[i];
-      out[i] = (T)(i == y ? (float)((double)g * rest_of_label(f, c, z))
-                          : -g * exp2_fast(exponent(f, c, z) * kLog2e));
-    }
+__global__ __launch_bounds__(Team<NT>::kBlock) void backward_kernel(const Logits l, const Scale c, const float* lse,
+                                                                    const float* g_rows, uint32_t first) {
+  using Tm = Team<NT>;
+  constexpr int K = Io<T>::K, U = 4;
+  const uint32_t tid = Tm::thread(), nv = l.vocab / K;
+  const uint32_t t = Tm::row(first);
+  if (t >= l.rows) return;
+  const T* row = static_cast<const T*>(l.x) + (uint64_t)t * l.x_stride;
+  T* out = static_cast<T*>(l.dx) + (uint64_t)t * l.dx_stride;
+  const int64_t y64 = l.labels[t];
+  const float z = lse[t];
+  float g = (float)(g_rows[t] * c.inv_tau);
+  if (y64 < 0 || z == -kInf || g == 0.0f) {
+    zero_row<T, NT>(out, l.vocab, tid);
+    return;
   }
+  if (y64 >= (int64_t)l.vocab) g = __builtin_nanf("");
+  const uint32_t y = y64 >= (int64_t)l.vocab ? 0u : (uint32_t)y64;
+  // the label's thread, the only one that writes its place, reads it first
+  const uint32_t owner = y < nv * K ? y / K % NT : y - nv * K;
+  const float fy = tid == owner ? (float)row[y] : 0.0f;
+  uint32_t v = tid;
+  for (; v + (U - 1) * NT < nv; v += U * NT) {
+    u32x4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) raw[u] = load_vec(row, v + u * NT);
+#pragma unroll
+    for (int u = 0; u < U; ++u) store_vec(out, v + u * NT, backward_vec<T>(raw[u], c, z, g));
+  }
+  for (; v < nv; v += NT) store_vec(out, v, backward_vec<T>(load_vec(row, v), c, z, g));
+  const uint32_t i = nv * K + tid;
+  if (i < l.vocab) out[i] = (T)(-g * exp2_fast(exponent((float)row[i], c, z) * kLog2e));
+  if (tid == owner) out[y] = (T)(float)((double)g * rest_of_label(fy, c, z));
 }
 
 // Sum over a workgroup, in a fixed order; every thread gets it.
 template <int NT>
 __device__ __forceinline__ double block_sum(double v, double* sh) {
 #pragma unroll
-  for (int w = 32; w > 0; w /= 2) v += shfl_xor(v, w);
+  for (int w = 32; w > 0; w /= 2) v += __shfl_xor(v, w);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
   __syncthreads();
@@ -524,21 +651,60 @@ template <int NT>
 __global__ __launch_bounds__(NT) void weighted_sum_kernel(const float* loss, const float* weights, uint32_t n,
                                                           float* out) {
   __shared__ double sh[NT / 64];
+  constexpr uint32_t U = 8;
   double sum = 0.0;
-  for (uint32_t i = threadIdx.x; i < n; i += NT) {
-    const float l = loss[i];
-    if (l != 0.0f) sum += (double)l * (double)weights[i];  // rows left out have 0, whatever their weight
+  for (uint64_t i = threadIdx.x; i < n; i += U * NT) {
+    float l[U], w[U];
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u) {
+      l[u] = w[u] = 0.0f;
+      if (i + u * NT < n) {
+        l[u] = loss[i + u * NT];
+        w[u] = weights[i + u * NT];
+      }
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u)
+      if (l[u] != 0.0f) sum += (double)l[u] * (double)w[u];  // rows left out have 0, whatever their weight
   }
   sum = block_sum<NT>(sum, sh);
   if (threadIdx.x == 0) *out = (float)sum;
 }
 
-uint32_t row_grid(uint32_t rows) { return std::min<uint32_t>(rows, 1u << 20); }
+// One team a row: launch(first row, workgroups) for slices of rows that keep a
+// launch's threads under 2^32.
+template <int NT, typename F>
+hipError_t for_rows(uint32_t rows, F&& launch) {
+  constexpr uint32_t kSlice = (1u << 21) * Team<NT>::kRows;
+  for (uint64_t first = 0; first < rows; first += kSlice) {
+    const uint32_t n = (uint32_t)std::min<uint64_t>(rows - first, kSlice);
+    launch((uint32_t)first, (n - 1) / Team<NT>::kRows + 1);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
 
+template <typename T, int NT, int NV, Mode MODE>
+hipError_t rows_n(RowsArgs a, hipStream_t s) {
+  return for_rows<NT>(a.l.rows, [&](uint32_t first, uint32_t grid) {
+    a.first = first;
+    rows_kernel<T, NT, NV, MODE><<<grid, Team<NT>::kBlock, 0, s>>>(a);
+  });
+}
+
+// The smallest team whose registers hold a row.
 template <typename T, Mode MODE>
 hipError_t rows_t(const RowsArgs& a, hipStream_t s) {
-  rows_kernel<T, 512, MODE><<<row_grid(a.l.rows), 512, 0, s>>>(a);
-  return hipGetLastError();
+  const uint32_t nv = a.l.vocab / Io<T>::K;
+  if (nv <= 16 * 4) return rows_n<T, 16, 4, MODE>(a, s);
+  if (nv <= 64 * 4) return rows_n<T, 64, 4, MODE>(a, s);
+  if (nv <= 256 * 4) return rows_n<T, 256, 4, MODE>(a, s);
+  if constexpr (MODE == kPolicy) {
+    if (nv > 512 * 16) return rows_n<T, 1024, 16, MODE>(a, s);
+    if (nv > 512 * 8) return rows_n<T, 512, 16, MODE>(a, s);
+  }
+  return rows_n<T, 512, 8, MODE>(a, s);
 }
 
 template <Mode MODE>
@@ -546,6 +712,36 @@ hipError_t rows_d(const RowsArgs& a, hipStream_t s) {
   if (a.l.kind == kF32) return rows_t<float, MODE>(a, s);
   if (a.l.kind == kBF16) return rows_t<__bf16, MODE>(a, s);
   return rows_t<_Float16, MODE>(a, s);
+}
+
+template <typename T, int NT>
+hipError_t grad_n(const Logits& l, const Scale& c, const RowState* states, const float* g, hipStream_t s) {
+  return for_rows<NT>(l.rows, [&](uint32_t first, uint32_t grid) {
+    grad_kernel<T, NT><<<grid, Team<NT>::kBlock, 0, s>>>(l, c, states, g, first);
+  });
+}
+
+template <typename T>
+hipError_t grad_t(const Logits& l, const Scale& c, const RowState* states, const float* g, hipStream_t s) {
+  const uint32_t nv = l.vocab / Io<T>::K;
+  if (nv <= 16 * 4) return grad_n<T, 16>(l, c, states, g, s);
+  if (nv <= 64 * 4) return grad_n<T, 64>(l, c, states, g, s);
+  return grad_n<T, 512>(l, c, states, g, s);
+}
+
+template <typename T, int NT>
+hipError_t backward_n(const Logits& l, const Scale& c, const float* lse, const float* g, hipStream_t s) {
+  return for_rows<NT>(l.rows, [&](uint32_t first, uint32_t grid) {
+    backward_kernel<T, NT><<<grid, Team<NT>::kBlock, 0, s>>>(l, c, lse, g, first);
+  });
+}
+
+template <typename T>
+hipError_t backward_t(const Logits& l, const Scale& c, const float* lse, const float* g, hipStream_t s) {
+  const uint32_t nv = l.vocab / Io<T>::K;
+  if (nv <= 16 * 4) return backward_n<T, 16>(l, c, lse, g, s);
+  if (nv <= 64 * 4) return backward_n<T, 64>(l, c, lse, g, s);
+  return backward_n<T, 512>(l, c, lse, g, s);
 }
 
 // Gradient clipping.
@@ -676,14 +872,9 @@ hipError_t launch_logprobs(const Logits& l, float* logp, float* lse, void*, hipS
 
 hipError_t launch_backward(const Logits& l, const float* lse, const float* g, hipStream_t s) {
   const Scale c = make_scale(l.tau);
-  const uint32_t grid = row_grid(l.rows);
-  if (l.kind == kF32)
-    backward_kernel<float, 512><<<grid, 512, 0, s>>>(l, c, lse, g);
-  else if (l.kind == kBF16)
-    backward_kernel<__bf16, 512><<<grid, 512, 0, s>>>(l, c, lse, g);
-  else
-    backward_kernel<_Float16, 512><<<grid, 512, 0, s>>>(l, c, lse, g);
-  return hipGetLastError();
+  if (l.kind == kF32) return backward_t<float>(l, c, lse, g, s);
+  if (l.kind == kBF16) return backward_t<__bf16>(l, c, lse, g, s);
+  return backward_t<_Float16>(l, c, lse, g, s);
 }
 
 hipError_t launch_preference(const Logits& l, const Pairs& p, void* ws, hipStream_t s) {
@@ -711,14 +902,9 @@ hipError_t launch_preference(const Logits& l, const Pairs& p, void* ws, hipStrea
   mean_kernel<256><<<1, 256, 0, s>>>(losses, p.pairs, p.loss);
   if ((e = hipGetLastError()) != hipSuccess || !l.rows || !l.dx) return e;
   const Scale c = make_scale(l.tau);
-  const uint32_t grid = row_grid(l.rows);
-  if (l.kind == kF32)
-    grad_kernel<float, 512><<<grid, 512, 0, s>>>(l, c, states, g);
-  else if (l.kind == kBF16)
-    grad_kernel<__bf16, 512><<<grid, 512, 0, s>>>(l, c, states, g);
-  else
-    grad_kernel<_Float16, 512><<<grid, 512, 0, s>>>(l, c, states, g);
-  return hipGetLastError();
+  if (l.kind == kF32) return grad_t<float>(l, c, states, g, s);
+  if (l.kind == kBF16) return grad_t<__bf16>(l, c, states, g, s);
+  return grad_t<_Float16>(l, c, states, g, s);
 }
 
 hipError_t launch_policy(const Logits& l, const Policy& p, void*, hipStream_t s) {

@@ -38,7 +38,7 @@
  *     alignment of the element type). A gradient may overwrite its logits (same
  *     address, same stride); no other overlap is allowed.
  *   - Results are deterministic: no sum depends on the order of execution.
- * Limits: rows < 2^31, vocab < 2^31, pairs < 2^30, tensors < 2^20.
+ * Limits: rows < 2^31, vocab < 2^29, pairs < 2^30, tensors < 2^20.
  */
 #ifndef HKV_TRAIN_H_
 #define HKV_TRAIN_H_
