@@ -62,37 +62,67 @@ class DeviceGuard {
   hipError_t err_;
 };
 
-// Checks that [p, p + bytes) is memory that GPU `*device` can access (device
-// memory of that GPU, or pinned host memory), inside one allocation. With
-// *device < 0 the buffer decides the GPU and has to be device memory.
-hkv_status check_buffer(int* device, const void* p, uint64_t bytes, const char* what) {
-  if (!p) return fail(HKV_EINVAL, "%s is NULL", what);
-  hipPointerAttribute_t a;
-  std::memset(&a, 0, sizeof(a));
-  hipError_t e = hipPointerGetAttributes(&a, p);
-  if (e != hipSuccess || a.type == hipMemoryTypeUnregistered) {
-    (void)hipGetLastError();
-    return fail(HKV_EINVAL, "%s (%p) is not device-accessible memory (pageable host memory?)", what, p);
+#define HKV_TRY(expr)                    \
+  do {                                   \
+    const hkv_status st_ = (expr);       \
+    if (st_ != HKV_OK) return st_;       \
+  } while (0)
+
+// The buffers of one call. The first one checked decides the GPU and has to be
+// device memory; the others have to be memory that this GPU can access (its
+// own, or pinned host memory). Each lies inside one allocation. Allocations are
+// remembered while the call lasts: a call's small tensors mostly share one, and
+// a lookup costs 0.1 us.
+class Buffers {
+ public:
+  int device() const { return device_; }
+
+  hkv_status check(const void* p, uint64_t bytes, const char* what, int64_t index = -1) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    for (const Range& r : known_)
+      if (a >= r.begin && a < r.end && bytes <= r.end - a) return HKV_OK;
+    char name[48];
+    if (index >= 0) {
+      std::snprintf(name, sizeof(name), "%s[%lld]", what, (long long)index);
+      what = name;
+    }
+    if (!p) return fail(HKV_EINVAL, "%s is NULL", what);
+    hipPointerAttribute_t attr;
+    std::memset(&attr, 0, sizeof(attr));
+    hipError_t e = hipPointerGetAttributes(&attr, p);
+    if (e != hipSuccess || attr.type == hipMemoryTypeUnregistered) {
+      (void)hipGetLastError();
+      return fail(HKV_EINVAL, "%s (%p) is not device-accessible memory (pageable host memory?)", what, p);
+    }
+    if (device_ < 0) {
+      if (attr.type != hipMemoryTypeDevice) return fail(HKV_EINVAL, "%s (%p) is not device memory", what, p);
+      device_ = attr.device;
+    } else if (attr.type == hipMemoryTypeDevice && attr.device != device_) {
+      return fail(HKV_EINVAL, "%s lives on device %d, the call runs on device %d", what, attr.device, device_);
+    }
+    hipDeviceptr_t base = nullptr;
+    size_t size = 0;
+    e = hipMemGetAddressRange(&base, &size, const_cast<void*>(p));
+    if (e == hipSuccess && base && size) {
+      const uint64_t off = a - reinterpret_cast<uintptr_t>(base);
+      if (off > size || bytes > size - off)
+        return fail(HKV_EINVAL, "%s holds %llu bytes past %p, call needs %llu", what,
+                    static_cast<unsigned long long>(size - off), p, static_cast<unsigned long long>(bytes));
+      known_[next_++ % 4] = Range{a - off, a - off + size};
+    } else {
+      (void)hipGetLastError();
+    }
+    return HKV_OK;
   }
-  if (*device < 0) {
-    if (a.type != hipMemoryTypeDevice) return fail(HKV_EINVAL, "%s (%p) is not device memory", what, p);
-    *device = a.device;
-  } else if (a.type == hipMemoryTypeDevice && a.device != *device) {
-    return fail(HKV_EINVAL, "%s lives on device %d, the call runs on device %d", what, a.device, *device);
-  }
-  hipDeviceptr_t base = nullptr;
-  size_t size = 0;
-  e = hipMemGetAddressRange(&base, &size, const_cast<void*>(p));
-  if (e == hipSuccess && base && size) {
-    const uint64_t off = reinterpret_cast<uintptr_t>(p) - reinterpret_cast<uintptr_t>(base);
-    if (off > size || bytes > size - off)
-      return fail(HKV_EINVAL, "%s holds %llu bytes past %p, call needs %llu", what,
-                  static_cast<unsigned long long>(size - off), p, static_cast<unsigned long long>(bytes));
-  } else {
-    (void)hipGetLastError();
-  }
-  return HKV_OK;
-}
+
+ private:
+  struct Range {
+    uintptr_t begin = 0, end = 0;
+  };
+  int device_ = -1;
+  Range known_[4];
+  unsigned next_ = 0;
+};
 
 bool kind_size(uint32_t kind, uint64_t* size) {
   if (kind > hkvt::kF16) return false;
@@ -105,15 +135,9 @@ bool overlap(const void* a, uint64_t an, const void* b, uint64_t bn) {
   return an && bn && x < y + bn && y < x + an;
 }
 
-#define HKV_TRY(expr)                    \
-  do {                                   \
-    const hkv_status st_ = (expr);       \
-    if (st_ != HKV_OK) return st_;       \
-  } while (0)
-
 // The arguments that every operator on logits has. A call without rows looks
 // at no array but its scalar outputs.
-hkv_status check_logits(int* device, uint64_t rows, uint64_t vocab, uint32_t dtype, const void* logits,
+hkv_status check_logits(Buffers& buffers, uint64_t rows, uint64_t vocab, uint32_t dtype, const void* logits,
                         uint64_t stride, const int64_t* labels, float temperature, const void* grad,
                         uint64_t grad_stride, hkvt::Logits* out) {
   uint64_t es = 0;
@@ -133,12 +157,12 @@ hkv_status check_logits(int* device, uint64_t rows, uint64_t vocab, uint32_t dty
                       dtype, temperature};
   if (rows == 0) return HKV_OK;
   const uint64_t bytes = ((rows - 1) * stride + vocab) * es;
-  HKV_TRY(check_buffer(device, logits, bytes, "logits"));
+  HKV_TRY(buffers.check(logits, bytes, "logits"));
   if (reinterpret_cast<uintptr_t>(logits) % es) return fail(HKV_EINVAL, "logits is not aligned to its type");
-  HKV_TRY(check_buffer(device, labels, rows * 8, "labels"));
+  HKV_TRY(buffers.check(labels, rows * 8, "labels"));
   if (grad) {
     const uint64_t gbytes = ((rows - 1) * grad_stride + vocab) * es;
-    HKV_TRY(check_buffer(device, grad, gbytes, "grad_out"));
+    HKV_TRY(buffers.check(grad, gbytes, "grad_out"));
     if (reinterpret_cast<uintptr_t>(grad) % es) return fail(HKV_EINVAL, "grad_out is not aligned to its type");
     if (!(grad == logits && grad_stride == stride) && overlap(grad, gbytes, logits, bytes))
       return fail(HKV_EINVAL, "grad_out overlaps logits without being the same array");
@@ -146,11 +170,11 @@ hkv_status check_logits(int* device, uint64_t rows, uint64_t vocab, uint32_t dty
   return HKV_OK;
 }
 
-hkv_status check_workspace(int* device, const void* ws, uint64_t bytes, uint64_t need) {
+hkv_status check_workspace(Buffers& buffers, const void* ws, uint64_t bytes, uint64_t need) {
   if (bytes < need)
     return fail(HKV_EINVAL, "workspace_bytes = %llu, the call needs %llu", (unsigned long long)bytes,
                 (unsigned long long)need);
-  HKV_TRY(check_buffer(device, ws, need, "workspace"));
+  HKV_TRY(buffers.check(ws, need, "workspace"));
   if (reinterpret_cast<uintptr_t>(ws) & 15) return fail(HKV_EINVAL, "workspace is not 16-byte aligned");
   return HKV_OK;
 }
@@ -167,13 +191,13 @@ HKV_API hkv_status hkv_token_logprobs(uint64_t rows, uint64_t vocab, uint32_t dt
                                       hipStream_t stream) {
   return guarded([&]() -> hkv_status {
     hkvt::Logits l;
-    int device = -1;
-    HKV_TRY(check_logits(&device, rows, vocab, dtype, logits, logits_stride, labels, temperature, nullptr, 0, &l));
+    Buffers buffers;
+    HKV_TRY(check_logits(buffers, rows, vocab, dtype, logits, logits_stride, labels, temperature, nullptr, 0, &l));
     if (rows == 0) return HKV_OK;
-    HKV_TRY(check_buffer(&device, logp_out, rows * 4, "logp_out"));
-    if (lse_out) HKV_TRY(check_buffer(&device, lse_out, rows * 4, "lse_out"));
-    HKV_TRY(check_workspace(&device, workspace, workspace_bytes, hkvt::workspace_bytes(rows, 0, 0)));
-    DeviceGuard dg(device);
+    HKV_TRY(buffers.check(logp_out, rows * 4, "logp_out"));
+    if (lse_out) HKV_TRY(buffers.check(lse_out, rows * 4, "lse_out"));
+    HKV_TRY(check_workspace(buffers, workspace, workspace_bytes, hkvt::workspace_bytes(rows, 0, 0)));
+    DeviceGuard dg(buffers.device());
     if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
     const hipError_t e = hkvt::launch_logprobs(l, logp_out, lse_out, workspace, stream);
     return e == hipSuccess ? HKV_OK : fail_hip(e, "hkv_token_logprobs launch");
@@ -186,14 +210,14 @@ HKV_API hkv_status hkv_token_logprobs_backward(uint64_t rows, uint64_t vocab, ui
                                                uint64_t grad_stride, hipStream_t stream) {
   return guarded([&]() -> hkv_status {
     hkvt::Logits l;
-    int device = -1;
+    Buffers buffers;
     if (!grad_out && rows) return fail(HKV_EINVAL, "grad_out is NULL");
-    HKV_TRY(check_logits(&device, rows, vocab, dtype, logits, logits_stride, labels, temperature, grad_out,
+    HKV_TRY(check_logits(buffers, rows, vocab, dtype, logits, logits_stride, labels, temperature, grad_out,
                          grad_stride, &l));
     if (rows == 0) return HKV_OK;
-    HKV_TRY(check_buffer(&device, lse, rows * 4, "lse"));
-    HKV_TRY(check_buffer(&device, grad_logp, rows * 4, "grad_logp"));
-    DeviceGuard dg(device);
+    HKV_TRY(buffers.check(lse, rows * 4, "lse"));
+    HKV_TRY(buffers.check(grad_logp, rows * 4, "grad_logp"));
+    DeviceGuard dg(buffers.device());
     if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
     const hipError_t e = hkvt::launch_backward(l, lse, grad_logp, stream);
     return e == hipSuccess ? HKV_OK : fail_hip(e, "hkv_token_logprobs_backward launch");
@@ -208,26 +232,26 @@ HKV_API hkv_status hkv_preference_loss(uint64_t rows, uint64_t vocab, uint32_t d
                                        void* workspace, uint64_t workspace_bytes, hipStream_t stream) {
   return guarded([&]() -> hkv_status {
     hkvt::Logits l;
-    int device = -1;
+    Buffers buffers;
     if (pairs >= (1ull << 30)) return fail(HKV_EINVAL, "pairs = %llu, the limit is 2^30 - 1", (unsigned long long)pairs);
     if (!std::isfinite(beta)) return fail(HKV_EINVAL, "beta = %g is not finite", (double)beta);
     if (!(label_smoothing >= 0.0f && label_smoothing <= 1.0f))
       return fail(HKV_EINVAL, "label_smoothing = %g is outside 0 .. 1", (double)label_smoothing);
     if (!std::isfinite(grad_scale)) return fail(HKV_EINVAL, "grad_scale = %g is not finite", (double)grad_scale);
-    HKV_TRY(check_logits(&device, rows, vocab, dtype, logits, logits_stride, labels, temperature, grad_out,
+    HKV_TRY(check_logits(buffers, rows, vocab, dtype, logits, logits_stride, labels, temperature, grad_out,
                          grad_stride, &l));
-    HKV_TRY(check_buffer(&device, loss_out, 4, "loss_out"));
+    HKV_TRY(buffers.check(loss_out, 4, "loss_out"));
     if (rows) {
-      if (ref_logp) HKV_TRY(check_buffer(&device, ref_logp, rows * 4, "ref_logp"));
-      HKV_TRY(check_buffer(&device, logp_out, rows * 4, "logp_out"));
+      if (ref_logp) HKV_TRY(buffers.check(ref_logp, rows * 4, "ref_logp"));
+      HKV_TRY(buffers.check(logp_out, rows * 4, "logp_out"));
     }
     if (pairs) {
-      HKV_TRY(check_buffer(&device, cu_seqlens, (2 * pairs + 1) * 8, "cu_seqlens"));
-      HKV_TRY(check_buffer(&device, losses_out, pairs * 4, "losses_out"));
-      HKV_TRY(check_buffer(&device, rewards_out, pairs * 8, "rewards_out"));
+      HKV_TRY(buffers.check(cu_seqlens, (2 * pairs + 1) * 8, "cu_seqlens"));
+      HKV_TRY(buffers.check(losses_out, pairs * 4, "losses_out"));
+      HKV_TRY(buffers.check(rewards_out, pairs * 8, "rewards_out"));
     }
-    HKV_TRY(check_workspace(&device, workspace, workspace_bytes, hkvt::workspace_bytes(rows, pairs, 0)));
-    DeviceGuard dg(device);
+    HKV_TRY(check_workspace(buffers, workspace, workspace_bytes, hkvt::workspace_bytes(rows, pairs, 0)));
+    DeviceGuard dg(buffers.device());
     if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
     const hkvt::Pairs p{(uint32_t)pairs, cu_seqlens, ref_logp, beta, label_smoothing, grad_scale, loss_out, losses_out,
                         rewards_out, logp_out};
@@ -245,7 +269,7 @@ HKV_API hkv_status hkv_policy_loss(uint64_t rows, uint64_t vocab, uint32_t dtype
                                    uint64_t workspace_bytes, hipStream_t stream) {
   return guarded([&]() -> hkv_status {
     hkvt::Logits l;
-    int device = -1;
+    Buffers buffers;
     if (!(clip_low >= 0.0f && clip_low <= 1.0f))
       return fail(HKV_EINVAL, "clip_low = %g is outside 0 .. 1", (double)clip_low);
     if (!(clip_high >= 0.0f) || !std::isfinite(clip_high))
@@ -253,20 +277,20 @@ HKV_API hkv_status hkv_policy_loss(uint64_t rows, uint64_t vocab, uint32_t dtype
     if (!std::isfinite(kl_coef)) return fail(HKV_EINVAL, "kl_coef = %g is not finite", (double)kl_coef);
     if (kl_coef != 0.0f && !ref_logp && rows) return fail(HKV_EINVAL, "kl_coef = %g without ref_logp", (double)kl_coef);
     if (!std::isfinite(grad_scale)) return fail(HKV_EINVAL, "grad_scale = %g is not finite", (double)grad_scale);
-    HKV_TRY(check_logits(&device, rows, vocab, dtype, logits, logits_stride, labels, temperature, grad_out,
+    HKV_TRY(check_logits(buffers, rows, vocab, dtype, logits, logits_stride, labels, temperature, grad_out,
                          grad_stride, &l));
-    HKV_TRY(check_buffer(&device, loss_out, 4, "loss_out"));
+    HKV_TRY(buffers.check(loss_out, 4, "loss_out"));
     if (rows) {
-      HKV_TRY(check_buffer(&device, old_logp, rows * 4, "old_logp"));
-      HKV_TRY(check_buffer(&device, advantages, rows * 4, "advantages"));
-      HKV_TRY(check_buffer(&device, weights, rows * 4, "weights"));
-      if (ref_logp) HKV_TRY(check_buffer(&device, ref_logp, rows * 4, "ref_logp"));
-      HKV_TRY(check_buffer(&device, token_loss_out, rows * 4, "token_loss_out"));
-      HKV_TRY(check_buffer(&device, kl_out, rows * 4, "kl_out"));
-      HKV_TRY(check_buffer(&device, logp_out, rows * 4, "logp_out"));
+      HKV_TRY(buffers.check(old_logp, rows * 4, "old_logp"));
+      HKV_TRY(buffers.check(advantages, rows * 4, "advantages"));
+      HKV_TRY(buffers.check(weights, rows * 4, "weights"));
+      if (ref_logp) HKV_TRY(buffers.check(ref_logp, rows * 4, "ref_logp"));
+      HKV_TRY(buffers.check(token_loss_out, rows * 4, "token_loss_out"));
+      HKV_TRY(buffers.check(kl_out, rows * 4, "kl_out"));
+      HKV_TRY(buffers.check(logp_out, rows * 4, "logp_out"));
     }
-    HKV_TRY(check_workspace(&device, workspace, workspace_bytes, hkvt::workspace_bytes(rows, 0, 0)));
-    DeviceGuard dg(device);
+    HKV_TRY(check_workspace(buffers, workspace, workspace_bytes, hkvt::workspace_bytes(rows, 0, 0)));
+    DeviceGuard dg(buffers.device());
     if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
     const hkvt::Policy p{old_logp, advantages, weights,    ref_logp, 1.0 - (double)clip_low, 1.0 + (double)clip_high,
                          kl_coef,  grad_scale, loss_out, token_loss_out, kl_out, logp_out};
@@ -283,7 +307,7 @@ HKV_API hkv_status hkv_clip_grad_norm(uint64_t tensors, void* const* grads, void
       return fail(HKV_EINVAL, "tensors = %llu, the limit is 2^20 - 1", (unsigned long long)tensors);
     if (tensors && (!grads || !numel || !dtypes)) return fail(HKV_EINVAL, "grads, numel or dtypes is NULL");
     if (!(max_norm >= 0.0f)) return fail(HKV_EINVAL, "max_norm = %g has to be >= 0", (double)max_norm);
-    int device = -1;
+    Buffers buffers;
     // the tensors that hold anything, and the ranges they read and write
     std::vector<hkvt::Tensor> list;
     list.reserve(tensors);
@@ -292,7 +316,7 @@ HKV_API hkv_status hkv_clip_grad_norm(uint64_t tensors, void* const* grads, void
       bool written;
     };
     std::vector<Range> ranges;
-    ranges.reserve(2 * tensors);
+    ranges.reserve(outs ? 2 * tensors : tensors);
     uint64_t chunks = 0;
     for (uint64_t i = 0; i < tensors; ++i) {
       uint64_t es = 0;
@@ -301,23 +325,19 @@ HKV_API hkv_status hkv_clip_grad_norm(uint64_t tensors, void* const* grads, void
       if (n == 0) continue;
       if (n > (1ull << 48)) return fail(HKV_EINVAL, "tensor %llu: numel", (unsigned long long)i);
       void* out = outs ? outs[i] : grads[i];
-      char name[48];
-      std::snprintf(name, sizeof(name), "grads[%llu]", (unsigned long long)i);
-      HKV_TRY(check_buffer(&device, grads[i], n * es, name));
-      if (out != grads[i]) {
-        std::snprintf(name, sizeof(name), "outs[%llu]", (unsigned long long)i);
-        HKV_TRY(check_buffer(&device, out, n * es, name));
-      }
+      HKV_TRY(buffers.check(grads[i], n * es, "grads", (int64_t)i));
+      if (out != grads[i]) HKV_TRY(buffers.check(out, n * es, "outs", (int64_t)i));
       if (reinterpret_cast<uintptr_t>(grads[i]) % es || reinterpret_cast<uintptr_t>(out) % es)
         return fail(HKV_EINVAL, "tensor %llu is not aligned to its type", (unsigned long long)i);
       list.push_back({grads[i], out, n, dtypes[i], 0});
-      chunks += (n + hkvt::kChunkElems - 1) / hkvt::kChunkElems;
+      chunks += (n - 1) / hkvt::chunk_elems(dtypes[i]) + 1;
       const uintptr_t a = reinterpret_cast<uintptr_t>(grads[i]), b = reinterpret_cast<uintptr_t>(out);
       ranges.push_back({a, a + n * es, out == grads[i]});
       if (out != grads[i]) ranges.push_back({b, b + n * es, true});
     }
-    if (chunks >= (1ull << 31)) return fail(HKV_EINVAL, "more than 2^31 chunks of %llu elements", (unsigned long long)hkvt::kChunkElems);
-    std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.begin < b.begin; });
+    if (chunks >= (1ull << 31)) return fail(HKV_EINVAL, "more than 2^31 chunks of %llu bytes", (unsigned long long)hkvt::kChunkBytes);
+    const auto before = [](const Range& a, const Range& b) { return a.begin < b.begin; };
+    if (!std::is_sorted(ranges.begin(), ranges.end(), before)) std::sort(ranges.begin(), ranges.end(), before);
     // a range that begins before an earlier one ends, of which one is written
     uintptr_t end = 0, written_end = 0;
     for (const Range& r : ranges) {
@@ -326,9 +346,9 @@ HKV_API hkv_status hkv_clip_grad_norm(uint64_t tensors, void* const* grads, void
       end = std::max(end, r.end);
       if (r.written) written_end = std::max(written_end, r.end);
     }
-    HKV_TRY(check_buffer(&device, norm_out, 4, "norm_out"));
-    HKV_TRY(check_workspace(&device, workspace, workspace_bytes, hkvt::workspace_bytes(0, 0, tensors)));
-    DeviceGuard dg(device);
+    HKV_TRY(buffers.check(norm_out, 4, "norm_out"));
+    HKV_TRY(check_workspace(buffers, workspace, workspace_bytes, hkvt::workspace_bytes(0, 0, tensors)));
+    DeviceGuard dg(buffers.device());
     if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
     const hipError_t e = hkvt::launch_clip(list.data(), (uint32_t)list.size(), max_norm, norm_out, workspace, stream);
     return e == hipSuccess ? HKV_OK : fail_hip(e, "hkv_clip_grad_norm launch");

@@ -78,8 +78,9 @@ hipError_t launch_backward(const Logits& l, const float* lse, const float* g, hi
 hipError_t launch_preference(const Logits& l, const Pairs& p, void* ws, hipStream_t s);
 hipError_t launch_policy(const Logits& l, const Policy& p, void* ws, hipStream_t s);
 
-// Elements of a tensor that one chunk covers.
-constexpr uint64_t kChunkElems = 16384;
+// A chunk of a tensor's elements.
+constexpr uint64_t kChunkBytes = 32768;
+__host__ __device__ constexpr uint64_t chunk_elems(uint32_t kind) { return kChunkBytes / (kind == kF32 ? 4 : 2); }
 // `first` is filled in here.
 hipError_t launch_clip(Tensor* t, uint32_t tensors, double max_norm, float* norm, void* ws, hipStream_t s);
 

@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "hkv_train_internal.h"
 
@@ -26,6 +27,7 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kInf = __builtin_inff();
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint32_t kFewRows = 256;  // as many as there are compute units
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -138,34 +140,60 @@ template <typename T, int NT>
 struct Cut {
   static constexpr uint32_t K = Io<T>::K;
   uint32_t head, nv, vocab;
-  __device__ __forceinline__ Cut(const T* lines, uint32_t vocab_) : vocab(vocab_) {
+  uint32_t begin, end;  // the vectors of this part of the row
+  __device__ __forceinline__ Cut(const T* lines, uint32_t vocab_, uint32_t part = 0, uint32_t parts = 1)
+      : vocab(vocab_) {
     const uint32_t off = (uint32_t)(0 - reinterpret_cast<uintptr_t>(lines)) & 127u;
     head = NT < 64 ? 0 : min(off / (uint32_t)sizeof(T), vocab);
     nv = (vocab - head) / K;
+    begin = (uint32_t)((uint64_t)nv * part / parts);
+    end = (uint32_t)((uint64_t)nv * (part + 1) / parts);
   }
-  __device__ __forceinline__ uint32_t singles() const { return vocab - nv * K; }
+  // Single elements: the first part's.
+  __device__ __forceinline__ uint32_t singles() const { return begin == 0 ? vocab - nv * K : 0; }
   // Element of the j-th single one.
   __device__ __forceinline__ uint32_t single(uint32_t j) const { return j < head ? j : j + nv * K; }
   // Vector that holds element y; nv or more: y is a single one.
   __device__ __forceinline__ uint32_t vec_of(uint32_t y) const { return y < head ? ~0u : (y - head) / K; }
-  // Thread that reads and writes element y.
+  // Thread that reads and writes element y; none of this part where it lies in another.
   __device__ __forceinline__ uint32_t owner(uint32_t y) const {
     const uint32_t v = vec_of(y);
-    return (v < nv ? v : y < head ? y : y - nv * K) % NT;
+    if (v < nv) return v >= begin && v < end ? (v - begin) % NT : ~0u;
+    return begin == 0 ? (y < head ? y : y - nv * K) % NT : ~0u;
   }
 };
 
-// Vectors of a row, read once and not needed again by this kernel. A row's
-// bytes are counted in 32 bits: a scalar base and one register of offset.
-template <typename T>
+// Vectors of a row. A row's bytes are counted in 32 bits: a scalar base and one
+// register of offset. What is read for the last time and what is written go
+// past the caches (2047 x 50021 fp32: 49 us against 55 us); kKeep is for what a
+// later kernel reads again: the preference loss's second reading finds up to
+// 256 MB of it in the memory-side cache (8192 x 32768 bf16: 168 us against
+// 198 us with no such reading, 191 us with both).
+template <typename T, bool kKeep = false>
 __device__ __forceinline__ u32x4 load_vec(const T* row, uint32_t v) {
-  return __builtin_nontemporal_load(
-      reinterpret_cast<const typename Io<T>::V*>(reinterpret_cast<const char*>(row) + v * 16u));
+  const auto* p = reinterpret_cast<const typename Io<T>::V*>(reinterpret_cast<const char*>(row) + v * 16u);
+  if (kKeep) return *p;
+  return __builtin_nontemporal_load(p);
 }
 
 template <typename T>
 __device__ __forceinline__ void store_vec(T* row, uint32_t v, u32x4 x) {
   __builtin_nontemporal_store(x, reinterpret_cast<typename Io<T>::V*>(reinterpret_cast<char*>(row) + v * 16u));
+}
+
+// Calls use(vector, its number) for a thread's share of vectors first .. nv of
+// a row, U of which are on the way at a time, in the last round too.
+template <typename T, int NT, int U, bool kKeep = false, typename F>
+__device__ __forceinline__ void for_vecs(const T* row, uint32_t first, uint32_t nv, uint32_t tid, F&& use) {
+  for (uint32_t v = first + tid; v < nv; v += U * NT) {
+    u32x4 raw[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v + u * NT < nv) raw[u] = load_vec<T, kKeep>(row, v + u * NT);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (v + u * NT < nv) use(raw[u], v + u * NT);
+  }
 }
 
 // Running maximum and sum of the elements a thread has seen.
@@ -200,6 +228,20 @@ struct Running {
     s += (double)e[0];
   }
 };
+
+// Sum over a workgroup, in a fixed order; every thread gets it.
+template <int NT>
+__device__ __forceinline__ double block_sum(double v, double* sh) {
+#pragma unroll
+  for (int w = 32; w > 0; w /= 2) v += __shfl_xor(v, w);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double all = 0.0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) all += sh[w];
+  return all;
+}
 
 // The threads that serve a row: a part of a wave, a wave, or a workgroup.
 template <int NT>
@@ -349,20 +391,13 @@ __device__ __forceinline__ void grad_singles(const T* row, T* out, const Cut<T, 
 template <typename T, int NT, int U>
 __device__ __forceinline__ void grad_vecs(const T* row, T* out, uint32_t first, uint32_t nv, uint32_t tid, float top,
                                           float k, float coef) {
-  uint32_t v = first + tid;
-  for (; v + (U - 1) * NT < nv; v += U * NT) {
-    u32x4 raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = load_vec(row, v + u * NT);
-#pragma unroll
-    for (int u = 0; u < U; ++u) store_vec(out, v + u * NT, grad_vec<T>(raw[u], top, k, coef));
-  }
-  for (; v < nv; v += NT) store_vec(out, v, grad_vec<T>(load_vec(row, v), top, k, coef));
+  for_vecs<T, NT, U>(row, first, nv, tid,
+                     [&](u32x4 raw, uint32_t v) { store_vec(out, v, grad_vec<T>(raw, top, k, coef)); });
 }
 
 template <typename T, int NT>
 __device__ __forceinline__ void zero_row(T* out, const Cut<T, NT>& cut, uint32_t tid) {
-  for (uint32_t v = tid; v < cut.nv; v += NT) store_vec(out + cut.head, v, u32x4{0, 0, 0, 0});
+  for (uint32_t v = cut.begin + tid; v < cut.end; v += NT) store_vec(out + cut.head, v, u32x4{0, 0, 0, 0});
   for (uint32_t j = tid; j < cut.singles(); j += NT) out[cut.single(j)] = (T)0.0f;
 }
 
@@ -454,7 +489,7 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         kept[i] = no_vec<T>();
-        if (v0 + i * NT < nv) kept[i] = load_vec(vecs, v0 + i * NT);
+        if (v0 + i * NT < nv) kept[i] = load_vec<T, MODE == kPairs>(vecs, v0 + i * NT);
       }
       const uint32_t at = yv >= v0 && (yv - v0) % NT == 0 ? (yv - v0) / NT : ~0u;
 #pragma unroll
@@ -517,31 +552,6 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a
   }
 }
 
-// The gradient of rows whose coefficients and statistics are known.
-template <typename T, int NT>
-__global__ __launch_bounds__(Team<NT>::kBlock) void grad_kernel(const Logits l, const Scale c, const RowState* states,
-                                                                const float* g_rows, uint32_t first) {
-  using Tm = Team<NT>;
-  const uint32_t tid = Tm::thread();
-  const uint32_t t = Tm::row(first);
-  if (t >= l.rows) return;
-  const T* row = static_cast<const T*>(l.x) + (uint64_t)t * l.x_stride;
-  T* out = static_cast<T*>(l.dx) + (uint64_t)t * l.dx_stride;
-  const Cut<T, NT> cut(out, l.vocab);
-  const RowState st = states[t];
-  const float g = st.counts ? g_rows[t] : 0.0f;
-  const int64_t y64 = l.labels[t];
-  if (g == 0.0f) {
-    zero_row<T, NT>(out, cut, tid);
-    return;
-  }
-  const uint32_t y = y64 >= (int64_t)l.vocab ? 0u : (uint32_t)y64;
-  const float coef = (float)(g * c.inv_tau / st.total);
-  grad_vecs<T, NT, 4>(row + cut.head, out + cut.head, 0, cut.nv, tid, st.top, c.k_hi, coef);
-  grad_singles<T, NT>(row, out, cut, tid, st.top, c.k_hi, coef);
-  if (tid == cut.owner(y)) out[y] = (T)(float)(g * c.inv_tau * st.rest);
-}
-
 // x / tau - lse: the first step cancels what the two have in common exactly,
 // the second adds what 1 / tau lacks in a float. The exponent is at most the
 // rounding of lse; where logits are so large (a row of the type's lowest value)
@@ -573,14 +583,12 @@ template <typename T, int NT>
 __global__ __launch_bounds__(Team<NT>::kBlock) void backward_kernel(const Logits l, const Scale c, const float* lse,
                                                                     const float* g_rows, uint32_t first) {
   using Tm = Team<NT>;
-  constexpr int U = 4;
   const uint32_t tid = Tm::thread();
   const uint32_t t = Tm::row(first);
   if (t >= l.rows) return;
   const T* row = static_cast<const T*>(l.x) + (uint64_t)t * l.x_stride;
   T* out = static_cast<T*>(l.dx) + (uint64_t)t * l.dx_stride;
-  const Cut<T, NT> cut(out, l.vocab);
-  const uint32_t nv = cut.nv;
+  const Cut<T, NT> cut(out, l.vocab, blockIdx.y, gridDim.y);
   const int64_t y64 = l.labels[t];
   const float z = lse[t];
   float g = (float)(g_rows[t] * c.inv_tau);
@@ -593,35 +601,14 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void backward_kernel(const Logits
   // the label's thread, the only one that writes its place, reads it first
   const uint32_t owner = cut.owner(y);
   const float fy = tid == owner ? (float)row[y] : 0.0f;
-  const T* vecs = row + cut.head;
-  uint32_t v = tid;
-  for (; v + (U - 1) * NT < nv; v += U * NT) {
-    u32x4 raw[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) raw[u] = load_vec(vecs, v + u * NT);
-#pragma unroll
-    for (int u = 0; u < U; ++u) store_vec(out + cut.head, v + u * NT, backward_vec<T>(raw[u], c, z, g));
-  }
-  for (; v < nv; v += NT) store_vec(out + cut.head, v, backward_vec<T>(load_vec(vecs, v), c, z, g));
+  for_vecs<T, NT, 4>(row + cut.head, cut.begin, cut.end, tid, [&](u32x4 raw, uint32_t v) {
+    store_vec(out + cut.head, v, backward_vec<T>(raw, c, z, g));
+  });
   for (uint32_t j = tid; j < cut.singles(); j += NT) {
     const uint32_t i = cut.single(j);
     out[i] = (T)(-g * exp2_fast(exponent((float)row[i], c, z) * kLog2e));
   }
   if (tid == owner) out[y] = (T)(float)((double)g * rest_of_label(fy, c, z));
-}
-
-// Sum over a workgroup, in a fixed order; every thread gets it.
-template <int NT>
-__device__ __forceinline__ double block_sum(double v, double* sh) {
-#pragma unroll
-  for (int w = 32; w > 0; w /= 2) v += __shfl_xor(v, w);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double all = 0.0;
-#pragma unroll
-  for (int w = 0; w < NT / 64; ++w) all += sh[w];
-  return all;
 }
 
 __device__ __forceinline__ void sequence(const Pairs& p, uint64_t s, uint32_t rows, uint32_t* begin, uint32_t* end) {
@@ -631,51 +618,98 @@ __device__ __forceinline__ void sequence(const Pairs& p, uint64_t s, uint32_t ro
   *end = (uint32_t)(b < a ? a : b);
 }
 
-// One workgroup a pair: the rewards of its sequences, its loss, its rows' coefficients.
+// One workgroup a pair: the rewards of its sequences, its loss, its rows'
+// coefficients. Half of the threads take each sequence.
 template <int NT>
 __global__ __launch_bounds__(NT) void pairs_kernel(const Pairs p, uint32_t rows, const RowState* states, float* g,
                                                    double* losses) {
   __shared__ double sh[NT / 64];
+  const uint32_t side = threadIdx.x / (NT / 2), tid = threadIdx.x % (NT / 2);
   for (uint32_t i = blockIdx.x; i < p.pairs; i += gridDim.x) {
-    double reward[2];
-    uint32_t begin[2], end[2];
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      sequence(p, 2ull * i + s, rows, &begin[s], &end[s]);
-      double sum = 0.0;
-      for (uint32_t t = begin[s] + threadIdx.x; t < end[s]; t += NT)
-        if (states[t].counts) sum += states[t].logp - (p.ref ? (double)p.ref[t] : 0.0);
-      reward[s] = p.beta * block_sum<NT>(sum, sh);
+    uint32_t begin, end;
+    sequence(p, 2ull * i + side, rows, &begin, &end);
+    double sum = 0.0;
+    for (uint32_t t = begin + tid; t < end; t += NT / 2) {
+      const RowState st = states[t];
+      const double ref = p.ref ? (double)p.ref[t] : 0.0;
+      if (st.counts) sum += st.logp - ref;
     }
+#pragma unroll
+    for (int w = 32; w > 0; w /= 2) sum += __shfl_xor(sum, w);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    double reward[2] = {0.0, 0.0};
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) reward[w / (NT / 128)] += sh[w];
+    reward[0] *= p.beta;
+    reward[1] *= p.beta;
     const double m = reward[0] - reward[1];
-    // log(1 + e^-m) and log(1 + e^m), sigma(m)
-    const double tail = log1p(exp(-fabs(m)));
-    const double down = fmax(-m, 0.0) + tail, up = fmax(m, 0.0) + tail;
-    double loss = m == m ? 0.0 : m;
-    if (p.smoothing != 1.0) loss += (1.0 - p.smoothing) * down;
-    if (p.smoothing != 0.0) loss += p.smoothing * up;
-    const double slope = 1.0 / (1.0 + exp(-m)) - 1.0 + p.smoothing;
-    const double c = p.beta * slope / p.pairs * p.grad_scale;
+    // log(1 + e^-m), log(1 + e^m) and sigma(m) from e^-|m|
+    const double e = exp(-fabs(m)), tail = log1p(e);
+    const double sigma = (m >= 0.0 ? 1.0 : e) / (1.0 + e);
+    const double c = p.beta * (m == m ? sigma - 1.0 + p.smoothing : m) / p.pairs * p.grad_scale;
+    for (uint32_t t = begin + tid; t < end; t += NT / 2) g[t] = (float)(side ? -c : c);
     if (threadIdx.x == 0) {
+      const double down = fmax(-m, 0.0) + tail, up = fmax(m, 0.0) + tail;
+      double loss = m == m ? 0.0 : m;
+      if (p.smoothing != 1.0) loss += (1.0 - p.smoothing) * down;
+      if (p.smoothing != 0.0) loss += p.smoothing * up;
       p.rewards[2ull * i] = (float)reward[0];
       p.rewards[2ull * i + 1] = (float)reward[1];
       p.losses[i] = (float)loss;
       losses[i] = loss;
     }
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-      for (uint32_t t = begin[s] + threadIdx.x; t < end[s]; t += NT) g[t] = (float)(s ? -c : c);
   }
 }
 
-// loss = scale * sum of losses, by one workgroup in a fixed order.
+// The mean of the pairs' losses, by one workgroup in a fixed order.
 template <int NT>
-__global__ __launch_bounds__(NT) void mean_kernel(const double* losses, uint32_t n, float* out) {
-  __shared__ double sh[NT / 64];
+__device__ __forceinline__ void mean_loss(const double* losses, uint32_t n, float* out, double* sh) {
   double sum = 0.0;
   for (uint32_t i = threadIdx.x; i < n; i += NT) sum += losses[i];
   sum = block_sum<NT>(sum, sh);
   if (threadIdx.x == 0) *out = n ? (float)(sum / n) : 0.0f;
+}
+
+template <int NT>
+__global__ __launch_bounds__(NT) void mean_kernel(const double* losses, uint32_t n, float* out) {
+  __shared__ double sh[NT / 64];
+  mean_loss<NT>(losses, n, out, sh);
+}
+
+// The gradient of rows whose coefficients and statistics are known. The last
+// workgroup of the launch has no rows: it takes the mean of the losses, which
+// as a kernel of its own cost 5 us.
+template <typename T, int NT>
+__global__ __launch_bounds__(Team<NT>::kBlock) void grad_kernel(const Logits l, const Scale c, const RowState* states,
+                                                                const float* g_rows, const double* losses,
+                                                                uint32_t pairs, float* loss, uint32_t first) {
+  using Tm = Team<NT>;
+  if (loss && blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.y) return;
+    __shared__ double sh[Tm::kBlock / 64];
+    mean_loss<Tm::kBlock>(losses, pairs, loss, sh);
+    return;
+  }
+  const uint32_t tid = Tm::thread();
+  const uint32_t t = Tm::row(first);
+  if (t >= l.rows) return;
+  const T* row = static_cast<const T*>(l.x) + (uint64_t)t * l.x_stride;
+  T* out = static_cast<T*>(l.dx) + (uint64_t)t * l.dx_stride;
+  const Cut<T, NT> cut(out, l.vocab, blockIdx.y, gridDim.y);
+  const RowState st = states[t];
+  const float g = st.counts ? g_rows[t] : 0.0f;
+  const int64_t y64 = l.labels[t];
+  if (g == 0.0f) {
+    zero_row<T, NT>(out, cut, tid);
+    return;
+  }
+  const uint32_t y = y64 >= (int64_t)l.vocab ? 0u : (uint32_t)y64;
+  const float coef = (float)(g * c.inv_tau / st.total);
+  grad_vecs<T, NT, 4>(row + cut.head, out + cut.head, cut.begin, cut.end, tid, st.top, c.k_hi, coef);
+  grad_singles<T, NT>(row, out, cut, tid, st.top, c.k_hi, coef);
+  if (tid == cut.owner(y)) out[y] = (T)(float)(g * c.inv_tau * st.rest);
 }
 
 template <int NT>
@@ -716,6 +750,13 @@ hipError_t for_rows(uint32_t rows, F&& launch) {
   return hipSuccess;
 }
 
+// Parts that a row's gradient is cut into, one workgroup each: where the rows
+// alone leave the chip idle, as long as a part has a few rounds of vectors.
+template <int NT>
+uint32_t row_parts(uint32_t rows, uint32_t nv) {
+  return std::max(1u, std::min(kFewRows / rows, nv / (NT * 2)));
+}
+
 template <typename T, int NT, int NV, Mode MODE>
 hipError_t rows_n(RowsArgs a, hipStream_t s) {
   return for_rows<NT>(a.l.rows, [&](uint32_t first, uint32_t grid) {
@@ -724,7 +765,8 @@ hipError_t rows_n(RowsArgs a, hipStream_t s) {
   });
 }
 
-// The smallest team whose registers hold a row.
+// The smallest team whose registers hold a row, or the largest where there are
+// fewer rows than compute units.
 template <typename T, Mode MODE>
 hipError_t rows_t(const RowsArgs& a, hipStream_t s) {
   const uint32_t nv = a.l.vocab / Io<T>::K;
@@ -732,9 +774,10 @@ hipError_t rows_t(const RowsArgs& a, hipStream_t s) {
   if (nv <= 64 * 4) return rows_n<T, 64, 4, MODE>(a, s);
   if (nv <= 256 * 4) return rows_n<T, 256, 4, MODE>(a, s);
   if constexpr (MODE == kPolicy) {
-    if (nv > 512 * 16) return rows_n<T, 1024, 16, MODE>(a, s);
+    if (nv > 512 * 16 || a.l.rows < kFewRows) return rows_n<T, 1024, 16, MODE>(a, s);
     if (nv > 512 * 8) return rows_n<T, 512, 16, MODE>(a, s);
   }
+  if (MODE != kPolicy && a.l.rows < kFewRows) return rows_n<T, 1024, 8, MODE>(a, s);
   return rows_n<T, 512, 8, MODE>(a, s);
 }
 
@@ -745,25 +788,38 @@ hipError_t rows_d(const RowsArgs& a, hipStream_t s) {
   return rows_t<_Float16, MODE>(a, s);
 }
 
+struct GradArgs {
+  Logits l;
+  Scale c;
+  const RowState* states;
+  const float* g;
+  const double* losses;
+  uint32_t pairs;
+  float* loss;
+};
+
 template <typename T, int NT>
-hipError_t grad_n(const Logits& l, const Scale& c, const RowState* states, const float* g, hipStream_t s) {
-  return for_rows<NT>(l.rows, [&](uint32_t first, uint32_t grid) {
-    grad_kernel<T, NT><<<grid, Team<NT>::kBlock, 0, s>>>(l, c, states, g, first);
+hipError_t grad_n(const GradArgs& a, hipStream_t s) {
+  return for_rows<NT>(a.l.rows, [&](uint32_t first, uint32_t grid) {
+    float* loss = first ? nullptr : a.loss;  // the first slice takes the mean
+    const dim3 blocks(grid + (loss ? 1 : 0), NT > 64 ? row_parts<NT>(a.l.rows, a.l.vocab / Io<T>::K) : 1);
+    grad_kernel<T, NT><<<blocks, Team<NT>::kBlock, 0, s>>>(a.l, a.c, a.states, a.g, a.losses, a.pairs, loss, first);
   });
 }
 
 template <typename T>
-hipError_t grad_t(const Logits& l, const Scale& c, const RowState* states, const float* g, hipStream_t s) {
-  const uint32_t nv = l.vocab / Io<T>::K;
-  if (nv <= 16 * 4) return grad_n<T, 16>(l, c, states, g, s);
-  if (nv <= 64 * 4) return grad_n<T, 64>(l, c, states, g, s);
-  return grad_n<T, 512>(l, c, states, g, s);
+hipError_t grad_t(const GradArgs& a, hipStream_t s) {
+  const uint32_t nv = a.l.vocab / Io<T>::K;
+  if (nv <= 16 * 4) return grad_n<T, 16>(a, s);
+  if (nv <= 64 * 4) return grad_n<T, 64>(a, s);
+  return grad_n<T, 512>(a, s);
 }
 
 template <typename T, int NT>
 hipError_t backward_n(const Logits& l, const Scale& c, const float* lse, const float* g, hipStream_t s) {
   return for_rows<NT>(l.rows, [&](uint32_t first, uint32_t grid) {
-    backward_kernel<T, NT><<<grid, Team<NT>::kBlock, 0, s>>>(l, c, lse, g, first);
+    const dim3 blocks(grid, NT > 64 ? row_parts<NT>(l.rows, l.vocab / Io<T>::K) : 1);
+    backward_kernel<T, NT><<<blocks, Team<NT>::kBlock, 0, s>>>(l, c, lse, g, first);
   });
 }
 
@@ -778,102 +834,176 @@ hipError_t backward_t(const Logits& l, const Scale& c, const float* lse, const f
 // Gradient clipping.
 
 constexpr int kClipThreads = 512;
-constexpr uint32_t kClipBlocks = 1024;
-constexpr int kUpload = 100;  // tensors a launch's arguments carry
+constexpr uint32_t kClipBlocks = 1024;  // partial sums, and workgroups of a launch
+constexpr uint64_t kKeepBytes = 192ull << 20;
+constexpr uint32_t kDirect = 140;       // tensors that a launch's arguments hold (4 KB at most)
+constexpr uint32_t kScaleBlocks = 8192;
 
-struct Upload {
-  Tensor t[kUpload];
+// The list of tensors, in the kernel's arguments where it fits there. A longer
+// one is carried to the workspace by upload_kernel, kDirect at a time: through
+// arguments, not a copy, so that a captured call owns what it needs.
+struct DirectList {
+  uint64_t in[kDirect], out[kDirect], n[kDirect];  // n: the kind in the top byte
+  uint32_t first[kDirect];
+
+  void set(uint32_t i, const Tensor& t) {
+    in[i] = reinterpret_cast<uint64_t>(t.in);
+    out[i] = reinterpret_cast<uint64_t>(t.out);
+    n[i] = t.n | (uint64_t)t.kind << 56;
+    first[i] = t.first;
+  }
+  __device__ __forceinline__ Tensor at(uint32_t i) const {
+    return Tensor{reinterpret_cast<const void*>(in[i]), reinterpret_cast<void*>(out[i]), n[i] & ((1ull << 56) - 1),
+                  (uint32_t)(n[i] >> 56), first[i]};
+  }
 };
 
-__global__ void upload_kernel(const Upload u, Tensor* to, uint32_t n) {
-  if (threadIdx.x < n) to[threadIdx.x] = u.t[threadIdx.x];
+struct StoredList {
+  const Tensor* t;
+};
+
+__global__ void upload_kernel(const DirectList list, Tensor* to, uint32_t n) {
+  if (threadIdx.x < n) to[threadIdx.x] = list.at(threadIdx.x);
 }
 
-// The tensor that holds chunk c.
-__device__ __forceinline__ uint32_t find_tensor(const Tensor* t, uint32_t tensors, uint32_t c) {
-  uint32_t lo = 0, hi = tensors;
+// The last of n tensors whose first chunk is `chunk` or an earlier one.
+template <typename F>
+__device__ __forceinline__ uint32_t find_tensor(uint32_t n, uint32_t chunk, F&& first) {
+  uint32_t lo = 0, hi = n;
   while (hi - lo > 1) {
     const uint32_t mid = (lo + hi) / 2;
-    if (t[mid].first <= c)
+    if (first(mid) <= chunk)
       lo = mid;
     else
       hi = mid;
   }
-  return lo;
+  return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// Squares in 64 bits: those of fp32 and bf16 gradients pass the range of 32.
-template <typename T>
+// Finds the tensor that holds a chunk. A workgroup keeps what the search reads
+// in LDS: the whole list from the arguments, the first chunks of a stored list
+// where they fit.
+template <typename L>
+struct Finder;
+
+template <>
+struct Finder<DirectList> {
+  typedef Tensor Held[kDirect];
+  const Tensor* held;
+  uint32_t tensors;
+  __device__ __forceinline__ Finder(const DirectList& list, uint32_t n, Held& lds) : held(lds), tensors(n) {
+    if (threadIdx.x < n) lds[threadIdx.x] = list.at(threadIdx.x);
+    __syncthreads();
+  }
+  __device__ __forceinline__ Tensor at(uint32_t chunk) const {
+    return held[find_tensor(tensors, chunk, [&](uint32_t i) { return held[i].first; })];
+  }
+};
+
+template <>
+struct Finder<StoredList> {
+  static constexpr uint32_t kHeld = 2048;
+  typedef uint32_t Held[kHeld];
+  const Tensor* list;
+  const uint32_t* held;
+  uint32_t tensors;
+  __device__ __forceinline__ Finder(const StoredList& l, uint32_t n, Held& lds) : list(l.t), held(lds), tensors(n) {
+    if (n <= kHeld)
+      for (uint32_t i = threadIdx.x; i < n; i += kClipThreads) lds[i] = list[i].first;
+    __syncthreads();
+  }
+  __device__ __forceinline__ Tensor at(uint32_t chunk) const {
+    return list[find_tensor(tensors, chunk, [&](uint32_t i) { return tensors <= kHeld ? held[i] : list[i].first; })];
+  }
+};
+
+// Squares are added in 64 bits: those of fp32 and bf16 gradients pass the range
+// of 32 on both sides.
+template <typename T, bool kKeep>
 __device__ __forceinline__ double chunk_squares(const T* p, uint32_t n) {
   constexpr int K = Io<T>::K;
-  double s = 0.0;
-  const uint32_t nv = n / K;
-  for (uint32_t v = threadIdx.x; v < nv; v += kClipThreads) {
+  double s = 0.0, s2 = 0.0;
+  const Cut<T, kClipThreads> cut(p, n);
+  for_vecs<T, kClipThreads, 4, kKeep>(p + cut.head, 0, cut.nv, threadIdx.x, [&](u32x4 raw, uint32_t) {
     float f[K];
-    Io<T>::unpack(*reinterpret_cast<const typename Io<T>::V*>(p + v * K), f);
+    Io<T>::unpack(raw, f);
 #pragma unroll
-    for (int i = 0; i < K; ++i) s += (double)f[i] * (double)f[i];
+    for (int i = 0; i < K; i += 2) {
+      s += (double)f[i] * (double)f[i];
+      s2 += (double)f[i + 1] * (double)f[i + 1];
+    }
+  });
+  if (threadIdx.x < cut.singles()) {
+    const double f = (float)p[cut.single(threadIdx.x)];
+    s += f * f;
   }
-  const uint32_t i = nv * K + threadIdx.x;
-  if (i < n) s += (double)(float)p[i] * (double)(float)p[i];
-  return s;
+  return s + s2;
 }
 
 template <typename T>
 __device__ __forceinline__ void chunk_scale(const T* p, T* q, uint32_t n, float c) {
   constexpr int K = Io<T>::K;
-  const uint32_t nv = n / K;
-  for (uint32_t v = threadIdx.x; v < nv; v += kClipThreads) {
+  const Cut<T, kClipThreads> cut(q, n);
+  for_vecs<T, kClipThreads, 4>(p + cut.head, 0, cut.nv, threadIdx.x, [&](u32x4 raw, uint32_t v) {
     float f[K];
-    Io<T>::unpack(*reinterpret_cast<const typename Io<T>::V*>(p + v * K), f);
+    Io<T>::unpack(raw, f);
 #pragma unroll
     for (int i = 0; i < K; ++i) f[i] *= c;
-    *reinterpret_cast<typename Io<T>::V*>(q + v * K) = Io<T>::pack(f);
+    store_vec(q + cut.head, v, Io<T>::pack(f));
+  });
+  if (threadIdx.x < cut.singles()) {
+    const uint32_t i = cut.single(threadIdx.x);
+    q[i] = (T)((float)p[i] * c);
   }
-  const uint32_t i = nv * K + threadIdx.x;
-  if (i < n) q[i] = (T)((float)p[i] * c);
 }
 
-__global__ __launch_bounds__(kClipThreads) void squares_kernel(const Tensor* t, uint32_t tensors, uint32_t chunks,
-                                                               double* partial) {
+// Chunks from `keep` on are left in the caches: the second pass begins there.
+template <typename L>
+__global__ __launch_bounds__(kClipThreads) void squares_kernel(const L list, uint32_t tensors, uint32_t chunks,
+                                                               uint32_t keep, double* partial) {
   __shared__ double sh[kClipThreads / 64];
+  __shared__ typename Finder<L>::Held held;
+  const Finder<L> find(list, tensors, held);
   double s = 0.0;
   for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const Tensor x = t[find_tensor(t, tensors, c)];
-    const uint64_t at = (uint64_t)(c - x.first) * kChunkElems;
-    const uint32_t n = (uint32_t)min(x.n - at, kChunkElems);
+    const Tensor x = find.at(c);
+    const uint64_t at = (c - x.first) * chunk_elems(x.kind);
+    const uint32_t n = (uint32_t)min(x.n - at, chunk_elems(x.kind));
+    auto squares = [&](auto* p) {
+      using T = std::remove_const_t<std::remove_pointer_t<decltype(p)>>;
+      return c >= keep ? chunk_squares<T, true>(p + at, n) : chunk_squares<T, false>(p + at, n);
+    };
     if (x.kind == kF32)
-      s += chunk_squares(static_cast<const float*>(x.in) + at, n);
+      s += squares(static_cast<const float*>(x.in));
     else if (x.kind == kBF16)
-      s += chunk_squares(static_cast<const __bf16*>(x.in) + at, n);
+      s += squares(static_cast<const __bf16*>(x.in));
     else
-      s += chunk_squares(static_cast<const _Float16*>(x.in) + at, n);
+      s += squares(static_cast<const _Float16*>(x.in));
   }
   s = block_sum<kClipThreads>(s, sh);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
-__global__ __launch_bounds__(kClipThreads) void norm_kernel(const double* partial, uint32_t blocks, double max_norm,
-                                                            float* norm, double* coef) {
+// Every workgroup adds the partial sums again, in the same order, which costs
+// less than a launch between the two passes; then the chunks, last first.
+template <typename L>
+__global__ __launch_bounds__(kClipThreads) void scale_kernel(const L list, uint32_t tensors, uint32_t chunks,
+                                                             uint32_t blocks, const double* partial, double max_norm,
+                                                             float* norm) {
   __shared__ double sh[kClipThreads / 64];
+  __shared__ typename Finder<L>::Held held;
   double s = 0.0;
   for (uint32_t i = threadIdx.x; i < blocks; i += kClipThreads) s += partial[i];
-  s = block_sum<kClipThreads>(s, sh);
-  if (threadIdx.x == 0) {
-    const double n = sqrt(s);
-    *norm = (float)n;
-    *coef = n <= max_norm ? 1.0 : max_norm / n;
-  }
-}
-
-__global__ __launch_bounds__(kClipThreads) void scale_kernel(const Tensor* t, uint32_t tensors, uint32_t chunks,
-                                                             const double* coef) {
-  const float k = (float)*coef;
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const Tensor x = t[find_tensor(t, tensors, c)];
+  const double total = sqrt(block_sum<kClipThreads>(s, sh));
+  if (blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)total;
+  const float k = (float)(total <= max_norm ? 1.0 : max_norm / total);
+  const Finder<L> find(list, tensors, held);
+  for (uint32_t r = blockIdx.x; r < chunks; r += gridDim.x) {
+    const uint32_t c = chunks - 1 - r;
+    const Tensor x = find.at(c);
     if (k == 1.0f && x.in == x.out) continue;
-    const uint64_t at = (uint64_t)(c - x.first) * kChunkElems;
-    const uint32_t n = (uint32_t)min(x.n - at, kChunkElems);
+    const uint64_t at = (c - x.first) * chunk_elems(x.kind);
+    const uint32_t n = (uint32_t)min(x.n - at, chunk_elems(x.kind));
     if (x.kind == kF32)
       chunk_scale(static_cast<const float*>(x.in) + at, static_cast<float*>(x.out) + at, n, k);
     else if (x.kind == kBF16)
@@ -881,6 +1011,19 @@ __global__ __launch_bounds__(kClipThreads) void scale_kernel(const Tensor* t, ui
     else
       chunk_scale(static_cast<const _Float16*>(x.in) + at, static_cast<_Float16*>(x.out) + at, n, k);
   }
+}
+
+template <typename L>
+hipError_t clip_list(const L& list, uint32_t tensors, uint32_t chunks, uint32_t keep, double max_norm, float* norm,
+                     double* partial, hipStream_t s) {
+  const uint32_t blocks = std::min(chunks, kClipBlocks);
+  if (blocks) {
+    squares_kernel<<<blocks, kClipThreads, 0, s>>>(list, tensors, chunks, keep, partial);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  scale_kernel<<<std::max(std::min(chunks, kScaleBlocks), 1u), kClipThreads, 0, s>>>(list, tensors, chunks, blocks, partial, max_norm, norm);
+  return hipGetLastError();
 }
 
 uint64_t up16(uint64_t b) { return (b + 15) & ~15ull; }
@@ -930,12 +1073,14 @@ hipError_t launch_preference(const Logits& l, const Pairs& p, void* ws, hipStrea
     pairs_kernel<256><<<std::min<uint32_t>(p.pairs, 1u << 20), 256, 0, s>>>(p, l.rows, states, g, losses);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  mean_kernel<256><<<1, 256, 0, s>>>(losses, p.pairs, p.loss);
-  if ((e = hipGetLastError()) != hipSuccess || !l.rows || !l.dx) return e;
-  const Scale c = make_scale(l.tau);
-  if (l.kind == kF32) return grad_t<float>(l, c, states, g, s);
-  if (l.kind == kBF16) return grad_t<__bf16>(l, c, states, g, s);
-  return grad_t<_Float16>(l, c, states, g, s);
+  if (!l.rows || !l.dx) {
+    mean_kernel<256><<<1, 256, 0, s>>>(losses, p.pairs, p.loss);
+    return hipGetLastError();
+  }
+  const GradArgs a{l, make_scale(l.tau), states, g, losses, p.pairs, p.loss};
+  if (l.kind == kF32) return grad_t<float>(a, s);
+  if (l.kind == kBF16) return grad_t<__bf16>(a, s);
+  return grad_t<_Float16>(a, s);
 }
 
 hipError_t launch_policy(const Logits& l, const Policy& p, void*, hipStream_t s) {
@@ -954,32 +1099,27 @@ hipError_t launch_policy(const Logits& l, const Policy& p, void*, hipStream_t s)
 
 hipError_t launch_clip(Tensor* t, uint32_t tensors, double max_norm, float* norm, void* ws, hipStream_t s) {
   char* at = static_cast<char*>(ws);
-  Tensor* list = reinterpret_cast<Tensor*>(at);
+  Tensor* stored = reinterpret_cast<Tensor*>(at);
   at += up16((uint64_t)tensors * sizeof(Tensor));
   double* partial = reinterpret_cast<double*>(at);
-  double* coef = partial + kClipBlocks;
   uint32_t chunks = 0;
   for (uint32_t i = 0; i < tensors; ++i) {
     t[i].first = chunks;
-    chunks += (uint32_t)((t[i].n + kChunkElems - 1) / kChunkElems);
+    chunks += (uint32_t)((t[i].n - 1) / chunk_elems(t[i].kind) + 1);
   }
-  hipError_t e = hipSuccess;
-  for (uint32_t i = 0; i < tensors; i += kUpload) {
-    const uint32_t n = std::min<uint32_t>(kUpload, tensors - i);
-    Upload u{};
-    std::copy(t + i, t + i + n, u.t);
-    upload_kernel<<<1, 128, 0, s>>>(u, list + i, n);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+  // the last chunks that the memory-side cache can hold for the second pass
+  const uint32_t keep = chunks - std::min<uint32_t>(chunks, kKeepBytes / kChunkBytes);
+  DirectList direct{};
+  for (uint32_t i = 0; i < tensors; i += kDirect) {
+    const uint32_t n = std::min(kDirect, tensors - i);
+    for (uint32_t j = 0; j < n; ++j) direct.set(j, t[i + j]);
+    if (tensors <= kDirect) break;
+    upload_kernel<<<1, 256, 0, s>>>(direct, stored + i, n);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  const uint32_t blocks = std::min(chunks, kClipBlocks);
-  if (blocks) {
-    squares_kernel<<<blocks, kClipThreads, 0, s>>>(list, tensors, chunks, partial);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
-  norm_kernel<<<1, kClipThreads, 0, s>>>(partial, blocks, max_norm, norm, coef);
-  if ((e = hipGetLastError()) != hipSuccess || !blocks) return e;
-  scale_kernel<<<blocks, kClipThreads, 0, s>>>(list, tensors, chunks, coef);
-  return hipGetLastError();
+  if (tensors <= kDirect) return clip_list(direct, tensors, chunks, keep, max_norm, norm, partial, s);
+  return clip_list(StoredList{stored}, tensors, chunks, keep, max_norm, norm, partial, s);
 }
 
 }  // namespace hkvt

@@ -15,7 +15,9 @@ returned, not recorded: pass one on with ``logits.backward(grad)``.
 
 from __future__ import annotations
 
+import array
 import ctypes
+import functools
 import pathlib
 from typing import NamedTuple, Optional
 
@@ -96,6 +98,15 @@ def _check(status: int) -> None:
         raise HkvError(status, load().hkv_train_last_error().decode(errors="replace"))
 
 
+def _current_stream(index):
+    """Handle of torch's current stream: the raw lookup where torch has it (the
+    public one builds a Stream object, 2 us of every call)."""
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 class _On:
     """The stream of a call: its handle, and the context in which the call's
     tensors are allocated, so that they belong to that stream."""
@@ -103,7 +114,7 @@ class _On:
     def __init__(self, stream, device):
         self.ctx = None
         if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
+            self.handle = _current_stream(device.index)
             return
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
@@ -145,6 +156,9 @@ def _row_stride(x, name):
 
 
 def _vector(t, dtype, numel, name, device):
+    if (t is not None and t.dtype is dtype and t.dim() == 1 and t.numel() == numel and t.is_contiguous()
+            and t.get_device() == device.index):
+        return t.data_ptr()
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype != dtype:
@@ -153,9 +167,7 @@ def _vector(t, dtype, numel, name, device):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, needs [{numel}]")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, logits on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, logits on {device}")
 
 
 def _grad(x, grad_out):
@@ -168,24 +180,34 @@ def _grad(x, grad_out):
     return grad_out, _row_stride(grad_out, "grad_out")
 
 
-def _workspace(rows, pairs, tensors, device):
-    n = load().hkv_train_workspace_bytes(rows, pairs, tensors)
-    return torch.empty(n, dtype=torch.uint8, device=device), n
+@functools.lru_cache(maxsize=256)
+def _workspace_floats(rows, pairs, tensors):
+    return (load().hkv_train_workspace_bytes(rows, pairs, tensors) + 3) // 4
+
+
+def _outputs(device, rows, pairs, tensors, *sizes):
+    """One allocation of float32: the call's workspace in front, then outputs of
+    the given sizes. Returns the workspace's address and bytes, the outputs'
+    addresses and the outputs."""
+    n = _workspace_floats(rows, pairs, tensors)
+    buf, *outs = torch.empty(n + sum(sizes), dtype=torch.float32, device=device).split_with_sizes((n, *sizes))
+    ws = buf.data_ptr()
+    at, ptrs = ws + 4 * n, []
+    for size in sizes:
+        ptrs.append(at)
+        at += 4 * size
+    return ws, 4 * n, ptrs, outs
 
 
 def token_logprobs(logits, labels, *, temperature: float = 1.0, stream=None):
     """(logp, lse), both [rows] float32: the log-probability of each row's
     label under softmax(logits / temperature), and the normaliser."""
     rows, vocab, stride = _logits(logits, labels)
-    dev = logits.device
-    with _On(stream, dev) as s:
-        out = torch.empty((2, rows), dtype=torch.float32, device=dev)
-        ws, n = _workspace(rows, 0, 0, dev)
-        logp, lse = out.unbind(0)
+    with _On(stream, logits.device) as s:
+        ws, n, (logp, lse), outs = _outputs(logits.device, rows, 0, 0, rows, rows)
         _check(load().hkv_token_logprobs(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride,
-                                         labels.data_ptr(), temperature, logp.data_ptr(), lse.data_ptr(),
-                                         ws.data_ptr(), n, s))
-    return logp, lse
+                                         labels.data_ptr(), temperature, logp, lse, ws, n, s))
+    return tuple(outs)
 
 
 def token_logprobs_backward(logits, labels, lse, grad_logp, *, temperature: float = 1.0, grad_out=None, stream=None):
@@ -219,20 +241,14 @@ def preference_loss(logits, labels, cu_seqlens, ref_logp=None, *, beta: float = 
     cu = _vector(cu_seqlens, torch.int64, 2 * pairs + 1, "cu_seqlens", dev)
     ref = None if ref_logp is None else _vector(ref_logp, torch.float32, rows, "ref_logp", dev)
     with _On(stream, dev) as s:
-        out = torch.empty(1 + 3 * pairs + rows, dtype=torch.float32, device=dev)
-        loss, losses, rewards, logp = out.split((1, pairs, 2 * pairs, rows))
-        gptr, gstride = None, 0
-        if with_grad:
-            grad_out, gstride = _grad(logits, grad_out)
-            gptr = grad_out.data_ptr()
-        else:
-            grad_out = None
-        ws, n = _workspace(rows, pairs, 0, dev)
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        ws, n, ptrs, (losses, rewards, logp) = _outputs(dev, rows, pairs, 0, pairs, 2 * pairs, rows)
+        grad, gstride = _grad(logits, grad_out) if with_grad else (None, 0)
         _check(load().hkv_preference_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride,
                                           labels.data_ptr(), temperature, pairs, cu, ref, beta, label_smoothing,
-                                          grad_scale, loss.data_ptr(), losses.data_ptr(), rewards.data_ptr(),
-                                          logp.data_ptr(), gptr, gstride, ws.data_ptr(), n, s))
-    return PreferenceLoss(loss.view(()), losses, rewards, logp, grad_out)
+                                          grad_scale, loss.data_ptr(), *ptrs,
+                                          None if grad is None else grad.data_ptr(), gstride, ws, n, s))
+    return PreferenceLoss(loss, losses, rewards, logp, grad)
 
 
 def policy_loss(logits, labels, old_logp, advantages, weights, ref_logp=None, *, clip_low: float = 0.2,
@@ -251,20 +267,14 @@ def policy_loss(logits, labels, old_logp, advantages, weights, ref_logp=None, *,
     if kl_coef != 0.0 and ref is None:
         raise ValueError("kl_coef needs ref_logp")
     with _On(stream, dev) as s:
-        out = torch.empty(1 + 3 * rows, dtype=torch.float32, device=dev)
-        loss, token_loss, kl, logp = out.split((1, rows, rows, rows))
-        gptr, gstride = None, 0
-        if with_grad:
-            grad_out, gstride = _grad(logits, grad_out)
-            gptr = grad_out.data_ptr()
-        else:
-            grad_out = None
-        ws, n = _workspace(rows, 0, 0, dev)
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        ws, n, ptrs, (token_loss, kl, logp) = _outputs(dev, rows, 0, 0, rows, rows, rows)
+        grad, gstride = _grad(logits, grad_out) if with_grad else (None, 0)
         _check(load().hkv_policy_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
                                       temperature, old, adv, wts, ref, clip_low, clip_high, kl_coef, grad_scale,
-                                      loss.data_ptr(), token_loss.data_ptr(), kl.data_ptr(), logp.data_ptr(), gptr,
-                                      gstride, ws.data_ptr(), n, s))
-    return PolicyLoss(loss.view(()), token_loss, kl, logp, grad_out)
+                                      loss.data_ptr(), *ptrs, None if grad is None else grad.data_ptr(), gstride,
+                                      ws, n, s))
+    return PolicyLoss(loss, token_loss, kl, logp, grad)
 
 
 def _dense(t) -> bool:
@@ -288,35 +298,40 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
     grads = list(grads)
     if not grads:
         raise ValueError("clip_grad_norm needs at least one tensor")
-    outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
-        raise ValueError(f"{len(outs)} tensors in out, {len(grads)} gradients")
-    dev = grads[0].device
+    dev, n = grads[0].device, len(grads)
     if dev.type != "cuda":
         raise ValueError("gradients must be on a GPU")
-    n = len(grads)
-    for i, g in enumerate(grads):
-        if g.dtype not in KINDS:
-            raise TypeError(f"gradient {i}: dtype {g.dtype} not in {tuple(KINDS)}")
-        if g.device != dev:
-            raise ValueError(f"gradient {i} is on {g.device}, the first on {dev}")
-        if not _dense(g):
-            raise ValueError(f"gradient {i} does not fill one stretch of memory (strides {g.stride()})")
+    kinds = [KINDS.get(g.dtype) for g in grads]
+    if None in kinds:
+        i = kinds.index(None)
+        raise TypeError(f"gradient {i}: dtype {grads[i].dtype} not in {tuple(KINDS)}")
+    if set(map(torch.Tensor.get_device, grads)) != {dev.index}:
+        raise ValueError(f"gradients are on several devices, the first on {dev}")
+    in_order = all(map(torch.Tensor.is_contiguous, grads))
+    if not in_order:
+        for i, g in enumerate(grads):
+            if not _dense(g):
+                raise ValueError(f"gradient {i} does not fill one stretch of memory (strides {g.stride()})")
+    outs = None
     if out is not None:
+        outs = list(out)
+        if len(outs) != n:
+            raise ValueError(f"{len(outs)} tensors in out, {n} gradients")
+        in_order = in_order and all(map(torch.Tensor.is_contiguous, outs))
         for i, (g, o) in enumerate(zip(grads, outs)):
             if o.dtype != g.dtype or o.shape != g.shape or o.device != dev:
                 raise ValueError(f"out {i}: {o.dtype} {tuple(o.shape)} on {o.device}, its gradient is {g.dtype} "
                                  f"{tuple(g.shape)} on {dev}")
-            if o.stride() != g.stride() and not (o.is_contiguous() and g.is_contiguous()):
+            if not in_order and o.stride() != g.stride():
                 raise ValueError(f"out {i} has strides {o.stride()}, its gradient {g.stride()}")
-    pointers = ctypes.c_void_p * n
-    ptrs = pointers(*[g.data_ptr() for g in grads])
-    optrs = None if out is None else pointers(*[o.data_ptr() for o in outs])
-    numel = (ctypes.c_uint64 * n)(*[g.numel() for g in grads])
-    kinds = bytes([KINDS[g.dtype] for g in grads])
+    ptrs = array.array("Q", map(torch.Tensor.data_ptr, grads))
+    optrs = None if outs is None else array.array("Q", map(torch.Tensor.data_ptr, outs))
+    numel = array.array("Q", map(torch.Tensor.numel, grads))
     with _On(stream, dev) as s:
         norm = torch.empty((), dtype=torch.float32, device=dev)
-        ws, nb = _workspace(0, 0, n, dev)
-        _check(load().hkv_clip_grad_norm(n, ptrs, optrs, numel, kinds, max_norm, norm.data_ptr(), ws.data_ptr(), nb,
-                                         s))
+        nb = 4 * _workspace_floats(0, 0, n)
+        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+        _check(load().hkv_clip_grad_norm(n, ptrs.buffer_info()[0], optrs and optrs.buffer_info()[0],
+                                         numel.buffer_info()[0], bytes(kinds), max_norm, norm.data_ptr(),
+                                         ws.data_ptr(), nb, s))
     return norm
