@@ -293,13 +293,45 @@ __device__ __forceinline__ void join(Running& r, const Scale& c, typename Team<N
   r.s = s;
 }
 
+// e^x to a float's precision, the argument in 64 bits: what the float argument
+// of the exponential lacks is put back to first order.
+__device__ __forceinline__ double exp_of(double x) {
+  const double a = x * 1.4426950408889634074;
+  const float f = (float)a, rest = (float)(a - (double)f);
+  const float e = exp2_fast(f);
+  return (double)e * (double)fmaf(rest, 0.69314718f, 1.0f);
+}
+
+// The logarithm to 1e-10, as the row's end takes it: log m = 2 atanh z with
+// z = (m - 1) / (m + 1), |z| < 0.172, whose series after its first term fits a
+// float. (The library's functions in 64 bits cost a row 2 us of one thread and
+// more than a hundred registers of constants.)
+__device__ __forceinline__ double log_from(int exponent, double z) {
+  const float w = (float)(z * z);
+  const float q = fmaf(w, fmaf(w, fmaf(w, fmaf(w, 1.0f / 11, 1.0f / 9), 1.0f / 7), 1.0f / 5), 1.0f / 3);
+  return (double)exponent * 0.69314718055994530942 + 2.0 * (z + z * (double)(w * q));
+}
+
+__device__ __forceinline__ double log_of(double u) {
+  double m = __builtin_amdgcn_frexp_mant(u);
+  int e = __builtin_amdgcn_frexp_exp(u);
+  if (m < 0.70710678) {
+    m *= 2.0;
+    e -= 1;
+  }
+  return log_from(e, (m - 1.0) / (m + 1.0));
+}
+
+// log(1 + u), u >= 0: of a small u every digit stays.
+__device__ __forceinline__ double log1p_of(double u) { return u < 0.41 ? log_from(0, u / (2.0 + u)) : log_of(1.0 + u); }
+
 struct RowEnd {
   double logp, lse;
   RowState state;
 };
 
 // (M, S, x_y) -> log-probability, normaliser and what the gradient needs.
-__device__ RowEnd finish_row(float m, double s, float xy, double inv_tau) {
+__device__ __forceinline__ RowEnd finish_row(float m, double s, float xy, double inv_tau) {
   RowEnd r;
   if (m == -kInf && xy == -kInf && s == 0.0) {
     r.logp = 0.0;
@@ -310,16 +342,16 @@ __device__ RowEnd finish_row(float m, double s, float xy, double inv_tau) {
   double d = ((double)xy - (double)m) * inv_tau;
   if (xy == kInf) d = __builtin_nan("");
   if (d >= 0.0) {
-    const double er = s * exp(-d);
-    r.logp = -log1p(er);
+    const double er = s * (d < 200.0 ? exp_of(-d) : 0.0);
+    r.logp = -log1p_of(er);
     r.lse = (double)xy * inv_tau - r.logp;
-    r.state = RowState{r.logp, xy, (float)(1.0 + er), (float)(er / (1.0 + er)), 1};
+    r.state = RowState{r.logp, xy, (float)(1.0 + er), (float)er / (float)(1.0 + er), 1};
   } else {
-    const double total = s + exp(d);
-    const double lt = log(total);
+    const double total = s + (d > -200.0 ? exp_of(d) : d == d ? 0.0 : d);
+    const double lt = log_of(total);
     r.logp = d - lt;
     r.lse = (double)m * inv_tau + lt;
-    r.state = RowState{r.logp, m, (float)total, (float)(s / total), 1};
+    r.state = RowState{r.logp, m, (float)total, (float)s / (float)total, 1};
   }
   return r;
 }
@@ -411,19 +443,32 @@ struct PolicyIn {
   float old_logp, advantage, weight, ref;
 };
 
-__device__ PolicyRow policy_row(const Policy& p, const PolicyIn& in, double logp) {
-  const double r = exp(logp - (double)in.old_logp), a = in.advantage;
-  const double free = r * a, bound = fmin(fmax(r, p.low), p.high) * a;
+__device__ __forceinline__ PolicyRow policy_row(const Policy& p, const PolicyIn& in, double logp) {
+  const double shift = logp - (double)in.old_logp, a = in.advantage;
+  // a ratio past 2^126 is that; NaN stays
+  const double r = shift > 87.0 ? 8.5e37 : shift < -200.0 ? 0.0 : exp_of(shift);
+  const double free = r * a, bound = (r < p.low ? p.low : r > p.high ? p.high : r) * a;
   double loss = -(free <= bound ? free : bound);
   double g = free <= bound ? -free : 0.0;
   if (!(free == free)) loss = g = free;
   double kl = 0.0;
   if (p.ref) {
-    const double d = (double)in.ref - logp, e = expm1(d);
-    kl = e - d;
+    const double d = (double)in.ref - logp;
+    double slope;  // e^d - 1
+    if (fabs(d) < 0.5) {
+      // d^2 (1/2 + d/6 + ...): the difference itself would lose what is small
+      const float f = (float)d;
+      const float q = fmaf(f, fmaf(f, fmaf(f, fmaf(f, fmaf(f, fmaf(f, 1.0f / 362880, 1.0f / 40320), 1.0f / 5040),
+                                                 1.0f / 720), 1.0f / 120), 1.0f / 24), 1.0f / 6);
+      kl = d * d * (0.5 + d * (double)q);
+      slope = kl + d;
+    } else {
+      slope = (d < 200.0 ? (d > -200.0 ? exp_of(d) : 0.0) : d == d ? (double)kInf : d) - 1.0;
+      kl = slope - d;
+    }
     if (p.kl_coef != 0.0) {
       loss += p.kl_coef * kl;
-      g -= p.kl_coef * e;
+      g -= p.kl_coef * slope;
     }
   }
   return PolicyRow{(float)loss, (float)kl, (float)(g * (double)in.weight * p.grad_scale)};
@@ -489,7 +534,7 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         kept[i] = no_vec<T>();
-        if (v0 + i * NT < nv) kept[i] = load_vec<T, MODE == kPairs>(vecs, v0 + i * NT);
+        if (v0 + i * NT < nv) kept[i] = load_vec<T, MODE == kPairs>(vecs + (ch * NV + i) * (NT * K), tid);
       }
       const uint32_t at = yv >= v0 && (yv - v0) % NT == 0 ? (yv - v0) / NT : ~0u;
 #pragma unroll
@@ -516,7 +561,8 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a
   }
   if (write) {
     float g = p.g, top = e.state.top;
-    float coef = (float)(g * a.c.inv_tau / e.state.total), at_label = (float)(g * a.c.inv_tau * e.state.rest);
+    const float gt = (float)(g * a.c.inv_tau);
+    float coef = gt / e.state.total, at_label = gt * e.state.rest;
     if (NT > 64) {
       if (tid == 0) {
         sh.got[0] = g;
@@ -544,7 +590,7 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (tid + i * NT < nv) store_vec(out + cut.head, tid + i * NT, grad_vec<T>(kept[i], top, a.c.k_hi, coef));
+        if (tid + i * NT < nv) store_vec(out + cut.head + i * (NT * K), tid, grad_vec<T>(kept[i], top, a.c.k_hi, coef));
       if (nv > NT * NV) grad_vecs<T, NT, 4>(vecs, out + cut.head, NT * NV, nv, tid, top, a.c.k_hi, coef);
       grad_singles<T, NT>(row, out, cut, tid, top, a.c.k_hi, coef);
       if (tid == cut.owner(y)) out[y] = (T)at_label;  // after its neighbours, by the same thread
@@ -646,7 +692,7 @@ __global__ __launch_bounds__(NT) void pairs_kernel(const Pairs p, uint32_t rows,
     reward[1] *= p.beta;
     const double m = reward[0] - reward[1];
     // log(1 + e^-m), log(1 + e^m) and sigma(m) from e^-|m|
-    const double e = exp(-fabs(m)), tail = log1p(e);
+    const double e = fabs(m) < 200.0 ? exp_of(-fabs(m)) : m == m ? 0.0 : m, tail = log1p_of(e);
     const double sigma = (m >= 0.0 ? 1.0 : e) / (1.0 + e);
     const double c = p.beta * (m == m ? sigma - 1.0 + p.smoothing : m) / p.pairs * p.grad_scale;
     for (uint32_t t = begin + tid; t < end; t += NT / 2) g[t] = (float)(side ? -c : c);
@@ -706,7 +752,7 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void grad_kernel(const Logits l, 
     return;
   }
   const uint32_t y = y64 >= (int64_t)l.vocab ? 0u : (uint32_t)y64;
-  const float coef = (float)(g * c.inv_tau / st.total);
+  const float coef = (float)(g * c.inv_tau) / st.total;
   grad_vecs<T, NT, 4>(row + cut.head, out + cut.head, cut.begin, cut.end, tid, st.top, c.k_hi, coef);
   grad_singles<T, NT>(row, out, cut, tid, st.top, c.k_hi, coef);
   if (tid == cut.owner(y)) out[y] = (T)(float)(g * c.inv_tau * st.rest);
