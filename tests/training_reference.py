@@ -4,8 +4,8 @@ error bounds that the 32-bit kernels are held to.
 Bounds. eps = 2^-24 is half a step of float32. The sum S of a row's
 exponentials: a term with exponent -a carries at most 2 a eps from its
 argument (weight e^-a, so under 2 eps of the sum), 2 eps from the exponential,
-3 eps from the sum of eight, and 4 eps for each of the few times that a thread
-finds a larger maximum: LOGP = 32 eps covers S, and with it logp, absolutely.
+up to 5 eps from the sum of up to 32 terms, and 4 eps for each of the few times
+that a thread finds a larger maximum: LOGP = 32 eps covers S, and with it logp, absolutely.
 An element of the gradient adds 3 a eps (a <= 60: what is smaller than e^-60 is
 covered by the absolute part) and a few roundings: GRAD = 220 eps, relatively.
 Then the rounding to the output's type, half its step.
