@@ -98,37 +98,23 @@ def _check(status: int) -> None:
         raise HkvError(status, load().hkv_train_last_error().decode(errors="replace"))
 
 
-def _current_stream(index):
-    """Handle of torch's current stream: the raw lookup where torch has it (the
-    public one builds a Stream object, 2 us of every call)."""
-    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
-
-
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-class _On:
-    """The stream of a call: its handle, and the context in which the call's
-    tensors are allocated, so that they belong to that stream."""
+def _current_stream(device):
+    """Handle of torch's current stream: the raw lookup where torch has it (the
+    public one builds a Stream object, 2 us of every call)."""
+    return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
 
-    def __init__(self, stream, device):
-        self.ctx = None
-        if stream is None:
-            self.handle = _current_stream(device.index)
-            return
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        self.handle = stream.cuda_stream
-        self.ctx = torch.cuda.stream(stream)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _on(stream, device):
+    """Context in which a call's tensors are allocated on, and its work goes to,
+    the stream that its caller named."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
 
 
 def _logits(x, labels):
@@ -173,7 +159,8 @@ def _vector(t, dtype, numel, name, device):
 def _grad(x, grad_out):
     """The tensor that takes the gradient, and its row stride."""
     if grad_out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device), x.shape[1]
+        grad = torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        return grad, x.shape[1]
     if grad_out.dtype != x.dtype or grad_out.shape != x.shape or grad_out.device != x.device:
         raise ValueError(f"grad_out: {grad_out.dtype} {tuple(grad_out.shape)} on {grad_out.device}, "
                          f"logits are {x.dtype} {tuple(x.shape)} on {x.device}")
@@ -202,26 +189,30 @@ def _outputs(device, rows, pairs, tensors, *sizes):
 def token_logprobs(logits, labels, *, temperature: float = 1.0, stream=None):
     """(logp, lse), both [rows] float32: the log-probability of each row's
     label under softmax(logits / temperature), and the normaliser."""
+    if stream is not None:
+        with _on(stream, logits.device):
+            return token_logprobs(logits, labels, temperature=temperature)
     rows, vocab, stride = _logits(logits, labels)
-    with _On(stream, logits.device) as s:
-        ws, n, (logp, lse), outs = _outputs(logits.device, rows, 0, 0, rows, rows)
-        _check(load().hkv_token_logprobs(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride,
-                                         labels.data_ptr(), temperature, logp, lse, ws, n, s))
+    ws, n, (logp, lse), outs = _outputs(logits.device, rows, 0, 0, rows, rows)
+    _check(load().hkv_token_logprobs(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
+                                     temperature, logp, lse, ws, n, _current_stream(logits.device)))
     return tuple(outs)
 
 
 def token_logprobs_backward(logits, labels, lse, grad_logp, *, temperature: float = 1.0, grad_out=None, stream=None):
     """The gradient of (grad_logp * logp).sum() with respect to the logits;
     grad_out takes it where given (it may be the logits)."""
+    if stream is not None:
+        with _on(stream, logits.device):
+            return token_logprobs_backward(logits, labels, lse, grad_logp, temperature=temperature, grad_out=grad_out)
     rows, vocab, stride = _logits(logits, labels)
     dev = logits.device
     z = _vector(lse, torch.float32, rows, "lse", dev)
     g = _vector(grad_logp, torch.float32, rows, "grad_logp", dev)
-    with _On(stream, dev) as s:
-        grad_out, gstride = _grad(logits, grad_out)
-        _check(load().hkv_token_logprobs_backward(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride,
-                                                  labels.data_ptr(), temperature, z, g, grad_out.data_ptr(),
-                                                  gstride, s))
+    grad_out, gstride = _grad(logits, grad_out)
+    _check(load().hkv_token_logprobs_backward(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride,
+                                              labels.data_ptr(), temperature, z, g, grad_out.data_ptr(), gstride,
+                                              _current_stream(dev)))
     return grad_out
 
 
@@ -233,6 +224,11 @@ def preference_loss(logits, labels, cu_seqlens, ref_logp=None, *, beta: float = 
     ref_logp: [rows] float32 log-probabilities of the reference (token_logprobs
     of its logits), 0 where not given. grad is grad_scale times the gradient of
     loss; with_grad=False leaves it out."""
+    if stream is not None:
+        with _on(stream, logits.device):
+            return preference_loss(logits, labels, cu_seqlens, ref_logp, beta=beta, label_smoothing=label_smoothing,
+                                   temperature=temperature, grad_scale=grad_scale, with_grad=with_grad,
+                                   grad_out=grad_out)
     rows, vocab, stride = _logits(logits, labels)
     dev = logits.device
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] % 2 != 1:
@@ -240,14 +236,13 @@ def preference_loss(logits, labels, cu_seqlens, ref_logp=None, *, beta: float = 
     pairs = cu_seqlens.shape[0] // 2
     cu = _vector(cu_seqlens, torch.int64, 2 * pairs + 1, "cu_seqlens", dev)
     ref = None if ref_logp is None else _vector(ref_logp, torch.float32, rows, "ref_logp", dev)
-    with _On(stream, dev) as s:
-        loss = torch.empty((), dtype=torch.float32, device=dev)
-        ws, n, ptrs, (losses, rewards, logp) = _outputs(dev, rows, pairs, 0, pairs, 2 * pairs, rows)
-        grad, gstride = _grad(logits, grad_out) if with_grad else (None, 0)
-        _check(load().hkv_preference_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride,
-                                          labels.data_ptr(), temperature, pairs, cu, ref, beta, label_smoothing,
-                                          grad_scale, loss.data_ptr(), *ptrs,
-                                          None if grad is None else grad.data_ptr(), gstride, ws, n, s))
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    ws, n, ptrs, (losses, rewards, logp) = _outputs(dev, rows, pairs, 0, pairs, 2 * pairs, rows)
+    grad, gstride = _grad(logits, grad_out) if with_grad else (None, 0)
+    _check(load().hkv_preference_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
+                                      temperature, pairs, cu, ref, beta, label_smoothing, grad_scale,
+                                      loss.data_ptr(), *ptrs, None if grad is None else grad.data_ptr(), gstride, ws,
+                                      n, _current_stream(dev)))
     return PreferenceLoss(loss, losses, rewards, logp, grad)
 
 
@@ -258,6 +253,11 @@ def policy_loss(logits, labels, old_logp, advantages, weights, ref_logp=None, *,
     weights (what each row counts in the sum), ref_logp: [rows] float32; a
     kl_coef needs ref_logp. grad is grad_scale times the gradient of loss;
     with_grad=False leaves it out."""
+    if stream is not None:
+        with _on(stream, logits.device):
+            return policy_loss(logits, labels, old_logp, advantages, weights, ref_logp, clip_low=clip_low,
+                               clip_high=clip_high, kl_coef=kl_coef, temperature=temperature, grad_scale=grad_scale,
+                               with_grad=with_grad, grad_out=grad_out)
     rows, vocab, stride = _logits(logits, labels)
     dev = logits.device
     old = _vector(old_logp, torch.float32, rows, "old_logp", dev)
@@ -266,14 +266,13 @@ def policy_loss(logits, labels, old_logp, advantages, weights, ref_logp=None, *,
     ref = None if ref_logp is None else _vector(ref_logp, torch.float32, rows, "ref_logp", dev)
     if kl_coef != 0.0 and ref is None:
         raise ValueError("kl_coef needs ref_logp")
-    with _On(stream, dev) as s:
-        loss = torch.empty((), dtype=torch.float32, device=dev)
-        ws, n, ptrs, (token_loss, kl, logp) = _outputs(dev, rows, 0, 0, rows, rows, rows)
-        grad, gstride = _grad(logits, grad_out) if with_grad else (None, 0)
-        _check(load().hkv_policy_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
-                                      temperature, old, adv, wts, ref, clip_low, clip_high, kl_coef, grad_scale,
-                                      loss.data_ptr(), *ptrs, None if grad is None else grad.data_ptr(), gstride,
-                                      ws, n, s))
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    ws, n, ptrs, (token_loss, kl, logp) = _outputs(dev, rows, 0, 0, rows, rows, rows)
+    grad, gstride = _grad(logits, grad_out) if with_grad else (None, 0)
+    _check(load().hkv_policy_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
+                                  temperature, old, adv, wts, ref, clip_low, clip_high, kl_coef, grad_scale,
+                                  loss.data_ptr(), *ptrs, None if grad is None else grad.data_ptr(), gstride, ws, n,
+                                  _current_stream(dev)))
     return PolicyLoss(loss, token_loss, kl, logp, grad)
 
 
@@ -298,6 +297,9 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
     grads = list(grads)
     if not grads:
         raise ValueError("clip_grad_norm needs at least one tensor")
+    if stream is not None:
+        with _on(stream, grads[0].device):
+            return clip_grad_norm(grads, max_norm, out=out)
     dev, n = grads[0].device, len(grads)
     if dev.type != "cuda":
         raise ValueError("gradients must be on a GPU")
@@ -327,11 +329,10 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
     ptrs = array.array("Q", map(torch.Tensor.data_ptr, grads))
     optrs = None if outs is None else array.array("Q", map(torch.Tensor.data_ptr, outs))
     numel = array.array("Q", map(torch.Tensor.numel, grads))
-    with _On(stream, dev) as s:
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        nb = 4 * _workspace_floats(0, 0, n)
-        ws = torch.empty(nb, dtype=torch.uint8, device=dev)
-        _check(load().hkv_clip_grad_norm(n, ptrs.buffer_info()[0], optrs and optrs.buffer_info()[0],
-                                         numel.buffer_info()[0], bytes(kinds), max_norm, norm.data_ptr(),
-                                         ws.data_ptr(), nb, s))
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    nb = 4 * _workspace_floats(0, 0, n)
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    _check(load().hkv_clip_grad_norm(n, ptrs.buffer_info()[0], optrs and optrs.buffer_info()[0],
+                                     numel.buffer_info()[0], bytes(kinds), max_norm, norm.data_ptr(), ws.data_ptr(),
+                                     nb, _current_stream(dev)))
     return norm

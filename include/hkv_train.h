@@ -37,7 +37,8 @@
  *     HKV_F16 whose rows are *_stride elements apart (stride >= vocab; any
  *     alignment of the element type). A gradient may overwrite its logits (same
  *     address, same stride); no other overlap is allowed.
- *   - Results are deterministic: no sum depends on the order of execution.
+ *   - Results are deterministic: no sum depends on the order of execution. (It
+ *     does depend on how a row is aligned, in its last bits.)
  * Limits: rows < 2^31, vocab < 2^29, pairs < 2^30, tensors < 2^20.
  */
 #ifndef HKV_TRAIN_H_

@@ -382,3 +382,141 @@ def test_repeats_are_bitwise_equal():
         again = H.preference_loss(x, y, cu)
         for a, b in zip(first, again):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("vocab", [5, 300, 1025, 4999, 20001])
+@pytest.mark.parametrize("shift", [0, 1, 3, 64])
+def test_nothing_is_written_outside_the_rows(vocab, shift, dtype):
+    """Logits and gradient inside wider arrays, at every kind of alignment and
+    of different ones: what lies around the rows stays as it was."""
+    import hash_table_cache_amd as H
+
+    rows, wide = 9, vocab + 70
+    gen = torch.Generator().manual_seed(shift)
+    whole = torch.randn(rows, wide, generator=gen).to(dtype).to(dev())
+    x = whole[:, shift:shift + vocab]
+    y = torch.randint(0, vocab, (rows,), generator=gen).to(dev())
+    y[4] = -1
+    want = R.Rows(x, y, 1.0)
+    f = (want.logp + 0.05).float().to(dev())
+    ones = torch.ones(rows, device=dev())
+    cu = torch.tensor([0, 4, 9], device=dev())
+    for call in (lambda o: H.token_logprobs_backward(x, y, want.lse.float().to(dev()), ones, grad_out=o),
+                 lambda o: H.preference_loss(x, y, cu, f, grad_out=o).grad,
+                 lambda o: H.policy_loss(x, y, f, ones, ones, grad_out=o).grad):
+        plain = call(None)
+        frame = torch.full((rows + 2, wide + 1), 7.0, dtype=dtype, device=dev())
+        inner = frame[1:-1, 2 + shift // 2:2 + shift // 2 + vocab]
+        call(inner)
+        # another alignment sums a row in another order: both results within their bound of the formula
+        near = 2 * (R.GRAD + R.half_step(dtype)) * R.f64(plain).abs() + R.TINY[dtype]
+        R.assert_near(inner, R.f64(plain), near, "grad")
+        inner.fill_(7.0)
+        assert bool((frame == 7.0).all())
+    before = whole.clone()
+    H.policy_loss(x, y, f, ones, ones, grad_out=x)  # in place
+    assert torch.equal(whole[:, :shift], before[:, :shift])
+    assert torch.equal(whole[:, shift + vocab:], before[:, shift + vocab:])
+
+
+def test_refusals_on_the_gpu():
+    import hash_table_cache_amd as H
+
+    x, y = make(6, 40, torch.float32, 3, special=False)
+    f = torch.zeros(6, device=dev())
+    cu = torch.tensor([0, 3, 6], device=dev())
+    with pytest.raises(TypeError, match="labels"):
+        H.token_logprobs(x, y.int())
+    with pytest.raises(ValueError, match="labels"):
+        H.token_logprobs(x, y[:5])
+    with pytest.raises(ValueError, match="labels"):
+        H.token_logprobs(x, y.cpu())
+    with pytest.raises(ValueError, match="next to each other"):
+        H.token_logprobs(x.t().contiguous().t(), y)
+    with pytest.raises(ValueError, match="overlap"):
+        H.token_logprobs(x[:1].expand(6, 40), y)
+    with pytest.raises(ValueError, match="cu_seqlens"):
+        H.preference_loss(x, y, cu[:2], f)
+    with pytest.raises(ValueError, match="kl_coef"):
+        H.policy_loss(x, y, f, f, f, kl_coef=0.1)
+    with pytest.raises(ValueError, match="grad_out"):
+        H.policy_loss(x, y, f, f, f, grad_out=torch.empty(6, 41, device=dev()))
+    wide = torch.zeros(7, 40, device=dev())
+    with pytest.raises(H.HkvError, match="overlaps"):
+        H.policy_loss(wide[:6], y, f, f, f, grad_out=wide[1:])
+    with pytest.raises(H.HkvError, match="temperature"):
+        H.token_logprobs(x, y, temperature=0.0)
+    with pytest.raises(H.HkvError, match="max_norm"):
+        H.clip_grad_norm([f], -1.0)
+    g = torch.ones(100, device=dev())
+    with pytest.raises(H.HkvError, match="overlap"):
+        H.clip_grad_norm([g, g], 1.0)
+    with pytest.raises(H.HkvError, match="overlap"):
+        H.clip_grad_norm([g[:60], g[50:]], 1.0)
+    with pytest.raises(H.HkvError, match="overlap"):
+        H.clip_grad_norm([g[:60]], 1.0, out=[g[10:70]])
+    with pytest.raises(ValueError, match="stretch"):
+        H.clip_grad_norm([g.view(10, 10)[:, :5]], 1.0)
+    with pytest.raises(ValueError, match="out"):
+        H.clip_grad_norm([g], 1.0, out=[g.half()])
+    with pytest.raises(ValueError, match="tensors in out"):
+        H.clip_grad_norm([g], 1.0, out=[])
+    assert bool((g == 1.0).all())  # no refused call has written
+
+
+def test_lists_longer_than_a_launch_holds():
+    """More tensors than the kernels' arguments or their shared memory hold."""
+    import hash_table_cache_amd as H
+
+    for n in (140, 141, 281, 2049, 5000):
+        sizes = [1 + (i * 37) % 90 for i in range(n)]
+        flat = torch.randn(sum(sizes), device=dev())
+        want = f_norm = float(R.f64(flat).norm())
+        out = torch.zeros_like(flat)
+        got = H.clip_grad_norm(flat.split(sizes), 0.5 * want, out=out.split(sizes))
+        assert float(got) == pytest.approx(f_norm, rel=1e-6)
+        coef = float(torch.tensor(0.5 * want, dtype=torch.float32)) / f_norm
+        R.assert_near(out, R.f64(flat) * coef, R.f64(out).abs() * 4 * R.EPS + 1e-30, f"out {n}")
+
+
+def test_example_learns():
+    import importlib.util
+    import pathlib
+
+    path = pathlib.Path(__file__).resolve().parent.parent / "examples" / "online_feedback.py"
+    spec = importlib.util.spec_from_file_location("online_feedback", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    preference, policy = example.train(steps=40)
+    assert preference[0] == pytest.approx(math.log(2.0), rel=1e-3)  # the model is its own reference at first
+    assert preference[-1] < 0.8 * preference[0]
+    assert all(math.isfinite(v) for v in preference + policy)
+
+
+def test_policy_far_from_the_old_policy():
+    """Ratios and divergences past a float's range, on both sides, and an advantage of 0."""
+    import hash_table_cache_amd as H
+
+    shifts = [300.0, 175.0, 100.0, 85.0, 60.0, 0.4999, 0.5001, -0.5001, 0.0, -60.0, -150.0, -300.0]
+    rows = 3 * len(shifts)
+    x, y = make(rows, 33, torch.float32, 8, special=False)
+    want = R.Rows(x, y, 1.0)
+    d = torch.tensor(shifts * 3, dtype=torch.float64)
+    old, ref = (want.logp - d).float(), (want.logp + d).float()
+    adv = torch.tensor([1.0] * len(shifts) + [-1.0] * len(shifts) + [0.0] * len(shifts))
+    w = torch.full((rows,), 1e-3)
+    for kl_coef, ref_ in ((0.0, None), (0.1, ref)):
+        total, loss, kl, g = R.policy(want, old, adv, w, ref_, 0.2, 0.2, kl_coef, 1.0)
+        got = H.policy_loss(x, y, old.to(dev()), adv.to(dev()), w.to(dev()), None if ref_ is None else ref_.to(dev()),
+                            kl_coef=kl_coef)
+        r = torch.exp(want.logp - old.double())
+        e = torch.exp(ref_.double() - want.logp) if kl_coef else torch.zeros_like(r)
+        slope = (r * adv.double()).abs() + kl_coef * (e + 1)
+        R.assert_near(got.token_loss, loss, slope * R.LOGP + loss.abs() * R.EPS + 1e-37, "token_loss")
+        R.assert_near(got.kl, kl, (e + 1) * R.LOGP + kl.abs() * R.EPS, "kl")
+        delta = slope * R.LOGP * w.double() + g.abs() * 4 * R.EPS
+        ref_grad = want.grad(g)
+        tol = grad_tolerance(want, g, torch.float32, delta)
+        fine = ref_grad.abs().amax(1) < 1e37  # an infinite coefficient times a small probability is infinite, not small
+        R.assert_near(got.grad[fine.to(dev())], ref_grad[fine], tol[fine] + 1e-37, "grad")
