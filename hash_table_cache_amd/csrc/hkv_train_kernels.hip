@@ -211,12 +211,21 @@ struct Running {
     float mx = f[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) mx = fmaxf(mx, f[i]);
+    raise(mx, c);
+    sum<N>(f, c);
+  }
+
+  __device__ __forceinline__ void raise(float mx, const Scale& c) {
     if (__any(mx > m)) {
       const float top = fmaxf(m, mx);
       const float t = top == -kInf ? 0.0f : m - top;
       s *= (double)exp2_fast(fmaf(t, c.k_hi, t * c.k_lo));
       m = top;
     }
+  }
+
+  template <int N>
+  __device__ __forceinline__ void sum(const float* f, const Scale& c) {
     const float base = m == -kInf ? 0.0f : m;
     float e[N];
 #pragma unroll
@@ -246,6 +255,12 @@ __device__ __forceinline__ double block_sum(double v, double* sh) {
   return all;
 }
 
+// What a row's gradient is written from: -coef 2^((x - top) k), at_label at the
+// label; zeros where g is 0.
+struct Slope {
+  float g, top, coef, at_label;
+};
+
 // The threads that serve a row: a part of a wave, a wave, or a workgroup.
 template <int NT>
 struct Team {
@@ -255,7 +270,7 @@ struct Team {
   struct Shared {
     float m[kWaves];
     double s[kWaves];
-    float got[4];
+    Slope got;
   };
   static __device__ __forceinline__ uint32_t thread() { return threadIdx.x % NT; }
   // This team's row; the same in every lane where a wave has one row, and then
@@ -456,6 +471,10 @@ struct PolicyIn {
   float old_logp, advantage, weight, ref;
 };
 
+__device__ __forceinline__ PolicyIn policy_in(const Policy& p, uint32_t t) {
+  return PolicyIn{p.old_logp[t], p.advantages[t], p.weights[t], p.ref ? p.ref[t] : 0.0f};
+}
+
 __device__ __forceinline__ PolicyRow policy_row(const Policy& p, const PolicyIn& in, double logp) {
   const double shift = logp - (double)in.old_logp, a = in.advantage;
   const double r = exp_wide(shift);
@@ -499,6 +518,16 @@ struct RowsArgs {
   uint32_t first;    // row of the first team
 };
 
+// The last step of a policy row, by one thread: its outputs and its slope.
+__device__ __forceinline__ Slope end_policy_row(const RowsArgs& a, uint32_t t, const PolicyIn& in, const RowEnd& e) {
+  PolicyRow p{0.0f, 0.0f, 0.0f};
+  if (e.state.counts) p = policy_row(a.p, in, e.logp);
+  a.p.token_loss[t] = p.loss;
+  a.p.kl[t] = p.kl;
+  const float gt = (float)(p.g * a.c.inv_tau);
+  return Slope{p.g, e.state.top, gt / e.state.total, gt * e.state.rest};
+}
+
 // Statistics of rows, by a team of NT threads each, and for the policy loss,
 // whose coefficient needs its own row alone, the gradient in the same kernel:
 // the first NV vectors of every thread stay in registers from the one to the
@@ -522,12 +551,7 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a
   const int64_t y64 = a.l.labels[t];
   const uint32_t y = y64 < 0 || y64 >= (int64_t)vocab ? 0u : (uint32_t)y64;
   PolicyIn in{};
-  if (MODE == kPolicy && tid == 0) {
-    in.old_logp = a.p.old_logp[t];
-    in.advantage = a.p.advantages[t];
-    in.weight = a.p.weights[t];
-    if (a.p.ref) in.ref = a.p.ref[t];
-  }
+  if (MODE == kPolicy && tid == 0) in = policy_in(a.p, t);
   RowEnd e;
   u32x4 kept[NV];
   if (y64 < 0) {
@@ -557,7 +581,7 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a
     join<NT>(r, a.c, sh);
     if (tid == 0) e = finish_row(r.m, r.s, xy, a.c.inv_tau);
   }
-  PolicyRow p{0.0f, 0.0f, 0.0f};
+  Slope k{};
   if (tid == 0) {
     a.logp[t] = (float)e.logp;
     if (MODE == kLogp && a.lse) a.lse[t] = (float)e.lse;
@@ -565,35 +589,20 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a
       a.states[t] = e.state;
       a.g[t] = 0.0f;
     }
-    if (MODE == kPolicy) {
-      if (e.state.counts) p = policy_row(a.p, in, e.logp);
-      a.p.token_loss[t] = p.loss;
-      a.p.kl[t] = p.kl;
-    }
+    if (MODE == kPolicy) k = end_policy_row(a, t, in, e);
   }
   if (write) {
-    float g = p.g, top = e.state.top;
-    const float gt = (float)(g * a.c.inv_tau);
-    float coef = gt / e.state.total, at_label = gt * e.state.rest;
     if (NT > 64) {
-      if (tid == 0) {
-        sh.got[0] = g;
-        sh.got[1] = top;
-        sh.got[2] = coef;
-        sh.got[3] = at_label;
-      }
+      if (tid == 0) sh.got = k;
       __syncthreads();
-      g = sh.got[0];
-      top = sh.got[1];
-      coef = sh.got[2];
-      at_label = sh.got[3];
+      k = sh.got;
     } else {
-      g = __shfl(g, 0, NT);
-      top = __shfl(top, 0, NT);
-      coef = __shfl(coef, 0, NT);
-      at_label = __shfl(at_label, 0, NT);
+      k.g = __shfl(k.g, 0, NT);
+      k.top = __shfl(k.top, 0, NT);
+      k.coef = __shfl(k.coef, 0, NT);
+      k.at_label = __shfl(k.at_label, 0, NT);
     }
-    if (g == 0.0f) {
+    if (k.g == 0.0f) {
       zero_row<T, NT>(out, cut, tid);
     } else {
       if (y64 >= (int64_t)vocab) {
@@ -602,12 +611,160 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (tid + i * NT < nv) store_vec(out + cut.head + i * (NT * K), tid, grad_vec<T>(kept[i], top, a.c.k_hi, coef));
-      if (nv > NT * NV) grad_vecs<T, NT, 4>(vecs, out + cut.head, NT * NV, nv, tid, top, a.c.k_hi, coef);
-      grad_singles<T, NT>(row, out, cut, tid, top, a.c.k_hi, coef);
-      if (tid == cut.owner(y)) out[y] = (T)at_label;  // after its neighbours, by the same thread
+        if (tid + i * NT < nv)
+          store_vec(out + cut.head + i * (NT * K), tid, grad_vec<T>(kept[i], k.top, a.c.k_hi, k.coef));
+      if (nv > NT * NV) grad_vecs<T, NT, 4>(vecs, out + cut.head, NT * NV, nv, tid, k.top, a.c.k_hi, k.coef);
+      grad_singles<T, NT>(row, out, cut, tid, k.top, a.c.k_hi, k.coef);
+      if (tid == cut.owner(y)) out[y] = (T)k.at_label;  // after its neighbours, by the same thread
     }
   }
+}
+
+// The largest element of a vector.
+template <typename T>
+__device__ __forceinline__ float vec_max(u32x4 raw) {
+  constexpr int K = Io<T>::K;
+  if constexpr (std::is_same_v<T, _Float16>) {
+    const f16x2 a = __builtin_elementwise_max(as_halves(raw[0]), as_halves(raw[1]));
+    const f16x2 b = __builtin_elementwise_max(as_halves(raw[2]), as_halves(raw[3]));
+    const f16x2 m = __builtin_elementwise_max(a, b);
+    return fmaxf((float)m[0], (float)m[1]);
+  } else {
+    float f[K];
+    Io<T>::unpack(raw, f);
+    float m = f[0];
+#pragma unroll
+    for (int i = 1; i < K; ++i) m = fmaxf(m, f[i]);
+    return m;
+  }
+}
+
+// Keeps the compiler from holding on to a vector's unpacked elements, twice its
+// size, between its uses.
+__device__ __forceinline__ void opaque(u32x4& v) { asm volatile("" : "+v"(v)); }
+
+// The policy loss of rows past 128 KiB, value and gradient. One workgroup of
+// such a row fills a compute unit's registers if they are to hold it, and then
+// nothing is read while it joins, and nothing written while it reads. So half
+// as many threads keep RV vectors each in registers and LV in LDS, two rows to
+// a compute unit, and what is past 16 * NT * (RV + LV) bytes is read a second
+// time. 12822 x 131072 fp16: 1172 us (5.45 TB/s) against 1208 us with 1024
+// threads of 16 vectors, 6100 x 100000 bf16: 353 us against 394 us; 4 or 8
+// vectors in LDS 1172 and 1174, 362 and 359 us.
+// All maxima of a chunk come before its sums; the label may be among them, for
+// a sum is taken from any value near the row's maximum.
+template <typename T, int NT, int RV, int LV>
+__global__ __launch_bounds__(NT, NT / 128) void long_policy_kernel(const RowsArgs a) {
+  constexpr int K = Io<T>::K;
+  __shared__ typename Team<NT>::Shared sh;
+  __shared__ u32x4 held[LV][NT];
+  const uint32_t tid = threadIdx.x, vocab = a.l.vocab, t = a.first + blockIdx.x;
+  const T* row = static_cast<const T*>(a.l.x) + (uint64_t)t * a.l.x_stride;
+  T* out = static_cast<T*>(a.l.dx) + (uint64_t)t * a.l.dx_stride;
+  const Cut<T, NT> cut(out, vocab);
+  const T* vecs = row + cut.head;
+  const uint32_t nv = cut.nv;
+  const int64_t y64 = a.l.labels[t];
+  const bool bad = y64 >= (int64_t)vocab;
+  const uint32_t y = y64 < 0 || bad ? 0u : (uint32_t)y64, yv = cut.vec_of(y), el = (y - cut.head) % K;
+  PolicyIn in{};
+  if (tid == 0) in = policy_in(a.p, t);
+  RowEnd e;
+  u32x4 kept[RV];
+  if (y64 < 0) {
+    e.logp = e.lse = 0.0;
+    e.state = RowState{0.0, 0.0f, 1.0f, 0.0f, 0};
+  } else {
+    const float xy = (float)row[y];
+    Running r;
+    auto sum = [&](u32x4 raw, uint32_t v) {
+      float f[K];
+      Io<T>::unpack(raw, f);
+      if (__any(v == yv)) {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+          if (v == yv && el == (uint32_t)i) f[i] = -kInf;
+      }
+      r.sum<K>(f, a.c);
+    };
+    for (uint32_t v0 = (RV + LV) * NT; v0 < nv; v0 += LV * NT) {
+      u32x4 raw[LV];
+      float mx = -kInf;
+#pragma unroll
+      for (int i = 0; i < LV; ++i) {
+        raw[i] = no_vec<T>();
+        if (v0 + tid + i * NT < nv) raw[i] = load_vec<T, true>(vecs, v0 + tid + i * NT);
+      }
+#pragma unroll
+      for (int i = 0; i < LV; ++i) mx = fmaxf(mx, vec_max<T>(raw[i]));
+      r.raise(mx, a.c);
+#pragma unroll
+      for (int i = 0; i < LV; ++i) {
+        opaque(raw[i]);
+        if (v0 + i * NT < nv) sum(raw[i], v0 + tid + i * NT);
+      }
+    }
+    {
+      const uint32_t v0 = RV * NT;
+      u32x4 raw[LV];
+      float mx = -kInf;
+#pragma unroll
+      for (int i = 0; i < LV; ++i) {
+        raw[i] = no_vec<T>();
+        if (v0 + tid + i * NT < nv) raw[i] = load_vec(vecs + v0 * K + i * (NT * K), tid);
+      }
+#pragma unroll
+      for (int i = 0; i < LV; ++i) mx = fmaxf(mx, vec_max<T>(raw[i]));
+      r.raise(mx, a.c);
+#pragma unroll
+      for (int i = 0; i < LV; ++i) {
+        opaque(raw[i]);
+        held[i][tid] = raw[i];
+        if (v0 + i * NT < nv) sum(raw[i], v0 + tid + i * NT);
+      }
+    }
+    float mx = -kInf;
+#pragma unroll
+    for (int i = 0; i < RV; ++i) {
+      kept[i] = no_vec<T>();
+      if (tid + i * NT < nv) kept[i] = load_vec(vecs + i * (NT * K), tid);
+    }
+#pragma unroll
+    for (int i = 0; i < RV; ++i) mx = fmaxf(mx, vec_max<T>(kept[i]));
+    r.raise(mx, a.c);
+#pragma unroll
+    for (int i = 0; i < RV; ++i) {
+      opaque(kept[i]);
+      if (i * NT < nv) sum(kept[i], tid + i * NT);
+    }
+    add_singles<T, NT>(r, row, cut, y, tid, a.c);
+    join<NT>(r, a.c, sh);
+    if (tid == 0) e = bad ? nan_row() : finish_row(r.m, r.s, xy, a.c.inv_tau);
+  }
+  if (tid == 0) {
+    a.logp[t] = (float)e.logp;
+    sh.got = end_policy_row(a, t, in, e);
+  }
+  __syncthreads();
+  const Slope k = sh.got;
+  if (k.g == 0.0f) {
+    zero_row<T, NT>(out, cut, tid);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < RV; ++i) {
+    opaque(kept[i]);
+    if (tid + i * NT < nv)
+      store_vec(out + cut.head + i * (NT * K), tid, grad_vec<T>(kept[i], k.top, a.c.k_hi, k.coef));
+  }
+#pragma unroll
+  for (int i = 0; i < LV; ++i)
+    if (tid + (RV + i) * NT < nv)
+      store_vec(out + cut.head + (RV + i) * (NT * K), tid, grad_vec<T>(held[i][tid], k.top, a.c.k_hi, k.coef));
+  if (nv > (RV + LV) * NT)
+    grad_vecs<T, NT, 2>(vecs, out + cut.head, (RV + LV) * NT, nv, tid, k.top, a.c.k_hi, k.coef);
+  grad_singles<T, NT>(row, out, cut, tid, k.top, a.c.k_hi, k.coef);
+  if (tid == cut.owner(y)) out[y] = (T)k.at_label;  // after its neighbours, by the same thread
 }
 
 // A row's gradient from known statistics is written by several workgroups, two
@@ -830,7 +987,8 @@ hipError_t rows_n(RowsArgs a, hipStream_t s) {
 }
 
 // The smallest team whose registers hold a row, or the largest where there are
-// fewer rows than compute units.
+// fewer rows than compute units; rows that no team holds twice over in a
+// compute unit go by long_policy_kernel.
 template <typename T, Mode MODE>
 hipError_t rows_t(const RowsArgs& a, hipStream_t s) {
   const uint32_t nv = a.l.vocab / Io<T>::K;
@@ -838,6 +996,12 @@ hipError_t rows_t(const RowsArgs& a, hipStream_t s) {
   if (nv <= 64 * 4) return rows_n<T, 64, 4, MODE>(a, s);
   if (nv <= 256 * 4) return rows_n<T, 256, 4, MODE>(a, s);
   if constexpr (MODE == kPolicy) {
+    if (nv > 512 * 16 && a.l.rows >= kFewRows && a.l.dx)
+      return for_rows<512>(a.l.rows, 1, [&](uint32_t first, uint32_t grid) {
+        RowsArgs slice = a;
+        slice.first = first;
+        long_policy_kernel<T, 512, 16, 6><<<grid, 512, 0, s>>>(slice);
+      });
     if (nv > 512 * 16 || a.l.rows < kFewRows) return rows_n<T, 1024, 16, MODE>(a, s);
     if (nv > 512 * 8) return rows_n<T, 512, 16, MODE>(a, s);
   }

@@ -520,3 +520,36 @@ def test_policy_far_from_the_old_policy():
         tol = grad_tolerance(want, g, torch.float32, delta)
         fine = ref_grad.abs().amax(1) < 1e37  # an infinite coefficient times a small probability is infinite, not small
         R.assert_near(got.grad[fine.to(dev())], ref_grad[fine], tol[fine] + 1e-37, "grad")
+
+
+# rows enough that every length goes to the teams of many rows: vectors a row up to 4096, 8192, 12288 and more
+@pytest.mark.parametrize("dtype,vocab", [(torch.float32, 9001), (torch.float32, 32003), (torch.float32, 33001),
+                                         (torch.float32, 60007), (torch.bfloat16, 20001), (torch.bfloat16, 50021),
+                                         (torch.bfloat16, 66003), (torch.bfloat16, 100003), (torch.float16, 66003),
+                                         (torch.float16, 1 << 17)])
+def test_many_rows(dtype, vocab):
+    import hash_table_cache_amd as H
+
+    rows = 259
+    x, y = make(rows, vocab, dtype, 700 + vocab % 1000, pad=5)
+    x[20, :] = -torch.inf  # one candidate, in the last place; the first; a huge gap
+    x[20, vocab - 1], y[20] = 1.0, vocab - 1
+    y[21] = 0
+    x[22, vocab // 2], y[22] = 60000.0, vocab // 2
+    x[23, vocab // 3], y[23] = 60000.0, vocab // 2
+    want = R.Rows(x, y, 0.75)
+    gen = torch.Generator().manual_seed(4)
+    base = want.logp.nan_to_num(0.0, 0.0, -3.0)
+    old = (base + 0.05).float()
+    adv, w = torch.randn(rows, generator=gen), torch.rand(rows, generator=gen)
+    logp, lse = H.token_logprobs(x, y, temperature=0.75)
+    R.assert_near(logp, want.logp, R.LOGP + want.logp.abs().nan_to_num(0, 0, 0) * R.EPS, "logp")
+    total, loss, kl, g = R.policy(want, old, adv, w, None, 0.2, 0.2, 0.0, 256.0)
+    slope = (torch.exp(want.logp - old.double()).nan_to_num(0, 0, 0) * adv.double()).abs()
+    delta = slope * R.LOGP * w.double() * 256.0 + g.abs().nan_to_num(0, 0, 0) * 4 * R.EPS
+    tol = grad_tolerance(want, g, dtype, delta).nan_to_num(0, 0, 0)
+    for out in (None, x):
+        got = H.policy_loss(x, y, old.to(dev()), adv.to(dev()), w.to(dev()), temperature=0.75, grad_scale=256.0,
+                            grad_out=out)
+        R.assert_near(got.logp, want.logp, R.LOGP + want.logp.abs().nan_to_num(0, 0, 0) * R.EPS, "policy logp")
+        R.assert_near(got.grad, want.grad(g), tol, "grad")
