@@ -533,7 +533,7 @@ __device__ __forceinline__ Slope end_policy_row(const RowsArgs& a, uint32_t t, c
 // the first NV vectors of every thread stay in registers from the one to the
 // other, so that a row of up to 16 * NT * NV bytes is read once. Without a
 // gradient the same registers hold what is in flight.
-template <typename T, int NT, int NV, Mode MODE>
+template <typename T, int NT, int NV, Mode MODE, bool kKeep>
 __global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a) {
   using Tm = Team<NT>;
   constexpr int K = Io<T>::K;
@@ -570,7 +570,7 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         kept[i] = no_vec<T>();
-        if (v0 + i * NT < nv) kept[i] = load_vec<T, MODE == kPairs>(vecs + (ch * NV + i) * (NT * K), tid);
+        if (v0 + i * NT < nv) kept[i] = load_vec<T, kKeep>(vecs + (ch * NV + i) * (NT * K), tid);
       }
       const uint32_t at = yv >= v0 && (yv - v0) % NT == 0 ? (yv - v0) / NT : ~0u;
 #pragma unroll
@@ -978,11 +978,14 @@ hipError_t for_rows(uint32_t rows, uint32_t parts, F&& launch) {
   return hipSuccess;
 }
 
-template <typename T, int NT, int NV, Mode MODE>
+// Whether logits are of a size that the caches hold a good part of.
+bool cached(const Logits& l, uint64_t size) { return (uint64_t)l.rows * l.vocab * size <= (768ull << 20); }
+
+template <typename T, int NT, int NV, Mode MODE, bool kKeep = MODE == kPairs>
 hipError_t rows_n(RowsArgs a, hipStream_t s) {
   return for_rows<NT>(a.l.rows, 1, [&](uint32_t first, uint32_t grid) {
     a.first = first;
-    rows_kernel<T, NT, NV, MODE><<<grid, Team<NT>::kBlock, 0, s>>>(a);
+    rows_kernel<T, NT, NV, MODE, kKeep><<<grid, Team<NT>::kBlock, 0, s>>>(a);
   });
 }
 
@@ -1005,7 +1008,14 @@ hipError_t rows_t(const RowsArgs& a, hipStream_t s) {
     if (nv > 512 * 16 || a.l.rows < kFewRows) return rows_n<T, 1024, 16, MODE>(a, s);
     if (nv > 512 * 8) return rows_n<T, 512, 16, MODE>(a, s);
   }
-  if (MODE != kPolicy && a.l.rows < kFewRows) return rows_n<T, 1024, 8, MODE>(a, s);
+  if constexpr (MODE != kPolicy) {
+    if (a.l.rows < kFewRows) return rows_n<T, 1024, 8, MODE>(a, s);
+  }
+  if constexpr (MODE == kPairs) {
+    // far more than the caches hold is not left in them: 15251 x 131072 bf16
+    // is read in 450 us against 500 us
+    if (!cached(a.l, sizeof(T))) return rows_n<T, 512, 8, MODE, false>(a, s);
+  }
   return rows_n<T, 512, 8, MODE>(a, s);
 }
 
@@ -1045,7 +1055,7 @@ hipError_t grad_t(const GradArgs& a, hipStream_t s) {
   // come faster than memory gives them, and the smaller parts' number shows:
   // 4493 x 40009 fp16 (0.36 GB) 158 us against 151 us; far above, 15251 x
   // 131072 bf16 (4 GB), it is 1601 us against 1638 us.
-  if ((uint64_t)a.l.rows * a.l.vocab * sizeof(T) <= (768ull << 20)) return grad_n<T, 256>(a, s);
+  if (cached(a.l, sizeof(T))) return grad_n<T, 256>(a, s);
   return grad_n<T, 128>(a, s);
 }
 
