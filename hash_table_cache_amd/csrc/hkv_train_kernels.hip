@@ -1279,7 +1279,7 @@ uint64_t workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tensors) {
          kClipBlocks * 8 + 16;
 }
 
-hipError_t launch_logprobs(const Logits& l, float* logp, float* lse, void*, hipStream_t s) {
+hipError_t launch_logprobs(const Logits& l, float* logp, float* lse, hipStream_t s) {
   RowsArgs a{};
   a.l = l;
   a.c = make_scale(l.tau);
@@ -1327,7 +1327,7 @@ hipError_t launch_preference(const Logits& l, const Pairs& p, void* ws, hipStrea
   return grad_t<_Float16>(a, s);
 }
 
-hipError_t launch_policy(const Logits& l, const Policy& p, void*, hipStream_t s) {
+hipError_t launch_policy(const Logits& l, const Policy& p, hipStream_t s) {
   if (l.rows) {
     RowsArgs a{};
     a.l = l;

@@ -10,7 +10,8 @@ float16 whose rows may lie inside wider ones (stride(0) >= vocab, stride(1) ==
 1). Labels are int64; a negative one leaves its row out. Work is enqueued on
 ``stream`` (a ``torch.cuda.Stream`` or a handle; torch's current stream by
 default), and what a call allocates belongs to that stream. Gradients are
-returned, not recorded: pass one on with ``logits.backward(grad)``.
+returned, not recorded: pass one on with ``logits.backward(grad)``. A gradient
+written over its logits (``grad_out=logits``) is written behind autograd's back.
 """
 
 from __future__ import annotations
@@ -67,13 +68,13 @@ def _load() -> ctypes.CDLL:
     logits = [u64, u64, u32, vp, u64, vp, f32]
     L.hkv_train_workspace_bytes.argtypes = [u64, u64, u64]
     L.hkv_train_workspace_bytes.restype = u64
-    L.hkv_token_logprobs.argtypes = [*logits, vp, vp, vp, u64, vp]
+    L.hkv_token_logprobs.argtypes = [*logits, vp, vp, vp]
     L.hkv_token_logprobs.restype = st
     L.hkv_token_logprobs_backward.argtypes = [*logits, vp, vp, vp, u64, vp]
     L.hkv_token_logprobs_backward.restype = st
     L.hkv_preference_loss.argtypes = [*logits, u64, vp, vp, f32, f32, f32, vp, vp, vp, vp, vp, u64, vp, u64, vp]
     L.hkv_preference_loss.restype = st
-    L.hkv_policy_loss.argtypes = [*logits, vp, vp, vp, vp, f32, f32, f32, f32, vp, vp, vp, vp, vp, u64, vp, u64, vp]
+    L.hkv_policy_loss.argtypes = [*logits, vp, vp, vp, vp, f32, f32, f32, f32, vp, vp, vp, vp, vp, u64, vp]
     L.hkv_policy_loss.restype = st
     L.hkv_clip_grad_norm.argtypes = [u64, vp, vp, vp, vp, f32, vp, vp, u64, vp]
     L.hkv_clip_grad_norm.restype = st
@@ -172,18 +173,14 @@ def _workspace_floats(rows, pairs, tensors):
     return (load().hkv_train_workspace_bytes(rows, pairs, tensors) + 3) // 4
 
 
-def _outputs(device, rows, pairs, tensors, *sizes):
-    """One allocation of float32: the call's workspace in front, then outputs of
-    the given sizes. Returns the workspace's address and bytes, the outputs'
-    addresses and the outputs."""
-    n = _workspace_floats(rows, pairs, tensors)
-    buf, *outs = torch.empty(n + sum(sizes), dtype=torch.float32, device=device).split_with_sizes((n, *sizes))
-    ws = buf.data_ptr()
-    at, ptrs = ws + 4 * n, []
+def _outputs(device, *sizes):
+    """Float32 tensors of the given sizes as parts of one allocation, and their addresses."""
+    buf = torch.empty(sum(sizes), dtype=torch.float32, device=device)
+    at, ptrs = buf.data_ptr(), []
     for size in sizes:
         ptrs.append(at)
         at += 4 * size
-    return ws, 4 * n, ptrs, outs
+    return ptrs, buf.split_with_sizes(sizes)
 
 
 def token_logprobs(logits, labels, *, temperature: float = 1.0, stream=None):
@@ -193,10 +190,10 @@ def token_logprobs(logits, labels, *, temperature: float = 1.0, stream=None):
         with _on(stream, logits.device):
             return token_logprobs(logits, labels, temperature=temperature)
     rows, vocab, stride = _logits(logits, labels)
-    ws, n, (logp, lse), outs = _outputs(logits.device, rows, 0, 0, rows, rows)
+    (logp, lse), outs = _outputs(logits.device, rows, rows)
     _check(load().hkv_token_logprobs(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
-                                     temperature, logp, lse, ws, n, _current_stream(logits.device)))
-    return tuple(outs)
+                                     temperature, logp, lse, _current_stream(logits.device)))
+    return outs
 
 
 def token_logprobs_backward(logits, labels, lse, grad_logp, *, temperature: float = 1.0, grad_out=None, stream=None):
@@ -237,12 +234,13 @@ def preference_loss(logits, labels, cu_seqlens, ref_logp=None, *, beta: float = 
     cu = _vector(cu_seqlens, torch.int64, 2 * pairs + 1, "cu_seqlens", dev)
     ref = None if ref_logp is None else _vector(ref_logp, torch.float32, rows, "ref_logp", dev)
     loss = torch.empty((), dtype=torch.float32, device=dev)
-    ws, n, ptrs, (losses, rewards, logp) = _outputs(dev, rows, pairs, 0, pairs, 2 * pairs, rows)
+    n = _workspace_floats(rows, pairs, 0)  # the workspace, in front of the outputs
+    (ws, *ptrs), (_, losses, rewards, logp) = _outputs(dev, n, pairs, 2 * pairs, rows)
     grad, gstride = _grad(logits, grad_out) if with_grad else (None, 0)
     _check(load().hkv_preference_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
                                       temperature, pairs, cu, ref, beta, label_smoothing, grad_scale,
                                       loss.data_ptr(), *ptrs, None if grad is None else grad.data_ptr(), gstride, ws,
-                                      n, _current_stream(dev)))
+                                      4 * n, _current_stream(dev)))
     return PreferenceLoss(loss, losses, rewards, logp, grad)
 
 
@@ -267,11 +265,11 @@ def policy_loss(logits, labels, old_logp, advantages, weights, ref_logp=None, *,
     if kl_coef != 0.0 and ref is None:
         raise ValueError("kl_coef needs ref_logp")
     loss = torch.empty((), dtype=torch.float32, device=dev)
-    ws, n, ptrs, (token_loss, kl, logp) = _outputs(dev, rows, 0, 0, rows, rows, rows)
+    ptrs, (token_loss, kl, logp) = _outputs(dev, rows, rows, rows)
     grad, gstride = _grad(logits, grad_out) if with_grad else (None, 0)
     _check(load().hkv_policy_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
                                   temperature, old, adv, wts, ref, clip_low, clip_high, kl_coef, grad_scale,
-                                  loss.data_ptr(), *ptrs, None if grad is None else grad.data_ptr(), gstride, ws, n,
+                                  loss.data_ptr(), *ptrs, None if grad is None else grad.data_ptr(), gstride,
                                   _current_stream(dev)))
     return PolicyLoss(loss, token_loss, kl, logp, grad)
 

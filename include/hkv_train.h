@@ -29,10 +29,10 @@
  * that the GPU can access (the GPU of the logits, or of the first gradient);
  * no C++ exception crosses the boundary. Differences:
  *   - There is no handle. Calls keep nothing from one to the next and allocate
- *     nothing: scratch comes from the caller (`workspace`, 16-byte aligned, at
- *     least hkv_train_workspace_bytes(...) bytes, any contents), must stay the
- *     call's own until the stream has passed it, and every call can be
- *     captured into a HIP graph.
+ *     nothing: where scratch is needed, it comes from the caller (`workspace`,
+ *     16-byte aligned, at least hkv_train_workspace_bytes(...) bytes, any
+ *     contents) and must stay the call's own until the stream has passed it.
+ *     Every call can be captured into a HIP graph.
  *   - Logits and gradients are [rows][vocab] arrays of HKV_F32, HKV_BF16 or
  *     HKV_F16 whose rows are *_stride elements apart (stride >= vocab; any
  *     alignment of the element type). A gradient may overwrite its logits (same
@@ -54,9 +54,9 @@ extern "C" {
 #define HKV_BF16 1u
 #define HKV_F16 2u
 
-/* Bytes of workspace that a call of the given size needs: rows of logits,
- * pairs (hkv_preference_loss), tensors (hkv_clip_grad_norm); 0 for what the
- * call does not have. */
+/* Bytes of workspace that a call needs: rows of logits and pairs for
+ * hkv_preference_loss, tensors for hkv_clip_grad_norm, 0 for what the call does
+ * not have. */
 uint64_t hkv_train_workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tensors);
 
 /*
@@ -68,7 +68,7 @@ uint64_t hkv_train_workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tenso
  */
 hkv_status hkv_token_logprobs(uint64_t rows, uint64_t vocab, uint32_t dtype, const void* logits,
                               uint64_t logits_stride, const int64_t* labels, float temperature, float* logp_out,
-                              float* lse_out, void* workspace, uint64_t workspace_bytes, hipStream_t stream);
+                              float* lse_out, hipStream_t stream);
 
 /*
  * hkv_token_logprobs_backward - gradient of sum_t g_t logp_t:
@@ -128,8 +128,7 @@ hkv_status hkv_policy_loss(uint64_t rows, uint64_t vocab, uint32_t dtype, const 
                            const int64_t* labels, float temperature, const float* old_logp, const float* advantages,
                            const float* weights, const float* ref_logp, float clip_low, float clip_high,
                            float kl_coef, float grad_scale, float* loss_out, float* token_loss_out, float* kl_out,
-                           float* logp_out, void* grad_out, uint64_t grad_stride, void* workspace,
-                           uint64_t workspace_bytes, hipStream_t stream);
+                           float* logp_out, void* grad_out, uint64_t grad_stride, hipStream_t stream);
 
 /*
  * hkv_clip_grad_norm - n = sqrt of the sum of squares over all elements of all
