@@ -263,7 +263,8 @@ HKV_API hkv_status hkv_policy_loss(uint64_t rows, uint64_t vocab, uint32_t dtype
                                    const float* old_logp, const float* advantages, const float* weights,
                                    const float* ref_logp, float clip_low, float clip_high, float kl_coef,
                                    float grad_scale, float* loss_out, float* token_loss_out, float* kl_out,
-                                   float* logp_out, void* grad_out, uint64_t grad_stride, hipStream_t stream) {
+                                   float* logp_out, void* grad_out, uint64_t grad_stride, void* workspace,
+                                   uint64_t workspace_bytes, hipStream_t stream) {
   return guarded([&]() -> hkv_status {
     hkvt::Logits l;
     Buffers buffers;
@@ -286,11 +287,12 @@ HKV_API hkv_status hkv_policy_loss(uint64_t rows, uint64_t vocab, uint32_t dtype
       HKV_TRY(buffers.check(kl_out, rows * 4, "kl_out"));
       HKV_TRY(buffers.check(logp_out, rows * 4, "logp_out"));
     }
+    HKV_TRY(check_workspace(buffers, workspace, workspace_bytes, hkvt::workspace_bytes(rows, 0, 0)));
     DeviceGuard dg(buffers.device());
     if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
     const hkvt::Policy p{old_logp, advantages, weights,    ref_logp, 1.0 - (double)clip_low, 1.0 + (double)clip_high,
                          kl_coef,  grad_scale, loss_out, token_loss_out, kl_out, logp_out};
-    const hipError_t e = hkvt::launch_policy(l, p, stream);
+    const hipError_t e = hkvt::launch_policy(l, p, static_cast<double*>(workspace), stream);
     return e == hipSuccess ? HKV_OK : fail_hip(e, "hkv_policy_loss launch");
   });
 }

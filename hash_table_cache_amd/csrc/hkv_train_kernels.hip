@@ -463,7 +463,8 @@ __device__ __forceinline__ void zero_row(T* out, const Cut<T, NT>& cut, uint32_t
 
 // Value and slope of one row of the policy loss.
 struct PolicyRow {
-  float loss, kl, g;
+  double loss;
+  float kl, g;
 };
 
 // What it takes beside the logits, loaded before them.
@@ -502,7 +503,7 @@ __device__ __forceinline__ PolicyRow policy_row(const Policy& p, const PolicyIn&
       g -= p.kl_coef * slope;
     }
   }
-  return PolicyRow{(float)loss, (float)kl, (float)(g * (double)in.weight * p.grad_scale)};
+  return PolicyRow{loss, (float)kl, (float)(g * (double)in.weight * p.grad_scale)};
 }
 
 enum Mode { kLogp, kPairs, kPolicy };
@@ -515,14 +516,16 @@ struct RowsArgs {
   RowState* states;  // kPairs
   float* g;          // kPairs: the rows' coefficients, cleared here
   Policy p;          // kPolicy
+  double* weighted;  // kPolicy: the rows' terms of the loss
   uint32_t first;    // row of the first team
 };
 
 // The last step of a policy row, by one thread: its outputs and its slope.
 __device__ __forceinline__ Slope end_policy_row(const RowsArgs& a, uint32_t t, const PolicyIn& in, const RowEnd& e) {
-  PolicyRow p{0.0f, 0.0f, 0.0f};
+  PolicyRow p{0.0, 0.0f, 0.0f};
   if (e.state.counts) p = policy_row(a.p, in, e.logp);
-  a.p.token_loss[t] = p.loss;
+  a.p.token_loss[t] = (float)p.loss;
+  a.weighted[t] = e.state.counts ? p.loss * (double)in.weight : 0.0;
   a.p.kl[t] = p.kl;
   const float gt = (float)(p.g * a.c.inv_tau);
   return Slope{p.g, e.state.top, gt / e.state.total, gt * e.state.rest};
@@ -940,25 +943,19 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void grad_kernel(const Logits l, 
   if (tid == cut.owner(y)) out[y] = (T)(float)(g * c.inv_tau * st.rest);
 }
 
+// The sum of the rows' terms, in 64 bits until the end: rewards of both signs
+// leave little of it, and rounded terms would leave that wrong.
 template <int NT>
-__global__ __launch_bounds__(NT) void weighted_sum_kernel(const float* loss, const float* weights, uint32_t n,
-                                                          float* out) {
+__global__ __launch_bounds__(NT) void sum_kernel(const double* terms, uint32_t n, float* out) {
   __shared__ double sh[NT / 64];
   constexpr uint32_t U = 8;
   double sum = 0.0;
   for (uint64_t i = threadIdx.x; i < n; i += U * NT) {
-    float l[U], w[U];
+    double v[U];
 #pragma unroll
-    for (uint32_t u = 0; u < U; ++u) {
-      l[u] = w[u] = 0.0f;
-      if (i + u * NT < n) {
-        l[u] = loss[i + u * NT];
-        w[u] = weights[i + u * NT];
-      }
-    }
+    for (uint32_t u = 0; u < U; ++u) v[u] = i + u * NT < n ? terms[i + u * NT] : 0.0;
 #pragma unroll
-    for (uint32_t u = 0; u < U; ++u)
-      if (l[u] != 0.0f) sum += (double)l[u] * (double)w[u];  // rows left out have 0, whatever their weight
+    for (uint32_t u = 0; u < U; ++u) sum += v[u];
   }
   sum = block_sum<NT>(sum, sh);
   if (threadIdx.x == 0) *out = (float)sum;
@@ -1327,17 +1324,18 @@ hipError_t launch_preference(const Logits& l, const Pairs& p, void* ws, hipStrea
   return grad_t<_Float16>(a, s);
 }
 
-hipError_t launch_policy(const Logits& l, const Policy& p, hipStream_t s) {
+hipError_t launch_policy(const Logits& l, const Policy& p, double* weighted, hipStream_t s) {
   if (l.rows) {
     RowsArgs a{};
     a.l = l;
     a.c = make_scale(l.tau);
     a.logp = p.logp;
     a.p = p;
+    a.weighted = weighted;
     const hipError_t e = rows_d<kPolicy>(a, s);
     if (e != hipSuccess) return e;
   }
-  weighted_sum_kernel<1024><<<1, 1024, 0, s>>>(p.token_loss, p.weights, l.rows, p.loss);
+  sum_kernel<1024><<<1, 1024, 0, s>>>(weighted, l.rows, p.loss);
   return hipGetLastError();
 }
 

@@ -74,7 +74,7 @@ def _load() -> ctypes.CDLL:
     L.hkv_token_logprobs_backward.restype = st
     L.hkv_preference_loss.argtypes = [*logits, u64, vp, vp, f32, f32, f32, vp, vp, vp, vp, vp, u64, vp, u64, vp]
     L.hkv_preference_loss.restype = st
-    L.hkv_policy_loss.argtypes = [*logits, vp, vp, vp, vp, f32, f32, f32, f32, vp, vp, vp, vp, vp, u64, vp]
+    L.hkv_policy_loss.argtypes = [*logits, vp, vp, vp, vp, f32, f32, f32, f32, vp, vp, vp, vp, vp, u64, vp, u64, vp]
     L.hkv_policy_loss.restype = st
     L.hkv_clip_grad_norm.argtypes = [u64, vp, vp, vp, vp, f32, vp, vp, u64, vp]
     L.hkv_clip_grad_norm.restype = st
@@ -265,12 +265,13 @@ def policy_loss(logits, labels, old_logp, advantages, weights, ref_logp=None, *,
     if kl_coef != 0.0 and ref is None:
         raise ValueError("kl_coef needs ref_logp")
     loss = torch.empty((), dtype=torch.float32, device=dev)
-    ptrs, (token_loss, kl, logp) = _outputs(dev, rows, rows, rows)
+    n = _workspace_floats(rows, 0, 0)  # the workspace, in front of the outputs
+    (ws, *ptrs), (_, token_loss, kl, logp) = _outputs(dev, n, rows, rows, rows)
     grad, gstride = _grad(logits, grad_out) if with_grad else (None, 0)
     _check(load().hkv_policy_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
                                   temperature, old, adv, wts, ref, clip_low, clip_high, kl_coef, grad_scale,
-                                  loss.data_ptr(), *ptrs, None if grad is None else grad.data_ptr(), gstride,
-                                  _current_stream(dev)))
+                                  loss.data_ptr(), *ptrs, None if grad is None else grad.data_ptr(), gstride, ws,
+                                  4 * n, _current_stream(dev)))
     return PolicyLoss(loss, token_loss, kl, logp, grad)
 
 

@@ -54,9 +54,9 @@ extern "C" {
 #define HKV_BF16 1u
 #define HKV_F16 2u
 
-/* Bytes of workspace that a call needs: rows of logits and pairs for
- * hkv_preference_loss, tensors for hkv_clip_grad_norm, 0 for what the call does
- * not have. */
+/* Bytes of workspace that a call needs: rows of logits for the two losses,
+ * pairs for hkv_preference_loss, tensors for hkv_clip_grad_norm, 0 for what the
+ * call does not have. */
 uint64_t hkv_train_workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tensors);
 
 /*
@@ -128,7 +128,8 @@ hkv_status hkv_policy_loss(uint64_t rows, uint64_t vocab, uint32_t dtype, const 
                            const int64_t* labels, float temperature, const float* old_logp, const float* advantages,
                            const float* weights, const float* ref_logp, float clip_low, float clip_high,
                            float kl_coef, float grad_scale, float* loss_out, float* token_loss_out, float* kl_out,
-                           float* logp_out, void* grad_out, uint64_t grad_stride, hipStream_t stream);
+                           float* logp_out, void* grad_out, uint64_t grad_stride, void* workspace,
+                           uint64_t workspace_bytes, hipStream_t stream);
 
 /*
  * hkv_clip_grad_norm - n = sqrt of the sum of squares over all elements of all

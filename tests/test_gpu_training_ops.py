@@ -553,3 +553,21 @@ def test_many_rows(dtype, vocab):
                             grad_out=out)
         R.assert_near(got.logp, want.logp, R.LOGP + want.logp.abs().nan_to_num(0, 0, 0) * R.EPS, "policy logp")
         R.assert_near(got.grad, want.grad(g), tol, "grad")
+
+
+def test_policy_loss_that_cancels():
+    """Terms of both signs whose sum is a thousandth of their size."""
+    import hash_table_cache_amd as H
+
+    rows, vocab = 2000, 50
+    x, y = make(rows, vocab, torch.float32, 21, special=False)
+    want = R.Rows(x, y, 1.0)
+    old = want.logp.float()
+    adv = torch.randn(rows, generator=torch.Generator().manual_seed(2))
+    adv -= adv.mean() - 1e-3
+    w = torch.full((rows,), 1.0 / rows)
+    total, loss, _, _ = R.policy(want, old, adv, w, None, 0.2, 0.2, 0.0, 1.0)
+    got = H.policy_loss(x, y, old.to(dev()), adv.to(dev()), w.to(dev()))
+    # each term's error is its logp's, at most 32 eps but of either sign: a random walk of 2000 steps, sixfold
+    walk = 6 * math.sqrt(rows) * float(adv.abs().max()) * 4 * R.EPS / rows
+    assert float(got.loss) == pytest.approx(float(total), abs=walk)

@@ -88,7 +88,8 @@ def test_every_logits_call_refuses(kw, needle):
     assert L.hkv_token_logprobs_backward(*a, P, P, P, 1 << 30, None) == _native.HKV_EINVAL and needle in last()
     assert L.hkv_preference_loss(*a, 1, P, P, .1, 0., 1., P, P, P, P, P, 1 << 30, P, 1 << 20, None) == _native.HKV_EINVAL
     assert needle in last()
-    assert L.hkv_policy_loss(*a, P, P, P, P, .2, .2, 0., 1., P, P, P, P, P, 1 << 30, None) == _native.HKV_EINVAL
+    assert L.hkv_policy_loss(*a, P, P, P, P, .2, .2, 0., 1., P, P, P, P, P, 1 << 30, P, 1 << 20,
+                             None) == _native.HKV_EINVAL
     assert needle in last()
 
 
@@ -115,7 +116,7 @@ def test_policy_refuses(low, high, kl, scale, ref, needle):
     from hash_table_cache_amd import _native
     from hash_table_cache_amd import training as T
 
-    st = T.load().hkv_policy_loss(*logits_args(), P, P, P, ref, low, high, kl, scale, P, P, P, P, P, 8, None)
+    st = T.load().hkv_policy_loss(*logits_args(), P, P, P, ref, low, high, kl, scale, P, P, P, P, P, 8, P, 1 << 20, None)
     assert st == _native.HKV_EINVAL and needle in last()
 
 
