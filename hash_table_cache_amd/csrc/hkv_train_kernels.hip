@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <type_traits>
 
 #include "hkv_train_internal.h"
@@ -27,7 +28,8 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kInf = __builtin_inff();
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr uint32_t kFewRows = 256;  // as many as there are compute units
+constexpr uint32_t kFewRows = 256;    // as many as there are compute units
+constexpr uint32_t kManyRows = 4096;  // as many as there are places for waves of 128 registers
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -116,7 +118,7 @@ struct Scale {
 void split(double v, float* hi, float* lo) {
   *hi = (float)v;
   if ((double)*hi >= v) *hi = std::nextafterf(*hi, 0.0f);
-  *lo = (float)(v - (double)*hi);
+  *lo = std::max((float)(v - (double)*hi), std::numeric_limits<float>::denorm_min());
 }
 
 Scale make_scale(double tau) {
@@ -775,11 +777,12 @@ __global__ __launch_bounds__(NT, NT / 128) void long_policy_kernel(const RowsArg
 // at a time then lies close together in memory. 8192 x 65536 bf16: 298 us (6.3
 // TB/s) in parts of 128 threads, 310 us of 256, 316 us of 512, 341 us with a
 // workgroup a row, 339 us with the parts of a row far apart in the launch; 307
-// and 323 us with one or four vectors a thread. Short rows have one part.
+// and 323 us with one or four vectors a thread. Rows of up to 512 vectors have
+// one part, a wave's or less (30000 x 2500 bf16: 54 us against 66 us).
 template <int NT>
 struct Part {
   static constexpr int kRounds = NT > 64 ? 2 : 4;
-  static constexpr uint32_t kVecs = NT * kRounds;
+  static constexpr uint32_t kVecs = NT > 64 ? NT * kRounds : ~0u;
   static uint32_t parts(uint32_t nv) { return nv ? (nv - 1) / kVecs + 1 : 1; }
 };
 
@@ -876,10 +879,10 @@ __global__ __launch_bounds__(NT) void pairs_kernel(const Pairs p, uint32_t rows,
     reward[0] *= p.beta;
     reward[1] *= p.beta;
     const double m = reward[0] - reward[1];
-    // log(1 + e^-m), log(1 + e^m) and sigma(m) from e^-|m|
+    // log(1 + e^-m), log(1 + e^m) and sigma(m) - 1 from e^-|m|
     const double e = exp_wide(-fabs(m)), tail = log1p_of(e);
-    const double sigma = (m >= 0.0 ? 1.0 : e) / (1.0 + e);
-    const double c = p.beta * (m == m ? sigma - 1.0 + p.smoothing : m) / p.pairs * p.grad_scale;
+    const double below = (m >= 0.0 ? -e : -1.0) / (1.0 + e);
+    const double c = p.beta * (below + p.smoothing) / p.pairs * p.grad_scale;
     for (uint32_t t = begin + tid; t < end; t += NT / 2) g[t] = (float)(side ? -c : c);
     if (threadIdx.x == 0) {
       const double down = fmax(-m, 0.0) + tail, up = fmax(m, 0.0) + tail;
@@ -988,11 +991,28 @@ hipError_t rows_n(RowsArgs a, hipStream_t s) {
 
 // The smallest team whose registers hold a row, or the largest where there are
 // fewer rows than compute units; rows that no team holds twice over in a
-// compute unit go by long_policy_kernel.
+// compute unit go by long_policy_kernel. With rows enough to fill the chip by
+// waves of their own, teams are as small as their registers allow: more rows
+// are on the way in a compute unit, and a wave waits for no other (bf16, larger
+// team / smaller: log-probabilities of 30000 x 5000 79 / 59 us, of 20000 x
+// 12000 124 / 77 us, of 60000 x 600 45 / 21 us; policy loss of 30000 x 2500
+// 115 / 68 us, of 20000 x 12000 246 / 170 us).
 template <typename T, Mode MODE>
 hipError_t rows_t(const RowsArgs& a, hipStream_t s) {
   const uint32_t nv = a.l.vocab / Io<T>::K;
   if (nv <= 16 * 4) return rows_n<T, 16, 4, MODE>(a, s);
+  if (a.l.rows >= kManyRows) {
+    if (nv <= 16 * 8) return rows_n<T, 16, 8, MODE>(a, s);
+    if (nv > 64 * 4 && nv <= 64 * 8) return rows_n<T, 64, 8, MODE>(a, s);
+    if constexpr (MODE == kPolicy) {
+      if (nv > 64 * 8 && nv <= 64 * 16) return rows_n<T, 64, 16, MODE>(a, s);
+      if (nv > 64 * 16 && nv <= 128 * 16) return rows_n<T, 128, 16, MODE>(a, s);
+      if (nv > 128 * 16 && nv <= 256 * 16) return rows_n<T, 256, 16, MODE>(a, s);
+    } else {
+      if (nv > 64 * 8 && nv <= 64 * 16) return rows_n<T, 64, 8, MODE>(a, s);
+      if (nv > 64 * 16 && nv <= 128 * 16) return rows_n<T, 128, 8, MODE>(a, s);
+    }
+  }
   if (nv <= 64 * 4) return rows_n<T, 64, 4, MODE>(a, s);
   if (nv <= 256 * 4) return rows_n<T, 256, 4, MODE>(a, s);
   if constexpr (MODE == kPolicy) {
@@ -1047,7 +1067,8 @@ template <typename T>
 hipError_t grad_t(const GradArgs& a, hipStream_t s) {
   const uint32_t nv = a.l.vocab / Io<T>::K;
   if (nv <= 16 * 4) return grad_n<T, 16>(a, s);
-  if (nv <= 64 * 4) return grad_n<T, 64>(a, s);
+  if (nv <= 64 * 8) return grad_n<T, 64>(a, s);
+  if (nv <= 64 * 16) return grad_n<T, 128>(a, s);
   // Logits of which the caches still hold a good part after their first reading
   // come faster than memory gives them, and the smaller parts' number shows:
   // 4493 x 40009 fp16 (0.36 GB) 158 us against 151 us; far above, 15251 x
@@ -1068,7 +1089,7 @@ template <typename T>
 hipError_t backward_t(const Logits& l, const Scale& c, const float* lse, const float* g, hipStream_t s) {
   const uint32_t nv = l.vocab / Io<T>::K;
   if (nv <= 16 * 4) return backward_n<T, 16>(l, c, lse, g, s);
-  if (nv <= 64 * 4) return backward_n<T, 64>(l, c, lse, g, s);
+  if (nv <= 64 * 8) return backward_n<T, 64>(l, c, lse, g, s);
   return backward_n<T, 128>(l, c, lse, g, s);
 }
 

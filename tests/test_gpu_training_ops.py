@@ -571,3 +571,50 @@ def test_policy_loss_that_cancels():
     # each term's error is its logp's, at most 32 eps but of either sign: a random walk of 2000 steps, sixfold
     walk = 6 * math.sqrt(rows) * float(adv.abs().max()) * 4 * R.EPS / rows
     assert float(got.loss) == pytest.approx(float(total), abs=walk)
+
+
+# rows enough for the small teams: up to 64, 128, 256, 512, 1024, 2048 and 4096 vectors a row
+@pytest.mark.parametrize("dtype,vocab", [(torch.bfloat16, 8), (torch.bfloat16, 509), (torch.float16, 1003),
+                                         (torch.bfloat16, 2001), (torch.float32, 2047), (torch.bfloat16, 4099),
+                                         (torch.bfloat16, 8111), (torch.float32, 7001), (torch.float16, 16001),
+                                         (torch.bfloat16, 30011)])
+def test_thousands_of_rows(dtype, vocab):
+    import hash_table_cache_amd as H
+
+    rows = 4099
+    gen = torch.Generator(device=dev()).manual_seed(vocab)
+    x = torch.randn(rows, vocab, device=dev(), generator=gen).mul_(3.0).to(dtype)
+    y = torch.randint(0, vocab, (rows,), device=dev(), generator=gen)
+    some, labels = make(48, vocab, dtype, 900 + vocab)
+    pick = torch.cat([torch.arange(0, 32), torch.arange(2050, 2058), torch.arange(rows - 8, rows)])
+    x[pick.to(dev())], y[pick.to(dev())] = some, labels
+    want = R.Rows(some, labels, 1.25)
+    logp, lse = H.token_logprobs(x, y, temperature=1.25)
+    R.assert_near(logp[pick], want.logp, R.LOGP + want.logp.abs().nan_to_num(0, 0, 0) * R.EPS, "logp")
+    near = R.LOGP + want.logp.abs().nan_to_num(0, 0, 0) * R.EPS
+    ones = torch.ones(rows, device=dev())
+    old = logp.nan_to_num(0.0, 0.0, -3.0) - 0.05
+    adv = torch.randn(rows, device=dev(), generator=gen)
+    got = H.policy_loss(x, y, old, adv, ones, temperature=1.25, grad_scale=8.0)
+    total, loss, kl, g = R.policy(want, old[pick], adv[pick], ones[pick], None, 0.2, 0.2, 0.0, 8.0)
+    slope = (torch.exp(want.logp - R.f64(old[pick])).nan_to_num(0, 0, 0) * R.f64(adv[pick])).abs()
+    delta = slope * R.LOGP * 8.0 + g.abs().nan_to_num(0, 0, 0) * 4 * R.EPS
+    R.assert_near(got.logp[pick], want.logp, near, "policy logp")
+    R.assert_near(got.grad[pick], want.grad(g), grad_tolerance(want, g, dtype, delta).nan_to_num(0, 0, 0), "policy grad")
+    # one pair of all rows without the special ones, whose NaN would be everyone's
+    y2 = y.clone()
+    y2[pick.to(dev())] = -1
+    y2[40:60] = torch.arange(20, device=dev()) % vocab
+    pref = H.preference_loss(x, y2, torch.tensor([0, 2000, rows], device=dev()), temperature=1.25, grad_scale=8.0)
+    sub = torch.arange(40, 60)
+    want = R.Rows(x[40:60], y2[40:60], 1.25)
+    R.assert_near(pref.logp[sub], want.logp, R.LOGP + want.logp.abs() * R.EPS, "pair logp")
+    reward = R.f64(pref.rewards)
+    c = 0.1 * (torch.sigmoid(reward[0] - reward[1]) - 1) * 8.0
+    g = torch.full((20,), float(c), dtype=torch.float64)
+    # the margin from the float32 rewards is off by an eps of each, sigma by a quarter of that
+    delta = 0.1 * 8.0 * reward.abs().sum() * R.EPS / 4 + g.abs() * 4 * R.EPS
+    R.assert_near(pref.grad[sub], want.grad(g), grad_tolerance(want, g, dtype, delta), "pair grad")
+    assert not bool(pref.grad[pick].any())
+    back = H.token_logprobs_backward(x[40:60], y2[40:60], want.lse.float().to(dev()), g.float().to(dev()), temperature=1.25)
+    assert back.shape == (20, vocab)
