@@ -187,7 +187,8 @@ HKV_API uint64_t hkv_train_workspace_bytes(uint64_t rows, uint64_t pairs, uint64
 
 HKV_API hkv_status hkv_token_logprobs(uint64_t rows, uint64_t vocab, uint32_t dtype, const void* logits,
                                       uint64_t logits_stride, const int64_t* labels, float temperature,
-                                      float* logp_out, float* lse_out, hipStream_t stream) {
+                                      float* logp_out, float* lse_out, void* workspace, uint64_t workspace_bytes,
+                                      hipStream_t stream) {
   return guarded([&]() -> hkv_status {
     hkvt::Logits l;
     Buffers buffers;
@@ -195,9 +196,10 @@ HKV_API hkv_status hkv_token_logprobs(uint64_t rows, uint64_t vocab, uint32_t dt
     if (rows == 0) return HKV_OK;
     HKV_TRY(buffers.check(logp_out, rows * 4, "logp_out"));
     if (lse_out) HKV_TRY(buffers.check(lse_out, rows * 4, "lse_out"));
+    HKV_TRY(check_workspace(buffers, workspace, workspace_bytes, hkvt::workspace_bytes(rows, 0, 0)));
     DeviceGuard dg(buffers.device());
     if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
-    const hipError_t e = hkvt::launch_logprobs(l, logp_out, lse_out, stream);
+    const hipError_t e = hkvt::launch_logprobs(l, logp_out, lse_out, workspace, stream);
     return e == hipSuccess ? HKV_OK : fail_hip(e, "hkv_token_logprobs launch");
   });
 }
@@ -292,7 +294,7 @@ HKV_API hkv_status hkv_policy_loss(uint64_t rows, uint64_t vocab, uint32_t dtype
     if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
     const hkvt::Policy p{old_logp, advantages, weights,    ref_logp, 1.0 - (double)clip_low, 1.0 + (double)clip_high,
                          kl_coef,  grad_scale, loss_out, token_loss_out, kl_out, logp_out};
-    const hipError_t e = hkvt::launch_policy(l, p, static_cast<double*>(workspace), stream);
+    const hipError_t e = hkvt::launch_policy(l, p, workspace, stream);
     return e == hipSuccess ? HKV_OK : fail_hip(e, "hkv_policy_loss launch");
   });
 }

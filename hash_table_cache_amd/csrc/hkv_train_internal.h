@@ -73,11 +73,10 @@ struct Tensor {
 // Bytes of workspace of a call (every part 16-byte aligned).
 uint64_t workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tensors);
 
-hipError_t launch_logprobs(const Logits& l, float* logp, float* lse, hipStream_t s);
+hipError_t launch_logprobs(const Logits& l, float* logp, float* lse, void* ws, hipStream_t s);
 hipError_t launch_backward(const Logits& l, const float* lse, const float* g, hipStream_t s);
 hipError_t launch_preference(const Logits& l, const Pairs& p, void* ws, hipStream_t s);
-// weighted: [rows] workspace.
-hipError_t launch_policy(const Logits& l, const Policy& p, double* weighted, hipStream_t s);
+hipError_t launch_policy(const Logits& l, const Policy& p, void* ws, hipStream_t s);
 
 // A chunk of a tensor's elements.
 constexpr uint64_t kChunkBytes = 32768;

@@ -29,6 +29,7 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 constexpr float kInf = __builtin_inff();
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kFewRows = 256;    // as many as there are compute units
+constexpr uint32_t kSharedRows = 64;
 constexpr uint32_t kManyRows = 4096;  // as many as there are places for waves of 128 registers
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -515,8 +516,8 @@ struct RowsArgs {
   Scale c;
   float* logp;
   float* lse;        // kLogp
-  RowState* states;  // kPairs
-  float* g;          // kPairs: the rows' coefficients, cleared here
+  RowState* states;  // kPairs, and kPolicy where rows are shared
+  float* g;          // the rows' coefficients; kPairs: cleared here
   Policy p;          // kPolicy
   double* weighted;  // kPolicy: the rows' terms of the loss
   uint32_t first;    // row of the first team
@@ -622,6 +623,78 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void rows_kernel(const RowsArgs a
       grad_singles<T, NT>(row, out, cut, tid, k.top, a.c.k_hi, k.coef);
       if (tid == cut.owner(y)) out[y] = (T)k.at_label;  // after its neighbours, by the same thread
     }
+  }
+}
+
+// Few long rows: a row is shared by workgroups, whose running values a wave
+// joins. One workgroup a row reads at what one compute unit can.
+struct Partial {
+  double s;
+  float m;
+};
+
+constexpr uint32_t kMostParts = 64;  // a lane each
+
+template <typename T>
+__global__ __launch_bounds__(256) void part_kernel(const RowsArgs a, uint32_t parts, uint32_t size, Partial* partial) {
+  constexpr int NT = 256, NV = 8, U = 4, K = Io<T>::K;
+  __shared__ typename Team<NT>::Shared sh;
+  const uint32_t tid = threadIdx.x, t = blockIdx.x / parts;
+  const int64_t y64 = a.l.labels[t];
+  if (y64 < 0 || y64 >= (int64_t)a.l.vocab) return;
+  const T* row = static_cast<const T*>(a.l.x) + (uint64_t)t * a.l.x_stride;
+  const Cut<T, NT> cut(row, a.l.vocab, blockIdx.x % parts, size);
+  const T* vecs = row + cut.head;
+  const uint32_t y = (uint32_t)y64, yv = cut.vec_of(y);
+  Running r;
+  for (uint32_t first = cut.begin; first < cut.end; first += NT * NV) {
+    const uint32_t v0 = first + tid;
+    u32x4 raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      raw[i] = no_vec<T>();
+      if (v0 + i * NT < cut.end) raw[i] = load_vec<T, true>(vecs, v0 + i * NT);
+    }
+    const uint32_t at = yv >= v0 && (yv - v0) % NT == 0 ? (yv - v0) / NT : ~0u;
+#pragma unroll
+    for (int i = 0; i < NV; i += U)
+      if (first + i * NT < cut.end) add_vecs<T, U>(r, raw + i, at - i, (y - cut.head) % K, a.c);
+  }
+  add_singles<T, NT>(r, row, cut, y, tid, a.c);
+  join<NT>(r, a.c, sh);
+  if (tid == 0) partial[blockIdx.x] = Partial{r.s, r.m};
+}
+
+template <typename T, Mode MODE>
+__global__ __launch_bounds__(64) void join_kernel(const RowsArgs a, uint32_t parts, const Partial* partial) {
+  __shared__ typename Team<64>::Shared sh;
+  const uint32_t t = blockIdx.x, lane = threadIdx.x;
+  const int64_t y64 = a.l.labels[t];
+  PolicyIn in{};
+  if (MODE == kPolicy && lane == 0) in = policy_in(a.p, t);
+  RowEnd e;
+  if (y64 < 0) {
+    e.logp = e.lse = 0.0;
+    e.state = RowState{0.0, 0.0f, 1.0f, 0.0f, 0};
+  } else if (y64 >= (int64_t)a.l.vocab) {
+    e = nan_row();
+  } else {
+    const float xy = (float)(static_cast<const T*>(a.l.x) + (uint64_t)t * a.l.x_stride)[y64];
+    Running r;
+    if (lane < parts) {
+      const Partial p = partial[t * parts + lane];
+      r.s = p.s;
+      r.m = p.m;
+    }
+    join<64>(r, a.c, sh);
+    if (lane == 0) e = finish_row(r.m, r.s, xy, a.c.inv_tau);
+  }
+  if (lane == 0) {
+    a.logp[t] = (float)e.logp;
+    if (MODE == kLogp && a.lse) a.lse[t] = (float)e.lse;
+    if (MODE != kLogp) a.states[t] = e.state;
+    if (MODE == kPairs) a.g[t] = 0.0f;
+    if (MODE == kPolicy) a.g[t] = end_policy_row(a, t, in, e).g;
   }
 }
 
@@ -1036,8 +1109,32 @@ hipError_t rows_t(const RowsArgs& a, hipStream_t s) {
   return rows_n<T, 512, 8, MODE>(a, s);
 }
 
+// Whether rows are shared by workgroups: so few that one to a row leaves most of
+// the chip idle, and longer than one takes in a round. Calls, shared against
+// not: log-probability of 1 x 262144 fp32 13.5 us against 21.3 us, policy loss
+// 26.7 us against 54 us, of 32 x 200001 bf16 27.4 us against 33.6 us, but of 128 x
+// 100000 fp32 33.8 us against 28.4 us.
+bool shared_rows(const Logits& l) {
+  return l.rows < kSharedRows && l.vocab / (l.kind == kF32 ? 4 : 8) > 1024 * 16;
+}
+
+template <typename T, Mode MODE>
+hipError_t shared_t(const RowsArgs& a, Partial* partial, hipStream_t s) {
+  const uint32_t nv = a.l.vocab / Io<T>::K, parts = std::min(nv / 2048, kMostParts), size = (nv - 1) / parts + 1;
+  part_kernel<T><<<a.l.rows * parts, 256, 0, s>>>(a, parts, size, partial);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  join_kernel<T, MODE><<<a.l.rows, 64, 0, s>>>(a, parts, partial);
+  return hipGetLastError();
+}
+
 template <Mode MODE>
-hipError_t rows_d(const RowsArgs& a, hipStream_t s) {
+hipError_t rows_d(const RowsArgs& a, Partial* partial, hipStream_t s) {
+  if (shared_rows(a.l)) {
+    if (a.l.kind == kF32) return shared_t<float, MODE>(a, partial, s);
+    if (a.l.kind == kBF16) return shared_t<__bf16, MODE>(a, partial, s);
+    return shared_t<_Float16, MODE>(a, partial, s);
+  }
   if (a.l.kind == kF32) return rows_t<float, MODE>(a, s);
   if (a.l.kind == kBF16) return rows_t<__bf16, MODE>(a, s);
   return rows_t<_Float16, MODE>(a, s);
@@ -1075,6 +1172,12 @@ hipError_t grad_t(const GradArgs& a, hipStream_t s) {
   // 131072 bf16 (4 GB), it is 1601 us against 1638 us.
   if (cached(a.l, sizeof(T))) return grad_n<T, 256>(a, s);
   return grad_n<T, 128>(a, s);
+}
+
+hipError_t grad_d(const GradArgs& a, hipStream_t s) {
+  if (a.l.kind == kF32) return grad_t<float>(a, s);
+  if (a.l.kind == kBF16) return grad_t<__bf16>(a, s);
+  return grad_t<_Float16>(a, s);
 }
 
 template <typename T, int NT>
@@ -1290,20 +1393,34 @@ hipError_t clip_list(const L& list, uint32_t tensors, uint32_t chunks, uint32_t 
 
 uint64_t up16(uint64_t b) { return (b + 15) & ~15ull; }
 
+// A call's workspace, handed out from its beginning.
+struct Workspace {
+  char* at;
+  template <typename T>
+  T* take(uint64_t n) {
+    T* p = reinterpret_cast<T*>(at);
+    at += up16(n * sizeof(T));
+    return p;
+  }
+};
+
+uint64_t partials(uint64_t rows) { return rows < kSharedRows ? rows * kMostParts : 0; }
+
 }  // namespace
 
 uint64_t workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tensors) {
-  return up16(rows * sizeof(RowState)) + up16(rows * 4) + up16(pairs * 8) + up16(tensors * sizeof(Tensor)) +
-         kClipBlocks * 8 + 16;
+  return up16(partials(rows) * sizeof(Partial)) + up16(rows * sizeof(RowState)) + up16(rows * 4) + up16(rows * 8) +
+         up16(pairs * 8) + up16(tensors * sizeof(Tensor)) + kClipBlocks * 8;
 }
 
-hipError_t launch_logprobs(const Logits& l, float* logp, float* lse, hipStream_t s) {
+hipError_t launch_logprobs(const Logits& l, float* logp, float* lse, void* ws, hipStream_t s) {
+  Workspace w{static_cast<char*>(ws)};
   RowsArgs a{};
   a.l = l;
   a.c = make_scale(l.tau);
   a.logp = logp;
   a.lse = lse;
-  return rows_d<kLogp>(a, s);
+  return rows_d<kLogp>(a, w.take<Partial>(partials(l.rows)), s);
 }
 
 hipError_t launch_backward(const Logits& l, const float* lse, const float* g, hipStream_t s) {
@@ -1314,12 +1431,11 @@ hipError_t launch_backward(const Logits& l, const float* lse, const float* g, hi
 }
 
 hipError_t launch_preference(const Logits& l, const Pairs& p, void* ws, hipStream_t s) {
-  char* at = static_cast<char*>(ws);
-  RowState* states = reinterpret_cast<RowState*>(at);
-  at += up16((uint64_t)l.rows * sizeof(RowState));
-  float* g = reinterpret_cast<float*>(at);
-  at += up16((uint64_t)l.rows * 4);
-  double* losses = reinterpret_cast<double*>(at);
+  Workspace w{static_cast<char*>(ws)};
+  Partial* partial = w.take<Partial>(partials(l.rows));
+  RowState* states = w.take<RowState>(l.rows);
+  float* g = w.take<float>(l.rows);
+  double* losses = w.take<double>(p.pairs);
   hipError_t e = hipSuccess;
   if (l.rows) {
     RowsArgs a{};
@@ -1328,7 +1444,7 @@ hipError_t launch_preference(const Logits& l, const Pairs& p, void* ws, hipStrea
     a.logp = p.logp;
     a.states = states;
     a.g = g;
-    e = rows_d<kPairs>(a, s);
+    e = rows_d<kPairs>(a, partial, s);
     if (e != hipSuccess) return e;
   }
   if (p.pairs) {
@@ -1339,13 +1455,12 @@ hipError_t launch_preference(const Logits& l, const Pairs& p, void* ws, hipStrea
     mean_kernel<256><<<1, 256, 0, s>>>(losses, p.pairs, p.loss);
     return hipGetLastError();
   }
-  const GradArgs a{l, make_scale(l.tau), states, g, losses, p.pairs, p.loss};
-  if (l.kind == kF32) return grad_t<float>(a, s);
-  if (l.kind == kBF16) return grad_t<__bf16>(a, s);
-  return grad_t<_Float16>(a, s);
+  return grad_d(GradArgs{l, make_scale(l.tau), states, g, losses, p.pairs, p.loss}, s);
 }
 
-hipError_t launch_policy(const Logits& l, const Policy& p, double* weighted, hipStream_t s) {
+hipError_t launch_policy(const Logits& l, const Policy& p, void* ws, hipStream_t s) {
+  Workspace w{static_cast<char*>(ws)};
+  double* weighted = w.take<double>(l.rows);
   if (l.rows) {
     RowsArgs a{};
     a.l = l;
@@ -1353,7 +1468,11 @@ hipError_t launch_policy(const Logits& l, const Policy& p, double* weighted, hip
     a.logp = p.logp;
     a.p = p;
     a.weighted = weighted;
-    const hipError_t e = rows_d<kPolicy>(a, s);
+    Partial* partial = w.take<Partial>(partials(l.rows));
+    a.states = w.take<RowState>(l.rows);
+    a.g = w.take<float>(l.rows);
+    hipError_t e = rows_d<kPolicy>(a, partial, s);
+    if (e == hipSuccess && l.dx && shared_rows(l)) e = grad_d(GradArgs{l, a.c, a.states, a.g, nullptr, 0, nullptr}, s);
     if (e != hipSuccess) return e;
   }
   sum_kernel<1024><<<1, 1024, 0, s>>>(weighted, l.rows, p.loss);
@@ -1361,10 +1480,9 @@ hipError_t launch_policy(const Logits& l, const Policy& p, double* weighted, hip
 }
 
 hipError_t launch_clip(Tensor* t, uint32_t tensors, double max_norm, float* norm, void* ws, hipStream_t s) {
-  char* at = static_cast<char*>(ws);
-  Tensor* stored = reinterpret_cast<Tensor*>(at);
-  at += up16((uint64_t)tensors * sizeof(Tensor));
-  double* partial = reinterpret_cast<double*>(at);
+  Workspace w{static_cast<char*>(ws)};
+  Tensor* stored = w.take<Tensor>(tensors);
+  double* partial = w.take<double>(kClipBlocks);
   uint32_t chunks = 0;
   for (uint32_t i = 0; i < tensors; ++i) {
     t[i].first = chunks;

@@ -68,7 +68,7 @@ def _load() -> ctypes.CDLL:
     logits = [u64, u64, u32, vp, u64, vp, f32]
     L.hkv_train_workspace_bytes.argtypes = [u64, u64, u64]
     L.hkv_train_workspace_bytes.restype = u64
-    L.hkv_token_logprobs.argtypes = [*logits, vp, vp, vp]
+    L.hkv_token_logprobs.argtypes = [*logits, vp, vp, vp, u64, vp]
     L.hkv_token_logprobs.restype = st
     L.hkv_token_logprobs_backward.argtypes = [*logits, vp, vp, vp, u64, vp]
     L.hkv_token_logprobs_backward.restype = st
@@ -190,10 +190,11 @@ def token_logprobs(logits, labels, *, temperature: float = 1.0, stream=None):
         with _on(stream, logits.device):
             return token_logprobs(logits, labels, temperature=temperature)
     rows, vocab, stride = _logits(logits, labels)
-    (logp, lse), outs = _outputs(logits.device, rows, rows)
+    n = _workspace_floats(rows, 0, 0)  # the workspace, in front of the outputs
+    (ws, *ptrs), (_, logp, lse) = _outputs(logits.device, n, rows, rows)
     _check(load().hkv_token_logprobs(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
-                                     temperature, logp, lse, _current_stream(logits.device)))
-    return outs
+                                     temperature, *ptrs, ws, 4 * n, _current_stream(logits.device)))
+    return logp, lse
 
 
 def token_logprobs_backward(logits, labels, lse, grad_logp, *, temperature: float = 1.0, grad_out=None, stream=None):

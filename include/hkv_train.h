@@ -54,9 +54,9 @@ extern "C" {
 #define HKV_BF16 1u
 #define HKV_F16 2u
 
-/* Bytes of workspace that a call needs: rows of logits for the two losses,
- * pairs for hkv_preference_loss, tensors for hkv_clip_grad_norm, 0 for what the
- * call does not have. */
+/* Bytes of workspace that a call needs: rows of logits, pairs for
+ * hkv_preference_loss, tensors for hkv_clip_grad_norm, 0 for what the call does
+ * not have. (hkv_token_logprobs_backward needs none.) */
 uint64_t hkv_train_workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tensors);
 
 /*
@@ -68,7 +68,7 @@ uint64_t hkv_train_workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tenso
  */
 hkv_status hkv_token_logprobs(uint64_t rows, uint64_t vocab, uint32_t dtype, const void* logits,
                               uint64_t logits_stride, const int64_t* labels, float temperature, float* logp_out,
-                              float* lse_out, hipStream_t stream);
+                              float* lse_out, void* workspace, uint64_t workspace_bytes, hipStream_t stream);
 
 /*
  * hkv_token_logprobs_backward - gradient of sum_t g_t logp_t:

@@ -618,3 +618,50 @@ def test_thousands_of_rows(dtype, vocab):
     assert not bool(pref.grad[pick].any())
     back = H.token_logprobs_backward(x[40:60], y2[40:60], want.lse.float().to(dev()), g.float().to(dev()), temperature=1.25)
     assert back.shape == (20, vocab)
+
+
+# few rows so long that workgroups share them: an even cut, a short last part, more than 64 parts' worth
+@pytest.mark.parametrize("dtype,vocab", [(torch.float32, 65541), (torch.float32, 600011), (torch.bfloat16, 131081),
+                                         (torch.float16, 262144), (torch.bfloat16, 1500007)])
+def test_few_long_rows(dtype, vocab):
+    import hash_table_cache_amd as H
+
+    rows = 20
+    x, y = make(rows, vocab, dtype, 800, pad=3)
+    x[16, :] = -torch.inf  # a single candidate at either end, and in the middle
+    x[16, vocab - 1], y[16] = 1.0, vocab - 1
+    x[17, :] = -torch.inf
+    x[17, 0], y[17] = 1.0, 0
+    x[18, :] = -torch.inf
+    x[18, vocab // 2], x[18, vocab // 3], y[18] = 1.0, 2.0, vocab // 3
+    want = R.Rows(x, y, 0.75)
+    near = R.LOGP + want.logp.abs().nan_to_num(0, 0, 0) * R.EPS
+    logp, lse = H.token_logprobs(x, y, temperature=0.75)
+    R.assert_near(logp, want.logp, near, "logp")
+    R.assert_near(lse, want.lse, R.LOGP + want.lse.abs().nan_to_num(0, 0, 0) * R.EPS, "lse")
+    gen = torch.Generator().manual_seed(4)
+    old = (want.logp.nan_to_num(0.0, 0.0, -3.0) + 0.05).float()
+    adv, w = torch.randn(rows, generator=gen), torch.rand(rows, generator=gen)
+    total, loss, kl, g = R.policy(want, old, adv, w, None, 0.2, 0.2, 0.0, 256.0)
+    slope = (torch.exp(want.logp - old.double()).nan_to_num(0, 0, 0) * adv.double()).abs()
+    delta = slope * R.LOGP * w.double() * 256.0 + g.abs().nan_to_num(0, 0, 0) * 4 * R.EPS
+    tol = grad_tolerance(want, g, dtype, delta).nan_to_num(0, 0, 0)
+    args = (old.to(dev()), adv.to(dev()), w.to(dev()))
+    plain = H.policy_loss(x, y, *args, temperature=0.75, with_grad=False)
+    got = H.policy_loss(x, y, *args, temperature=0.75, grad_scale=256.0)
+    R.assert_near(got.token_loss, loss, slope * R.LOGP + loss.abs().nan_to_num(0, 0, 0) * R.EPS, "token_loss")
+    R.assert_near(got.grad, want.grad(g), tol, "grad")
+    assert torch.equal(plain.token_loss.nan_to_num(), got.token_loss.nan_to_num()) and plain.grad is None
+    y[8] = y[9] = y[13] = y[15] = -1  # the NaN rows
+    cu = torch.tensor([0, 3, 10, 16, 20])
+    want = R.Rows(x, y, 0.75)
+    ref = want.logp.nan_to_num(0.0, 0.0, -3.0).float() - 0.1
+    keep = torch.isfinite(want.logp)
+    y[~keep.to(dev())] = -1
+    want = R.Rows(x, y, 0.75)
+    loss, losses, rewards, g = R.preference(want, cu, ref, 0.2, 0.0, 256.0)
+    out = H.preference_loss(x, y, cu.to(dev()), ref.to(dev()), beta=0.2, temperature=0.75, grad_scale=256.0, grad_out=x)
+    d_reward = 0.2 * (cu[1:] - cu[:-1]).double() * R.LOGP
+    R.assert_near(out.rewards, rewards, d_reward + rewards.abs() * R.EPS, "rewards")
+    delta = torch.full((rows,), 256.0 * 0.2 / 2 * float(d_reward.max()) / 2, dtype=torch.float64) + g.abs() * 4 * R.EPS
+    R.assert_near(out.grad, want.grad(g), grad_tolerance(want, g, dtype, delta), "pair grad")

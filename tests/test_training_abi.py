@@ -84,7 +84,7 @@ def test_every_logits_call_refuses(kw, needle):
 
     L = T.load()
     a = logits_args(**kw)
-    assert L.hkv_token_logprobs(*a, P, P, None) == _native.HKV_EINVAL and needle in last()
+    assert L.hkv_token_logprobs(*a, P, P, P, 1 << 20, None) == _native.HKV_EINVAL and needle in last()
     assert L.hkv_token_logprobs_backward(*a, P, P, P, 1 << 30, None) == _native.HKV_EINVAL and needle in last()
     assert L.hkv_preference_loss(*a, 1, P, P, .1, 0., 1., P, P, P, P, P, 1 << 30, P, 1 << 20, None) == _native.HKV_EINVAL
     assert needle in last()
@@ -145,9 +145,10 @@ def test_host_memory_is_refused():
 
     host = torch.zeros(64)
     y = torch.zeros(4, dtype=torch.int64)
-    st = T.load().hkv_token_logprobs(4, 8, 0, host.data_ptr(), 8, y.data_ptr(), 1.0, host.data_ptr(), None, None)
+    st = T.load().hkv_token_logprobs(4, 8, 0, host.data_ptr(), 8, y.data_ptr(), 1.0, host.data_ptr(), None,
+                                     host.data_ptr(), 1 << 20, None)
     assert st == _native.HKV_EINVAL and "logits" in last()
-    assert T.load().hkv_token_logprobs(4, 8, 0, None, 8, None, 1.0, None, None, None) == _native.HKV_EINVAL
+    assert T.load().hkv_token_logprobs(4, 8, 0, None, 8, None, 1.0, None, None, None, 1 << 20, None) == _native.HKV_EINVAL
     assert "NULL" in last()
 
 
