@@ -315,8 +315,9 @@ HKV_API hkv_status hkv_clip_grad_norm(uint64_t tensors, void* const* grads, void
       uintptr_t begin, end;
       bool written;
     };
-    std::vector<Range> ranges;
+    std::vector<Range> ranges, more;  // of the gradients, of outputs elsewhere
     ranges.reserve(outs ? 2 * tensors : tensors);
+    if (outs) more.reserve(tensors);
     uint64_t chunks = 0;
     for (uint64_t i = 0; i < tensors; ++i) {
       uint64_t es = 0;
@@ -333,11 +334,14 @@ HKV_API hkv_status hkv_clip_grad_norm(uint64_t tensors, void* const* grads, void
       chunks += (n - 1) / hkvt::chunk_elems(dtypes[i]) + 1;
       const uintptr_t a = reinterpret_cast<uintptr_t>(grads[i]), b = reinterpret_cast<uintptr_t>(out);
       ranges.push_back({a, a + n * es, out == grads[i]});
-      if (out != grads[i]) ranges.push_back({b, b + n * es, true});
+      if (out != grads[i]) more.push_back({b, b + n * es, true});
     }
     if (chunks >= (1ull << 31)) return fail(HKV_EINVAL, "more than 2^31 chunks of %llu bytes", (unsigned long long)hkvt::kChunkBytes);
     const auto before = [](const Range& a, const Range& b) { return a.begin < b.begin; };
-    if (!std::is_sorted(ranges.begin(), ranges.end(), before)) std::sort(ranges.begin(), ranges.end(), before);
+    for (auto* part : {&ranges, &more})  // mostly in the order of their allocation
+      if (!std::is_sorted(part->begin(), part->end(), before)) std::sort(part->begin(), part->end(), before);
+    const auto middle = ranges.insert(ranges.end(), more.begin(), more.end());
+    std::inplace_merge(ranges.begin(), middle, ranges.end(), before);
     // a range that begins before an earlier one ends, of which one is written
     uintptr_t end = 0, written_end = 0;
     for (const Range& r : ranges) {

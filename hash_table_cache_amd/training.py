@@ -19,6 +19,7 @@ from __future__ import annotations
 import array
 import ctypes
 import functools
+import operator
 import pathlib
 from typing import NamedTuple, Optional
 
@@ -276,6 +277,9 @@ def policy_loss(logits, labels, old_logp, advantages, weights, ref_logp=None, *,
     return PolicyLoss(loss, token_loss, kl, logp, grad)
 
 
+_dtype = operator.attrgetter("dtype")
+
+
 def _dense(t) -> bool:
     """Whether t's elements fill one stretch of memory, in whatever order of its axes."""
     if t.is_contiguous():
@@ -291,9 +295,10 @@ def _dense(t) -> bool:
 def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
     """Scales the gradients (a sequence of tensors, of mixed float types) so
     that their global 2-norm is at most max_norm; returns the norm that they
-    had ([] float32, on their GPU). out: tensors like the gradients that take
-    the result (by default it replaces them). Each tensor has to fill one
-    stretch of memory; the order of its axes is free, and out's is the same."""
+    had ([] float32, on their GPU). out: tensors of the gradients' types and
+    sizes that take the result (by default it replaces them). Each tensor has
+    to fill one stretch of memory; the order of its axes is free, and out's is
+    the same."""
     grads = list(grads)
     if not grads:
         raise ValueError("clip_grad_norm needs at least one tensor")
@@ -303,36 +308,38 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
     dev, n = grads[0].device, len(grads)
     if dev.type != "cuda":
         raise ValueError("gradients must be on a GPU")
-    kinds = [KINDS.get(g.dtype) for g in grads]
-    if None in kinds:
-        i = kinds.index(None)
-        raise TypeError(f"gradient {i}: dtype {grads[i].dtype} not in {tuple(KINDS)}")
-    if set(map(torch.Tensor.get_device, grads)) != {dev.index}:
-        raise ValueError(f"gradients are on several devices, the first on {dev}")
+    dtypes = list(map(_dtype, grads))
+    try:
+        kinds = bytes(map(KINDS.__getitem__, dtypes))
+    except KeyError:
+        i = next(i for i, d in enumerate(dtypes) if d not in KINDS)
+        raise TypeError(f"gradient {i}: dtype {dtypes[i]} not in {tuple(KINDS)}") from None
     in_order = all(map(torch.Tensor.is_contiguous, grads))
     if not in_order:
         for i, g in enumerate(grads):
             if not _dense(g):
                 raise ValueError(f"gradient {i} does not fill one stretch of memory (strides {g.stride()})")
-    outs = None
+    # on which GPU each lies is asked of its address, by the library
+    ptrs = array.array("Q", map(torch.Tensor.data_ptr, grads))
+    numel = array.array("Q", map(torch.Tensor.numel, grads))
+    optrs = None
     if out is not None:
         outs = list(out)
         if len(outs) != n:
             raise ValueError(f"{len(outs)} tensors in out, {n} gradients")
         in_order = in_order and all(map(torch.Tensor.is_contiguous, outs))
-        for i, (g, o) in enumerate(zip(grads, outs)):
-            if o.dtype != g.dtype or o.shape != g.shape or o.device != dev:
-                raise ValueError(f"out {i}: {o.dtype} {tuple(o.shape)} on {o.device}, its gradient is {g.dtype} "
-                                 f"{tuple(g.shape)} on {dev}")
-            if not in_order and o.stride() != g.stride():
-                raise ValueError(f"out {i} has strides {o.stride()}, its gradient {g.stride()}")
-    ptrs = array.array("Q", map(torch.Tensor.data_ptr, grads))
-    optrs = None if outs is None else array.array("Q", map(torch.Tensor.data_ptr, outs))
-    numel = array.array("Q", map(torch.Tensor.numel, grads))
+        if (list(map(_dtype, outs)) != dtypes or array.array("Q", map(torch.Tensor.numel, outs)) != numel
+                or not (in_order or [(o.shape, o.stride()) for o in outs] == [(g.shape, g.stride()) for g in grads])):
+            for i, (g, o) in enumerate(zip(grads, outs)):
+                if (o.dtype, o.numel()) != (g.dtype, g.numel()) or not (
+                        (o.shape, o.stride()) == (g.shape, g.stride()) or (o.is_contiguous() and g.is_contiguous())):
+                    raise ValueError(f"out {i}: {o.dtype} {tuple(o.shape)} with strides {o.stride()}, its gradient is "
+                                     f"{g.dtype} {tuple(g.shape)} with strides {g.stride()}")
+        optrs = array.array("Q", map(torch.Tensor.data_ptr, outs))
     norm = torch.empty((), dtype=torch.float32, device=dev)
     nb = 4 * _workspace_floats(0, 0, n)
     ws = torch.empty(nb, dtype=torch.uint8, device=dev)
     _check(load().hkv_clip_grad_norm(n, ptrs.buffer_info()[0], optrs and optrs.buffer_info()[0],
-                                     numel.buffer_info()[0], bytes(kinds), max_norm, norm.data_ptr(), ws.data_ptr(),
+                                     numel.buffer_info()[0], kinds, max_norm, norm.data_ptr(), ws.data_ptr(),
                                      nb, _current_stream(dev)))
     return norm

@@ -458,6 +458,8 @@ def test_refusals_on_the_gpu():
         H.clip_grad_norm([g[:60]], 1.0, out=[g[10:70]])
     with pytest.raises(ValueError, match="stretch"):
         H.clip_grad_norm([g.view(10, 10)[:, :5]], 1.0)
+    with pytest.raises(H.HkvError, match="pageable"):
+        H.clip_grad_norm([g, torch.ones(5)], 1.0)
     with pytest.raises(ValueError, match="out"):
         H.clip_grad_norm([g], 1.0, out=[g.half()])
     with pytest.raises(ValueError, match="tensors in out"):
