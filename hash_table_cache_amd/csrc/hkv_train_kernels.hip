@@ -314,23 +314,25 @@ __device__ __forceinline__ void join(Running& r, const Scale& c, typename Team<N
   r.s = s;
 }
 
-// e^x to a float's precision, the argument in 64 bits: what the float argument
-// of the exponential lacks is put back to first order.
+// e^x to 1e-11: 2^n times the series of the rest, |u| < 0.35. What is left of a
+// sum of losses of both signs may be a hundredth of them, and a ratio to a
+// float's precision would then be wrong in its fifth digit.
 __device__ __forceinline__ double exp_of(double x) {
-  const double a = x * 1.4426950408889634074;
-  const float f = (float)a, rest = (float)(a - (double)f);
-  const float e = exp2_fast(f);
-  return (double)e * (double)fmaf(rest, 0.69314718f, 1.0f);
-}
-
-// The same past a float's range on both sides, up to e^170, which as a float
-// has long become an infinity.
-__device__ __forceinline__ double exp_wide(double x) {
-  if (x < -200.0) return 0.0;
-  if (!(x > 80.0)) return exp_of(x);
-  if (x == (double)kInf) return x;
-  const double root = exp_of(0.5 * (x < 170.0 ? x : 170.0));
-  return root * root;
+  if (x > 709.0) return (double)kInf;
+  if (x < -745.0) return 0.0;
+  const double n = rint(x * 1.4426950408889634074);
+  const double u = fma(n, -0.69314718055994530942, x);
+  double s = 1.0 / 362880;
+  s = fma(s, u, 1.0 / 40320);
+  s = fma(s, u, 1.0 / 5040);
+  s = fma(s, u, 1.0 / 720);
+  s = fma(s, u, 1.0 / 120);
+  s = fma(s, u, 1.0 / 24);
+  s = fma(s, u, 1.0 / 6);
+  s = fma(s, u, 0.5);
+  s = fma(s, u, 1.0);
+  s = fma(s, u, 1.0);
+  return __builtin_ldexp(s, (int)n);
 }
 
 // The logarithm to 1e-10, as the row's end takes it: log m = 2 atanh z with
@@ -373,12 +375,12 @@ __device__ __forceinline__ RowEnd finish_row(float m, double s, float xy, double
   double d = ((double)xy - (double)m) * inv_tau;
   if (xy == kInf) d = __builtin_nan("");
   if (d >= 0.0) {
-    const double er = s * exp_wide(-d);
+    const double er = s * exp_of(-d);
     r.logp = -log1p_of(er);
     r.lse = (double)xy * inv_tau - r.logp;
     r.state = RowState{r.logp, xy, (float)(1.0 + er), (float)er / (float)(1.0 + er), 1};
   } else {
-    const double total = s + exp_wide(d);
+    const double total = s + exp_of(d);
     const double lt = log_of(total);
     r.logp = d - lt;
     r.lse = (double)m * inv_tau + lt;
@@ -481,7 +483,7 @@ __device__ __forceinline__ PolicyIn policy_in(const Policy& p, uint32_t t) {
 
 __device__ __forceinline__ PolicyRow policy_row(const Policy& p, const PolicyIn& in, double logp) {
   const double shift = logp - (double)in.old_logp, a = in.advantage;
-  const double r = exp_wide(shift);
+  const double r = exp_of(shift);
   const double free = r * a, bound = (r < p.low ? p.low : r > p.high ? p.high : r) * a;
   double loss = -(free <= bound ? free : bound);
   double g = free <= bound ? -free : 0.0;
@@ -498,7 +500,7 @@ __device__ __forceinline__ PolicyRow policy_row(const Policy& p, const PolicyIn&
       kl = d * d * (0.5 + d * (double)q);
       slope = kl + d;
     } else {
-      slope = exp_wide(d) - 1.0;
+      slope = exp_of(d) - 1.0;
       kl = slope - d;
     }
     if (p.kl_coef != 0.0) {
@@ -953,7 +955,7 @@ __global__ __launch_bounds__(NT) void pairs_kernel(const Pairs p, uint32_t rows,
     reward[1] *= p.beta;
     const double m = reward[0] - reward[1];
     // log(1 + e^-m), log(1 + e^m) and sigma(m) - 1 from e^-|m|
-    const double e = exp_wide(-fabs(m)), tail = log1p_of(e);
+    const double e = exp_of(-fabs(m)), tail = log1p_of(e);
     const double below = (m >= 0.0 ? -e : -1.0) / (1.0 + e);
     const double c = p.beta * (below + p.smoothing) / p.pairs * p.grad_scale;
     for (uint32_t t = begin + tid; t < end; t += NT / 2) g[t] = (float)(side ? -c : c);
