@@ -135,6 +135,10 @@ bool overlap(const void* a, uint64_t an, const void* b, uint64_t bn) {
   return an && bn && x < y + bn && y < x + an;
 }
 
+// Whether rows this far apart reach past 2^60 elements, whose bytes the checks
+// below (and the kernels' addresses) could no longer count in 64 bits.
+bool too_far(uint64_t rows, uint64_t stride) { return rows > 1 && stride > (1ull << 60) / (rows - 1); }
+
 // The arguments that every operator on logits has. A call without rows looks
 // at no array but its scalar outputs.
 hkv_status check_logits(Buffers& buffers, uint64_t rows, uint64_t vocab, uint32_t dtype, const void* logits,
@@ -153,6 +157,10 @@ hkv_status check_logits(Buffers& buffers, uint64_t rows, uint64_t vocab, uint32_
   if (grad && (grad_stride < vocab || grad_stride > (1ull << 40)))
     return fail(HKV_EINVAL, "grad_stride = %llu with vocab = %llu", (unsigned long long)grad_stride,
                 (unsigned long long)vocab);
+  if (too_far(rows, stride) || (grad && too_far(rows, grad_stride)))
+    return fail(HKV_EINVAL, "%s = %llu with rows = %llu: an array of more than 2^60 elements",
+                too_far(rows, stride) ? "logits_stride" : "grad_stride",
+                (unsigned long long)(too_far(rows, stride) ? stride : grad_stride), (unsigned long long)rows);
   *out = hkvt::Logits{logits, stride, const_cast<void*>(grad), grad_stride, labels, (uint32_t)rows, (uint32_t)vocab,
                       dtype, temperature};
   if (rows == 0) return HKV_OK;

@@ -39,7 +39,8 @@
  *     address, same stride); no other overlap is allowed.
  *   - Results are deterministic: no sum depends on the order of execution. (It
  *     does depend on how a row is aligned, in its last bits.)
- * Limits: rows < 2^31, vocab < 2^29, pairs < 2^30, tensors < 2^20.
+ * Limits: rows < 2^31, vocab < 2^29, pairs < 2^30, tensors < 2^20, strides up
+ * to 2^40 elements, (rows - 1) * stride up to 2^60.
  */
 #ifndef HKV_TRAIN_H_
 #define HKV_TRAIN_H_
