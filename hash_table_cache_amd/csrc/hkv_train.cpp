@@ -135,6 +135,15 @@ bool overlap(const void* a, uint64_t an, const void* b, uint64_t bn) {
   return an && bn && x < y + bn && y < x + an;
 }
 
+// Whether two [rows][vocab] arrays whose ranges overlap lie in different columns
+// of the same wider rows: no row of the one then reaches into a row of the other.
+bool beside(const void* a, uint64_t a_stride, const void* b, uint64_t b_stride, uint64_t vocab, uint64_t es) {
+  if (a_stride != b_stride) return false;
+  const int64_t elems = ((int64_t)reinterpret_cast<uintptr_t>(a) - (int64_t)reinterpret_cast<uintptr_t>(b)) / (int64_t)es;
+  const int64_t stride = (int64_t)a_stride, column = ((elems % stride) + stride) % stride;
+  return column >= (int64_t)vocab && column <= stride - (int64_t)vocab;
+}
+
 // Whether rows this far apart reach past 2^60 elements, whose bytes the checks
 // below (and the kernels' addresses) could no longer count in 64 bits.
 bool too_far(uint64_t rows, uint64_t stride) { return rows > 1 && stride > (1ull << 60) / (rows - 1); }
@@ -172,7 +181,8 @@ hkv_status check_logits(Buffers& buffers, uint64_t rows, uint64_t vocab, uint32_
     const uint64_t gbytes = ((rows - 1) * grad_stride + vocab) * es;
     HKV_TRY(buffers.check(grad, gbytes, "grad_out"));
     if (reinterpret_cast<uintptr_t>(grad) % es) return fail(HKV_EINVAL, "grad_out is not aligned to its type");
-    if (!(grad == logits && grad_stride == stride) && overlap(grad, gbytes, logits, bytes))
+    if (!(grad == logits && grad_stride == stride) && overlap(grad, gbytes, logits, bytes) &&
+        !beside(grad, grad_stride, logits, stride, vocab, es))
       return fail(HKV_EINVAL, "grad_out overlaps logits without being the same array");
   }
   return HKV_OK;

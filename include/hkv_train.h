@@ -36,7 +36,9 @@
  *   - Logits and gradients are [rows][vocab] arrays of HKV_F32, HKV_BF16 or
  *     HKV_F16 whose rows are *_stride elements apart (stride >= vocab; any
  *     alignment of the element type). A gradient may overwrite its logits (same
- *     address, same stride); no other overlap is allowed.
+ *     address, same stride) or lie beside them (other columns of the same wider
+ *     rows: same stride, no common element); no other overlap of the memory
+ *     from an array's first element to its last is allowed.
  *   - Results are deterministic: no sum depends on the order of execution. (It
  *     does depend on how a row is aligned, in its last bits.)
  * Limits: rows < 2^31, vocab < 2^29, pairs < 2^30, tensors < 2^20, strides up
