@@ -214,7 +214,8 @@ HKV_API hkv_status hkv_token_logprobs(uint64_t rows, uint64_t vocab, uint32_t dt
     if (rows == 0) return HKV_OK;
     HKV_TRY(buffers.check(logp_out, rows * 4, "logp_out"));
     if (lse_out) HKV_TRY(buffers.check(lse_out, rows * 4, "lse_out"));
-    HKV_TRY(check_workspace(buffers, workspace, workspace_bytes, hkvt::workspace_bytes(rows, 0, 0)));
+    const uint64_t need = hkvt::logprobs_workspace_bytes(l);
+    if (need) HKV_TRY(check_workspace(buffers, workspace, workspace_bytes, need));
     DeviceGuard dg(buffers.device());
     if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
     const hipError_t e = hkvt::launch_logprobs(l, logp_out, lse_out, workspace, stream);

@@ -72,6 +72,8 @@ struct Tensor {
 
 // Bytes of workspace of a call (every part 16-byte aligned).
 uint64_t workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tensors);
+// launch_logprobs: 0 unless workgroups share the rows.
+uint64_t logprobs_workspace_bytes(const Logits& l);
 
 hipError_t launch_logprobs(const Logits& l, float* logp, float* lse, void* ws, hipStream_t s);
 hipError_t launch_backward(const Logits& l, const float* lse, const float* g, hipStream_t s);

@@ -1415,6 +1415,8 @@ uint64_t workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tensors) {
          up16(pairs * 8) + up16(tensors * sizeof(Tensor)) + kClipBlocks * 8;
 }
 
+uint64_t logprobs_workspace_bytes(const Logits& l) { return shared_rows(l) ? workspace_bytes(l.rows, 0, 0) : 0; }
+
 hipError_t launch_logprobs(const Logits& l, float* logp, float* lse, void* ws, hipStream_t s) {
   Workspace w{static_cast<char*>(ws)};
   RowsArgs a{};

@@ -170,18 +170,24 @@ def _grad(x, grad_out):
 
 
 @functools.lru_cache(maxsize=256)
-def _workspace_floats(rows, pairs, tensors):
-    return (load().hkv_train_workspace_bytes(rows, pairs, tensors) + 3) // 4
+def _workspace_bytes(rows, pairs, tensors):
+    return load().hkv_train_workspace_bytes(rows, pairs, tensors)
 
 
-def _outputs(device, *sizes):
-    """Float32 tensors of the given sizes as parts of one allocation, and their addresses."""
-    buf = torch.empty(sum(sizes), dtype=torch.float32, device=device)
-    at, ptrs = buf.data_ptr(), []
-    for size in sizes:
-        ptrs.append(at)
-        at += 4 * size
-    return ptrs, buf.split_with_sizes(sizes)
+# Results have memory of their own each, and the workspace goes when the call
+# returns: parts of one allocation would cost a call 2 us less, but a kept logp
+# would hold all of it, torch.save would write all of it, and autograd would
+# take a write into one result for a write into the others.
+def _floats(size, device):
+    return torch.empty(size, dtype=torch.float32, device=device)
+
+
+def _scalar(device):
+    return torch.empty_strided((), (), dtype=torch.float32, device=device)
+
+
+def _workspace(size, device):
+    return torch.empty(size, dtype=torch.uint8, device=device)
 
 
 def token_logprobs(logits, labels, *, temperature: float = 1.0, stream=None):
@@ -191,10 +197,15 @@ def token_logprobs(logits, labels, *, temperature: float = 1.0, stream=None):
         with _on(stream, logits.device):
             return token_logprobs(logits, labels, temperature=temperature)
     rows, vocab, stride = _logits(logits, labels)
-    n = _workspace_floats(rows, 0, 0)  # the workspace, in front of the outputs
-    (ws, *ptrs), (_, logp, lse) = _outputs(logits.device, n, rows, rows)
+    dev = logits.device
+    logp, lse = _floats(rows, dev), _floats(rows, dev)
+    ws, nb = None, 0
+    if rows < 64 and vocab * logits.element_size() > 1 << 18:  # few long rows, the only ones that take a workspace
+        nb = _workspace_bytes(rows, 0, 0)
+        ws = _workspace(nb, dev)
     _check(load().hkv_token_logprobs(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
-                                     temperature, *ptrs, ws, 4 * n, _current_stream(logits.device)))
+                                     temperature, logp.data_ptr(), lse.data_ptr(), ws if ws is None else ws.data_ptr(),
+                                     nb, _current_stream(dev)))
     return logp, lse
 
 
@@ -235,14 +246,15 @@ def preference_loss(logits, labels, cu_seqlens, ref_logp=None, *, beta: float = 
     pairs = cu_seqlens.shape[0] // 2
     cu = _vector(cu_seqlens, torch.int64, 2 * pairs + 1, "cu_seqlens", dev)
     ref = None if ref_logp is None else _vector(ref_logp, torch.float32, rows, "ref_logp", dev)
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    n = _workspace_floats(rows, pairs, 0)  # the workspace, in front of the outputs
-    (ws, *ptrs), (_, losses, rewards, logp) = _outputs(dev, n, pairs, 2 * pairs, rows)
+    loss, losses, rewards, logp = _scalar(dev), _floats(pairs, dev), _floats(2 * pairs, dev), _floats(rows, dev)
+    nb = _workspace_bytes(rows, pairs, 0)
+    ws = _workspace(nb, dev)
     grad, gstride = _grad(logits, grad_out) if with_grad else (None, 0)
     _check(load().hkv_preference_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
                                       temperature, pairs, cu, ref, beta, label_smoothing, grad_scale,
-                                      loss.data_ptr(), *ptrs, None if grad is None else grad.data_ptr(), gstride, ws,
-                                      4 * n, _current_stream(dev)))
+                                      loss.data_ptr(), losses.data_ptr(), rewards.data_ptr(), logp.data_ptr(),
+                                      None if grad is None else grad.data_ptr(), gstride, ws.data_ptr(), nb,
+                                      _current_stream(dev)))
     return PreferenceLoss(loss, losses, rewards, logp, grad)
 
 
@@ -266,14 +278,15 @@ def policy_loss(logits, labels, old_logp, advantages, weights, ref_logp=None, *,
     ref = None if ref_logp is None else _vector(ref_logp, torch.float32, rows, "ref_logp", dev)
     if kl_coef != 0.0 and ref is None:
         raise ValueError("kl_coef needs ref_logp")
-    loss = torch.empty((), dtype=torch.float32, device=dev)
-    n = _workspace_floats(rows, 0, 0)  # the workspace, in front of the outputs
-    (ws, *ptrs), (_, token_loss, kl, logp) = _outputs(dev, n, rows, rows, rows)
+    loss, token_loss, kl, logp = _scalar(dev), _floats(rows, dev), _floats(rows, dev), _floats(rows, dev)
+    nb = _workspace_bytes(rows, 0, 0)
+    ws = _workspace(nb, dev)
     grad, gstride = _grad(logits, grad_out) if with_grad else (None, 0)
     _check(load().hkv_policy_loss(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride, labels.data_ptr(),
                                   temperature, old, adv, wts, ref, clip_low, clip_high, kl_coef, grad_scale,
-                                  loss.data_ptr(), *ptrs, None if grad is None else grad.data_ptr(), gstride, ws,
-                                  4 * n, _current_stream(dev)))
+                                  loss.data_ptr(), token_loss.data_ptr(), kl.data_ptr(), logp.data_ptr(),
+                                  None if grad is None else grad.data_ptr(), gstride, ws.data_ptr(), nb,
+                                  _current_stream(dev)))
     return PolicyLoss(loss, token_loss, kl, logp, grad)
 
 
@@ -336,9 +349,9 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, stream=None):
                     raise ValueError(f"out {i}: {o.dtype} {tuple(o.shape)} with strides {o.stride()}, its gradient is "
                                      f"{g.dtype} {tuple(g.shape)} with strides {g.stride()}")
         optrs = array.array("Q", map(torch.Tensor.data_ptr, outs))
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    nb = 4 * _workspace_floats(0, 0, n)
-    ws = torch.empty(nb, dtype=torch.uint8, device=dev)
+    norm = _scalar(dev)
+    nb = _workspace_bytes(0, 0, n)
+    ws = _workspace(nb, dev)
     _check(load().hkv_clip_grad_norm(n, ptrs.buffer_info()[0], optrs and optrs.buffer_info()[0],
                                      numel.buffer_info()[0], kinds, max_norm, norm.data_ptr(), ws.data_ptr(),
                                      nb, _current_stream(dev)))

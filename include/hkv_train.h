@@ -59,7 +59,8 @@ extern "C" {
 
 /* Bytes of workspace that a call needs: rows of logits, pairs for
  * hkv_preference_loss, tensors for hkv_clip_grad_norm, 0 for what the call does
- * not have. (hkv_token_logprobs_backward needs none.) */
+ * not have. (hkv_token_logprobs_backward needs none, hkv_token_logprobs only for
+ * fewer than 64 rows of more than 256 KiB: its workspace may be NULL otherwise.) */
 uint64_t hkv_train_workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tensors);
 
 /*

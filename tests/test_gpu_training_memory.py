@@ -6,7 +6,7 @@ import torch
 
 import training_reference as R
 from conftest import gpu_available
-from test_gpu_training_ops import TYPES, dev
+from test_gpu_training_ops import TYPES, dev, make
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
 
@@ -59,3 +59,49 @@ def test_columns_that_share_elements_are_refused():
         with pytest.raises(H.HkvError, match="overlaps"):
             H.policy_loss(logits, y, f, f, f, grad_out=out)
     assert not bool(wide.any()) and not bool(flat.any())
+
+
+@pytest.mark.parametrize("rows", [1, 40, 100])
+def test_results_stand_alone(rows):
+    """Every result has memory of its own, of its own size (a kept logp keeps
+    nothing else), and writing into one leaves what autograd saved of another."""
+    import hash_table_cache_amd as H
+
+    x, y = make(rows, 60, torch.float32, 11, special=False)
+    f = torch.zeros(rows, device=dev())
+    cu = torch.tensor([0, rows // 2, rows], device=dev())
+    pref = H.preference_loss(x, y, cu, f)
+    pol = H.policy_loss(x, y, f, f + 1, f + 1, f, kl_coef=0.1)
+    logp, lse = H.token_logprobs(x, y)
+    for results in ((logp, lse), pref, pol):
+        assert len({t.untyped_storage().data_ptr() for t in results}) == len(results)
+        for t in results:
+            assert t.untyped_storage().nbytes() == t.numel() * t.element_size() and t.storage_offset() == 0
+    for saved, other in ((logp, lse), (pref.logp, pref.rewards), (pol.logp, pol.token_loss)):
+        p = torch.ones(rows, device=dev(), requires_grad=True)
+        loss = (p * saved).sum()
+        other.mul_(2.0)
+        loss.backward()
+        assert torch.equal(p.grad, saved)
+
+
+@pytest.mark.parametrize("dtype,rows,vocab", [(torch.float32, 63, 1 << 16), (torch.float32, 64, 65541), (torch.float32, 63, 65540),
+                                              (torch.bfloat16, 1, 1 << 17), (torch.float16, 3, 131081)])
+def test_workspace_of_logprobs(dtype, rows, vocab):
+    """The rule by which log-probabilities go without a workspace is the library's own, on both sides of its borders."""
+    import hash_table_cache_amd as H
+
+    x, y = make(rows, vocab, dtype, 12, special=False)
+    logp, lse = H.token_logprobs(x, y)
+    want = R.Rows(x, y, 1.0)
+    R.assert_near(logp, want.logp, R.LOGP + want.logp.abs() * R.EPS, "logp")
+    L = H.training.load()
+    stream = torch.cuda.current_stream().cuda_stream
+    args = (rows, vocab, H.training.KINDS[dtype], x.data_ptr(), vocab, y.data_ptr(), 1.0, logp.data_ptr(), None, None, 0, stream)
+    few_long = rows < 64 and vocab * x.element_size() // 16 > 1 << 14
+    logp.fill_(7.0)
+    assert (L.hkv_token_logprobs(*args) == 0) == (not few_long)
+    if few_long:
+        assert "workspace" in L.hkv_train_last_error().decode() and bool((logp == 7.0).all())
+    else:
+        R.assert_near(logp, want.logp, R.LOGP + want.logp.abs() * R.EPS, "logp")
