@@ -356,9 +356,11 @@ __device__ __forceinline__ double exp_of(double x) {
   return __builtin_ldexp(s, (int)n);
 }
 
-// The logarithm to 1e-10, as the row's end takes it: log m = 2 atanh z with
-// z = (m - 1) / (m + 1), |z| < 0.172, whose series after its first term fits a
-// float. (The library's functions in 64 bits cost a row 2 us of one thread and
+// The logarithm to 5e-10, as the row's end takes it: log m = 2 atanh z with
+// z = (m - 1) / (m + 1), |z| < 0.172, whose series after its first term is taken
+// in floats: it is at most 3.4e-3, and their roundings of it are what the bound
+// is. (Of log(1 + u) for small u, 1.4e-9 of its size.) A row's sum is off by
+// 1e-8. (The library's functions in 64 bits cost a row 2 us of one thread and
 // more than a hundred registers of constants.)
 __device__ __forceinline__ double log_from(int exponent, double z) {
   const float w = (float)(z * z);
