@@ -120,6 +120,10 @@ hkv_status hkv_preference_loss(uint64_t rows, uint64_t vocab, uint32_t dtype, co
  *   loss = sum_t weights[t] l_t.
  * grad_out = grad_scale * d loss / d logits, where the clamped side of the
  * minimum has no slope and at equality the other side is taken.
+ * A label whose own logit is -inf beside finite ones (logp -inf) has r = 0; with
+ * a finite ref_logp its d is +inf and its kl, inf - inf, NaN. Without kl_coef that
+ * stays in kl_out; with one, l_t and the loss are NaN and the row's coefficient is
+ * infinite: a program that masks labels leaves such rows out by a negative label.
  *   old_logp, advantages, weights [rows] float32, input
  *   ref_logp       [rows] float32, input, nullable (then kl_coef must be 0)
  *   loss_out       [1] float32, output

@@ -52,3 +52,24 @@ def test_weighted_policy_loss(rows, vocab, kl_coef):
     delta = slope * R.LOGP * w.double() * 32.0 + g.abs() * 4 * R.EPS
     R.assert_near(got.grad[some], want.grad(g)[some], grad_tolerance(want, g, torch.float32, delta)[some], "grad")
     assert int((got.grad != 0).any(1).sum()) == int((g != 0).sum())
+
+
+def test_masked_label_with_a_reference():
+    """A label whose own logit is -inf: its divergence is NaN and stays in kl_out unless the loss counts it."""
+    import hash_table_cache_amd as H
+
+    rows, vocab = 20, 50
+    x, y = make(rows, vocab, torch.float32, 31, special=False)
+    x[3, y[3]] = -torch.inf
+    want = R.Rows(x, y, 1.0)
+    old = want.logp.nan_to_num(0.0, 0.0, -3.0).float().to(dev())
+    ones = torch.ones(rows, device=dev())
+    got = H.policy_loss(x, y, old, ones, ones, old)
+    assert math.isnan(float(got.kl[3])) and int(got.kl.isnan().sum()) == 1
+    assert float(got.logp[3]) == -math.inf and float(got.token_loss[3]) == 0.0 and not bool(got.grad[3].any())
+    # every other ratio is 1 but for the rounding of the old log-probability, of at most 8 units
+    assert float(got.loss) == pytest.approx(-(rows - 1), rel=8 * R.EPS)
+    assert math.isnan(float(H.policy_loss(x, y, old, ones, ones, old, kl_coef=0.1).loss))
+    y[3] = -1
+    got = H.policy_loss(x, y, old, ones, ones, old, kl_coef=0.1)
+    assert float(got.loss) == pytest.approx(-(rows - 1), rel=8 * R.EPS) and not bool(got.kl.isnan().any())
