@@ -192,7 +192,9 @@ def _workspace(size, device):
 
 def token_logprobs(logits, labels, *, temperature: float = 1.0, stream=None):
     """(logp, lse), both [rows] float32: the log-probability of each row's
-    label under softmax(logits / temperature), and the normaliser."""
+    label under softmax(logits / temperature), and the normaliser. Autograd does
+    not follow them: a loss made of logp gives its gradient with respect to logp
+    to token_logprobs_backward."""
     if stream is not None:
         with _on(stream, logits.device):
             return token_logprobs(logits, labels, temperature=temperature)
@@ -211,7 +213,8 @@ def token_logprobs(logits, labels, *, temperature: float = 1.0, stream=None):
 
 def token_logprobs_backward(logits, labels, lse, grad_logp, *, temperature: float = 1.0, grad_out=None, stream=None):
     """The gradient of (grad_logp * logp).sum() with respect to the logits;
-    grad_out takes it where given (it may be the logits)."""
+    grad_out takes it where given (it may be the logits, or other columns of
+    their rows)."""
     if stream is not None:
         with _on(stream, logits.device):
             return token_logprobs_backward(logits, labels, lse, grad_logp, temperature=temperature, grad_out=grad_out)
