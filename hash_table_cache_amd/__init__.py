@@ -40,16 +40,20 @@ from ._native import (  # noqa: F401
 from .training import (
     PolicyLoss,
     PreferenceLoss,
+    TokenStats,
     clip_grad_norm,
     policy_loss,
     preference_loss,
     token_logprobs,
     token_logprobs_backward,
+    token_stats,
+    token_stats_backward,
 )
 
 __all__ = ["HashTable", "HkvError", "BUCKET_SLOTS", "EMPTY_KEY", "LOCKED_KEY", "HKV_FLAG_SERIAL_INSERT",
-           "HKV_FLAG_RW_LOCK", "HKV_FLAG_UNIQUE_KEYS", "PolicyLoss", "PreferenceLoss", "clip_grad_norm",
-           "policy_loss", "preference_loss", "token_logprobs", "token_logprobs_backward"]
+           "HKV_FLAG_RW_LOCK", "HKV_FLAG_UNIQUE_KEYS", "PolicyLoss", "PreferenceLoss", "TokenStats",
+           "clip_grad_norm", "policy_loss", "preference_loss", "token_logprobs", "token_logprobs_backward", "token_stats",
+           "token_stats_backward"]
 
 
 class HashTable:

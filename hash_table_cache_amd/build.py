@@ -28,7 +28,7 @@ MIXED_SOURCE = CSRC / "hkv_mixed_driver.cpp"
 MIXED_LIB_PATH = PKG / "_lib" / "libhkv_mixed.so"
 # the training operators (include/hkv_train.h), a library of their own: they
 # work on logits and gradients and hold no table
-TRAIN_SOURCES = [CSRC / "hkv_train_kernels.hip", CSRC / "hkv_train.cpp"]
+TRAIN_SOURCES = [CSRC / "hkv_train_kernels.hip", CSRC / "hkv_train_stats.hip", CSRC / "hkv_train.cpp"]
 TRAIN_LIB_PATH = PKG / "_lib" / "libhkv_train.so"
 ARCH = "gfx950"
 
@@ -74,7 +74,7 @@ def _compile(src: pathlib.Path, verbose: bool) -> pathlib.Path:
 def build(verbose: bool = False) -> pathlib.Path:
     BUILD_DIR.mkdir(parents=True, exist_ok=True)
     LIB_PATH.parent.mkdir(parents=True, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=5) as pool:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=8) as pool:
         futs = [pool.submit(_compile, src, verbose) for src in (*SOURCES, MIXED_SOURCE, *TRAIN_SOURCES)]
         objs = [f.result() for f in futs]
     tmp = LIB_PATH.with_suffix(".so.tmp")

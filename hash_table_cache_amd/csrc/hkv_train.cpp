@@ -243,6 +243,69 @@ HKV_API hkv_status hkv_token_logprobs_backward(uint64_t rows, uint64_t vocab, ui
   });
 }
 
+HKV_API uint64_t hkv_token_stats_workspace_bytes(uint64_t rows, uint64_t vocab, uint32_t dtype, uint32_t k) {
+  if (rows >= (1ull << 31) || vocab >= (1ull << 29) || dtype > hkvt::kF16 || k > hkvt::kMostTops) return 0;
+  hkvt::Logits l{};
+  l.rows = (uint32_t)rows;
+  l.vocab = (uint32_t)vocab;
+  l.kind = dtype;
+  return hkvt::stats_workspace_bytes(l, k);
+}
+
+HKV_API hkv_status hkv_token_stats(uint64_t rows, uint64_t vocab, uint32_t dtype, const void* logits,
+                                   uint64_t logits_stride, const int64_t* labels, float temperature, uint32_t k,
+                                   float* logp_out, float* lse_out, float* entropy_out, float* top_logp_out,
+                                   int64_t* top_ids_out, void* workspace, uint64_t workspace_bytes,
+                                   hipStream_t stream) {
+  return guarded([&]() -> hkv_status {
+    hkvt::Logits l;
+    Buffers buffers;
+    if (k > hkvt::kMostTops) return fail(HKV_EINVAL, "k = %u, the limit is %u", k, hkvt::kMostTops);
+    HKV_TRY(check_logits(buffers, rows, vocab, dtype, logits, logits_stride, labels, temperature, nullptr, 0, &l));
+    if (rows == 0) return HKV_OK;
+    HKV_TRY(buffers.check(logp_out, rows * 4, "logp_out"));
+    if (lse_out) HKV_TRY(buffers.check(lse_out, rows * 4, "lse_out"));
+    HKV_TRY(buffers.check(entropy_out, rows * 4, "entropy_out"));
+    if (k) {
+      HKV_TRY(buffers.check(top_logp_out, rows * k * 4, "top_logp_out"));
+      HKV_TRY(buffers.check(top_ids_out, rows * k * 8, "top_ids_out"));
+    }
+    const uint64_t need = hkvt::stats_workspace_bytes(l, k);
+    if (need) HKV_TRY(check_workspace(buffers, workspace, workspace_bytes, need));
+    DeviceGuard dg(buffers.device());
+    if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
+    const hkvt::Stats out{logp_out, lse_out, entropy_out, top_logp_out, top_ids_out, k};
+    const hipError_t e = hkvt::launch_stats(l, out, workspace, stream);
+    return e == hipSuccess ? HKV_OK : fail_hip(e, "hkv_token_stats launch");
+  });
+}
+
+HKV_API hkv_status hkv_token_stats_backward(uint64_t rows, uint64_t vocab, uint32_t dtype, const void* logits,
+                                            uint64_t logits_stride, const int64_t* labels, float temperature,
+                                            const float* lse, const float* entropy, const float* grad_logp,
+                                            const float* grad_entropy, void* grad_out, uint64_t grad_stride,
+                                            hipStream_t stream) {
+  return guarded([&]() -> hkv_status {
+    hkvt::Logits l;
+    Buffers buffers;
+    if (!grad_out && rows) return fail(HKV_EINVAL, "grad_out is NULL");
+    if (!grad_logp && !grad_entropy && rows) return fail(HKV_EINVAL, "grad_logp and grad_entropy are NULL");
+    HKV_TRY(check_logits(buffers, rows, vocab, dtype, logits, logits_stride, labels, temperature, grad_out,
+                         grad_stride, &l));
+    if (rows == 0) return HKV_OK;
+    HKV_TRY(buffers.check(lse, rows * 4, "lse"));
+    if (grad_logp) HKV_TRY(buffers.check(grad_logp, rows * 4, "grad_logp"));
+    if (grad_entropy) {
+      HKV_TRY(buffers.check(grad_entropy, rows * 4, "grad_entropy"));
+      HKV_TRY(buffers.check(entropy, rows * 4, "entropy"));
+    }
+    DeviceGuard dg(buffers.device());
+    if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
+    const hipError_t e = hkvt::launch_stats_backward(l, lse, entropy, grad_logp, grad_entropy, stream);
+    return e == hipSuccess ? HKV_OK : fail_hip(e, "hkv_token_stats_backward launch");
+  });
+}
+
 HKV_API hkv_status hkv_preference_loss(uint64_t rows, uint64_t vocab, uint32_t dtype, const void* logits,
                                        uint64_t logits_stride, const int64_t* labels, float temperature,
                                        uint64_t pairs, const int64_t* cu_seqlens, const float* ref_logp, float beta,

@@ -61,6 +61,18 @@ struct Policy {
   float* logp;
 };
 
+// Statistics of rows: [rows] each, and [rows][k] for the largest logits.
+struct Stats {
+  float* logp;
+  float* lse;
+  float* entropy;
+  float* top_logp;
+  int64_t* top_ids;
+  uint32_t k;
+};
+
+constexpr uint32_t kMostTops = 64;  // a lane each
+
 // One gradient tensor: `n` elements of `kind` at `in`, the product goes to `out`.
 struct Tensor {
   const void* in;
@@ -77,6 +89,11 @@ uint64_t logprobs_workspace_bytes(const Logits& l);
 
 hipError_t launch_logprobs(const Logits& l, float* logp, float* lse, void* ws, hipStream_t s);
 hipError_t launch_backward(const Logits& l, const float* lse, const float* g, hipStream_t s);
+// 0 unless workgroups share the rows.
+uint64_t stats_workspace_bytes(const Logits& l, uint32_t k);
+hipError_t launch_stats(const Logits& l, const Stats& out, void* ws, hipStream_t s);
+hipError_t launch_stats_backward(const Logits& l, const float* lse, const float* entropy, const float* g,
+                                 const float* ge, hipStream_t s);
 hipError_t launch_preference(const Logits& l, const Pairs& p, void* ws, hipStream_t s);
 hipError_t launch_policy(const Logits& l, const Policy& p, void* ws, hipStream_t s);
 

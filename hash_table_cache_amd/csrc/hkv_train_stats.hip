@@ -1,0 +1,616 @@
+// gfx950 kernels of the token statistics (include/hkv_train.h): log-probability,
+// entropy and the k largest logits of each row, and the gradient through the
+// first two.
+//
+// Row mathematics. With M the row's maximum, a_v = (M - x_v) / tau >= 0,
+// S = sum over v != y of e^-a_v and W = sum over v != y of a_v e^-a_v:
+//   T = S + e^-a_y,  logp = -a_y - log T,  H = log T + (W + a_y e^-a_y) / T.
+// Both terms of H are sums of what is not negative, so nothing cancels where a
+// row is nearly certain; the label stays out of the sums for the same reason as
+// in token_logprobs. A row is read once: S and W are rescaled when a larger
+// maximum comes, and the k largest elements are kept beside them.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "hkv_train_internal.h"
+#include "hkv_train_rows.h"
+
+namespace hkvt {
+namespace {
+
+constexpr float kLn2 = 0.69314718055994530942f;
+
+// Running maximum and sums of the elements a thread has seen; w is in units of
+// log 2, as the exponents are.
+struct Spread {
+  float m = -kInf;
+  double s = 0.0, w = 0.0;
+
+  // Takes the sums to a new base, `t` = (old - new) / tau in units of log 2.
+  __device__ __forceinline__ void rescale(float t) {
+    const double f = exp2_fast(t);
+    w = f == 0.0 ? 0.0 : f * (w - s * (double)t);
+    s *= f;
+  }
+
+  __device__ __forceinline__ void raise(float mx, const Scale& c) {
+    if (__any(mx > m)) {
+      const float top = fmaxf(m, mx);
+      const float t = top == -kInf ? 0.0f : m - top;
+      rescale(fmaf(t, c.k_hi, t * c.k_lo));
+      m = top;
+    }
+  }
+
+  // N elements, none above m. Up to F of them are added in 32 bits.
+  template <int N, int F>
+  __device__ __forceinline__ void sum(const float* f, const Scale& c) {
+    const float base = m == -kInf ? 0.0f : m;
+    float e[N], a[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float t = f[i] - base, z = fmaf(t, c.k_hi, t * c.k_lo);
+      e[i] = exp2_fast(z);
+      a[i] = e[i] * fminf(-z, 1024.0f);  // a masked element has no weight, nor an infinite distance
+    }
+    constexpr int G = N < F ? N : F;
+#pragma unroll
+    for (int i = 0; i < N; i += G) {
+#pragma unroll
+      for (int w = G / 2; w > 0; w /= 2)
+#pragma unroll
+        for (int j = 0; j < w; ++j) {
+          e[i + j] += e[i + j + w];
+          a[i + j] += a[i + j + w];
+        }
+      s += (double)e[i];
+      w += (double)a[i];
+    }
+  }
+};
+
+// Joins a wave's lanes, whose largest maximum is `top`; every lane gets the sums.
+__device__ __forceinline__ void join_lanes(Spread& r, float top, const Scale& c) {
+  const float base = top == -kInf ? 0.0f : top;
+  const float t = r.m - base;
+  r.rescale(fmaf(t, c.k_hi, t * c.k_lo));
+  r.m = top;
+#pragma unroll
+  for (int w = 32; w > 0; w /= 2) {
+    r.s += __shfl_xor(r.s, w);
+    r.w += __shfl_xor(r.w, w);
+  }
+}
+
+__device__ __forceinline__ float max_lanes(float v) {
+#pragma unroll
+  for (int w = 32; w > 0; w /= 2) v = fmaxf(v, __shfl_xor(v, w));
+  return v;
+}
+
+struct StatsEnd {
+  double logp, lse, entropy;
+  bool counts;  // false: the row is left out
+};
+
+// (M, S, W, x_y) -> log-probability, normaliser and entropy.
+__device__ __forceinline__ StatsEnd finish_stats(const Spread& r, float xy, double inv_tau) {
+  if (r.m == -kInf && xy == -kInf && r.s == 0.0) return StatsEnd{0.0, -(double)kInf, 0.0, false};
+  StatsEnd e;
+  e.counts = true;
+  double d = ((double)xy - (double)r.m) * inv_tau;
+  if (xy == kInf) d = __builtin_nan("");
+  const double w = r.w * 0.69314718055994530942;
+  if (d >= 0.0) {
+    const double f = exp_of(-d), er = r.s * f, lt = log1p_of(er);
+    e.logp = -lt;
+    e.lse = (double)xy * inv_tau + lt;
+    e.entropy = lt + (f == 0.0 ? 0.0 : f * (w + r.s * d)) / (1.0 + er);
+  } else {
+    const double f = exp_of(d), total = r.s + f, lt = log_of(total);
+    e.logp = d - lt;
+    e.lse = (double)r.m * inv_tau + lt;
+    e.entropy = lt + (f == 0.0 ? w : w - f * d) / total;
+  }
+  if (e.entropy < 0.0) e.entropy = 0.0;
+  return e;
+}
+
+__device__ __forceinline__ StatsEnd nan_stats() {
+  const double q = __builtin_nan("");
+  return StatsEnd{q, q, q, true};
+}
+
+// The largest elements. An element is a key of 64 bits that sorts as they do:
+// its value in order, and under it the index, lower ones above. 0 is no element.
+typedef unsigned long long Key;
+
+__device__ __forceinline__ Key key_of(float f, uint32_t i) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, f + 0.0f);  // -0 is 0
+  return (Key)(u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) << 32 | (uint32_t)~i;
+}
+
+__device__ __forceinline__ float value_of(Key k) {
+  const uint32_t u = (uint32_t)(k >> 32);
+  return as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+
+__device__ __forceinline__ uint32_t index_of(Key k) { return ~(uint32_t)k; }
+
+// The lanes' values sorted downwards within blocks of SIZE lanes from blocks
+// that go up and down: the steps of a bitonic sort.
+template <typename V, int SIZE>
+__device__ __forceinline__ V sort_step(V v, bool down, int lane) {
+#pragma unroll
+  for (int w = SIZE / 2; w > 0; w /= 2) {
+    const V o = __shfl_xor(v, w);
+    v = (((lane & w) == 0) == down) == (v > o) ? v : o;
+  }
+  return v;
+}
+
+template <typename V>
+__device__ __forceinline__ V sort_lanes(V v, int lane) {
+  v = sort_step<V, 2>(v, (lane & 2) == 0, lane);
+  v = sort_step<V, 4>(v, (lane & 4) == 0, lane);
+  v = sort_step<V, 8>(v, (lane & 8) == 0, lane);
+  v = sort_step<V, 16>(v, (lane & 16) == 0, lane);
+  v = sort_step<V, 32>(v, (lane & 32) == 0, lane);
+  return sort_step<V, 64>(v, true, lane);
+}
+
+// The 64 largest of two sorted lists. `other` comes in reverse.
+__device__ __forceinline__ Key merge_lanes(Key v, Key other, int lane) {
+  return sort_step<Key, 64>(v > other ? v : other, true, lane);
+}
+
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The k <= 64 largest elements that a wave has seen, sorted, one a lane, and a
+// bound under which no element comes among them. Elements that pass the bound
+// are gathered in LDS and join the list 64 at a time. N: how many may be added
+// before the list takes them.
+template <int N>
+struct Tops {
+  static constexpr int kHeld = N + 64;
+  Key list = 0;
+  float bound = -kInf;      // an element of this value passes
+  uint32_t bound_at = 0;    // if its index is lower
+  uint32_t count = 0;       // gathered
+  Key* held;
+  uint32_t k;
+  int lane;
+
+  __device__ __forceinline__ Tops(Key* lds, uint32_t k_) : held(lds), k(k_), lane(threadIdx.x & 63) {}
+
+  // A bound from the lanes' maxima of what comes next: k lanes have an element
+  // of at least the k-th largest of them.
+  __device__ __forceinline__ void expect(float mx) {
+    if (__popcll(__ballot(mx > bound)) < 16 && bound > -kInf) return;
+    const float v = sort_lanes(mx, lane);
+    const float at = __shfl(v, (int)k - 1);
+    if (at > bound) {
+      bound = at;
+      bound_at = ~0u;
+    }
+  }
+
+  __device__ __forceinline__ bool passes(float f, uint32_t i) const {
+    return f > bound || (f == bound && i < bound_at);
+  }
+
+  __device__ __forceinline__ void add(float f, uint32_t i, bool live) {
+    const bool in = live && passes(f, i);
+    const uint64_t who = __ballot(in);
+    if (who == 0) return;
+    const uint32_t below = __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+    if (in) held[count + below] = key_of(f, i);
+    count += __popcll(who);
+  }
+
+  // Joins the last 64 gathered ones, or all of fewer.
+  __device__ __forceinline__ void take() {
+    const uint32_t n = min(count, 64u);
+    count -= n;
+    wave_sync();
+    Key v = (uint32_t)lane < n ? held[count + lane] : 0;
+    v = sort_lanes(v, lane);
+    list = merge_lanes(list, __shfl(v, 63 - lane), lane);
+    const Key last = __shfl(list, (int)k - 1);
+    if (last) {
+      const float at = value_of(last);
+      if (at >= bound) {  // not below what expect() found
+        bound_at = at > bound ? index_of(last) : min(bound_at, index_of(last));
+        bound = at;
+      }
+    }
+    wave_sync();
+  }
+};
+
+struct StatsArgs {
+  Logits l;
+  Scale c;
+  Stats out;
+  uint32_t first;  // row of the first team
+};
+
+// Writes a row's results: `lane` of its first wave, with the row's list.
+__device__ __forceinline__ void write_stats(const StatsArgs& a, uint32_t t, const StatsEnd& e, Key list, int lane) {
+  if (lane == 0) {
+    a.out.logp[t] = (float)e.logp;
+    if (a.out.lse) a.out.lse[t] = (float)e.lse;
+    a.out.entropy[t] = (float)e.entropy;
+  }
+  if ((uint32_t)lane < a.out.k) {
+    const bool lives = list != 0 && e.lse == e.lse;
+    const double v = lives ? (double)value_of(list) * a.c.inv_tau - e.lse : e.lse == e.lse ? -(double)kInf : e.lse;
+    a.out.top_logp[(uint64_t)t * a.out.k + lane] = (float)v;
+    a.out.top_ids[(uint64_t)t * a.out.k + lane] = lives ? (int64_t)index_of(list) : -1;
+  }
+}
+
+// One row, or a part of it, by a team: sums in r, the largest in the waves' lists.
+template <typename T, int NT, int NV, bool TOP>
+__device__ __forceinline__ void scan_row(const T* row, const Cut<T, NT>& cut, uint32_t y, uint32_t tid, const Scale& c,
+                                         Spread& r, Tops<64 * Io<T>::K>& tops) {
+  constexpr int K = Io<T>::K;
+  const T* vecs = row + cut.head;
+  const uint32_t yv = cut.vec_of(y), el = (y - cut.head) % K;
+  for (uint32_t c0 = cut.begin; c0 < cut.end; c0 += NT * NV) {
+    u32x4 raw[NV];
+    float mx[NV], most = -kInf;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      raw[i] = no_vec<T>();
+      if (c0 + i * NT + tid < cut.end) raw[i] = load_vec(vecs, c0 + i * NT + tid);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      mx[i] = vec_max<T>(raw[i]);
+      most = fmaxf(most, mx[i]);
+    }
+    r.raise(most, c);
+    if (TOP) tops.expect(most);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      opaque(raw[i]);
+      const uint32_t v = c0 + i * NT + tid;
+      if (c0 + i * NT < cut.end) {
+        float f[K];
+        Io<T>::unpack(raw[i], f);
+        if (__any(v == yv)) {
+#pragma unroll
+          for (int j = 0; j < K; ++j)
+            if (v == yv && el == (uint32_t)j) f[j] = -kInf;
+        }
+        r.sum<K, Io<T>::kFloats>(f, c);
+      }
+    }
+    if (TOP) {
+      uint32_t some = 0;  // vectors in which some lane's maximum may pass
+#pragma unroll
+      for (int i = 0; i < NV; ++i) some |= __any(mx[i] >= tops.bound && mx[i] > -kInf) ? 1u << i : 0u;
+      while (some) {
+        const int at = __builtin_ctz(some);
+        some &= some - 1;
+        u32x4 x = raw[0];
+#pragma unroll
+        for (int i = 1; i < NV; ++i)
+          if (at == i) x = raw[i];
+        float f[K];
+        Io<T>::unpack(x, f);
+        const uint32_t v = c0 + at * NT + tid, base = cut.head + v * K;
+#pragma unroll
+        for (int j = 0; j < K; ++j) tops.add(f[j], base + j, v < cut.end);
+        while (tops.count >= 64) tops.take();
+      }
+    }
+  }
+  for (uint32_t j0 = 0; j0 < cut.singles(); j0 += NT) {
+    const uint32_t j = j0 + tid, i = cut.single(j);
+    float f = j < cut.singles() ? (float)row[i] : -kInf;
+    if (TOP) {
+      tops.add(f, i, j < cut.singles());
+      while (tops.count >= 64) tops.take();
+    }
+    if (i == y) f = -kInf;
+    r.raise(f, c);
+    r.sum<1, 1>(&f, c);
+  }
+  if (TOP)
+    while (tops.count) tops.take();
+}
+
+template <int NT, bool TOP, int HELD>
+struct StatsShared {
+  static constexpr int kWaves = Team<NT>::kBlock / 64;
+  float m[kWaves];
+  double s[kWaves], w[kWaves];
+  Key held[TOP ? kWaves : 1][TOP ? HELD : 1];
+};
+
+// Joins the waves of a team; the first wave gets it all.
+template <int NT, bool TOP, typename Sh>
+__device__ __forceinline__ void join_waves(Spread& r, Key& list, const Scale& c, Sh& sh) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const float top = max_lanes(r.m);
+  join_lanes(r, top, c);
+  if (NT == 64) return;
+  constexpr int W = NT / 64;
+  if (lane == 0) {
+    sh.m[wave] = r.m;
+    sh.s[wave] = r.s;
+    sh.w[wave] = r.w;
+  }
+  if (TOP) sh.held[wave][lane] = list;
+  __syncthreads();
+  if (TOP) {
+#pragma unroll
+    for (int n = W / 2; n > 0; n /= 2) {
+      if (wave < n) {
+        list = merge_lanes(list, sh.held[wave + n][63 - lane], lane);
+        if (n > 1) sh.held[wave][lane] = list;
+      }
+      if (n > 1) __syncthreads();
+    }
+  }
+  if (wave == 0) {
+    r.m = lane < W ? sh.m[lane] : -kInf;
+    r.s = lane < W ? sh.s[lane] : 0.0;
+    r.w = lane < W ? sh.w[lane] : 0.0;
+    join_lanes(r, max_lanes(r.m), c);  // every lane gets it
+  }
+}
+
+template <typename T, int NT, int NV, bool TOP>
+__global__ __launch_bounds__(Team<NT>::kBlock) void stats_kernel(const StatsArgs a) {
+  using Tm = Team<NT>;
+  constexpr int N = 64 * Io<T>::K;
+  __shared__ StatsShared<NT, TOP, Tops<N>::kHeld> sh;
+  const uint32_t tid = Tm::thread(), t = Tm::row(a.first, blockIdx.x);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (t >= a.l.rows) return;  // a whole team
+  const T* row = static_cast<const T*>(a.l.x) + (uint64_t)t * a.l.x_stride;
+  const int64_t y64 = a.l.labels[t];
+  StatsEnd e;
+  Key list = 0;
+  if (y64 < 0) {
+    e = StatsEnd{0.0, 0.0, 0.0, false};
+  } else if (y64 >= (int64_t)a.l.vocab) {
+    e = nan_stats();
+  } else {
+    const float xy = (float)row[y64];
+    const Cut<T, NT> cut(row, a.l.vocab);
+    Spread r;
+    Tops<N> tops(TOP ? sh.held[wave] : nullptr, a.out.k);
+    scan_row<T, NT, NV, TOP>(row, cut, (uint32_t)y64, tid, a.c, r, tops);
+    list = tops.list;
+    join_waves<NT, TOP>(r, list, a.c, sh);
+    e = finish_stats(r, xy, a.c.inv_tau);
+  }
+  if (tid < 64) write_stats(a, t, e, list, lane);
+}
+
+// Few long rows: a row is shared by workgroups, whose sums and lists one joins.
+struct StatsPartial {
+  double s, w;
+  float m;
+};
+
+constexpr uint32_t kStatsParts = 64;
+
+template <typename T, bool TOP>
+__global__ __launch_bounds__(256) void stats_part_kernel(const StatsArgs a, uint32_t parts, uint32_t size,
+                                                         StatsPartial* partial, Key* lists) {
+  constexpr int NT = 256, NV = 4, N = 64 * Io<T>::K;
+  __shared__ StatsShared<NT, TOP, Tops<N>::kHeld> sh;
+  const uint32_t tid = threadIdx.x, t = blockIdx.x / parts;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t y64 = a.l.labels[t];
+  if (y64 < 0 || y64 >= (int64_t)a.l.vocab) return;
+  const T* row = static_cast<const T*>(a.l.x) + (uint64_t)t * a.l.x_stride;
+  const Cut<T, NT> cut(row, a.l.vocab, blockIdx.x % parts, size);
+  Spread r;
+  Tops<N> tops(TOP ? sh.held[wave] : nullptr, a.out.k);
+  scan_row<T, NT, NV, TOP>(row, cut, (uint32_t)y64, tid, a.c, r, tops);
+  Key list = tops.list;
+  join_waves<NT, TOP>(r, list, a.c, sh);
+  if (tid == 0) partial[blockIdx.x] = StatsPartial{r.s, r.w, r.m};
+  if (TOP && tid < 64) lists[(uint64_t)blockIdx.x * 64 + lane] = list;
+}
+
+template <typename T, bool TOP>
+__global__ __launch_bounds__(512) void stats_join_kernel(const StatsArgs a, uint32_t parts, const StatsPartial* partial,
+                                                         const Key* lists) {
+  constexpr int W = 8;
+  __shared__ Key held[W][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t t = blockIdx.x;
+  const int64_t y64 = a.l.labels[t];
+  const bool reads = y64 >= 0 && y64 < (int64_t)a.l.vocab;
+  Key list = 0;
+  if (TOP && reads) {
+    for (uint32_t p = wave; p < parts; p += W)
+      list = merge_lanes(list, lists[((uint64_t)t * parts + p) * 64 + 63 - lane], lane);
+    held[wave][lane] = list;
+    __syncthreads();
+#pragma unroll
+    for (int n = W / 2; n > 0; n /= 2) {
+      if (wave < n) {
+        list = merge_lanes(list, held[wave + n][63 - lane], lane);
+        held[wave][lane] = list;
+      }
+      __syncthreads();
+    }
+  }
+  if (wave) return;
+  StatsEnd e;
+  if (y64 < 0) {
+    e = StatsEnd{0.0, 0.0, 0.0, false};
+  } else if (!reads) {
+    e = nan_stats();
+  } else {
+    Spread r;
+    if ((uint32_t)lane < parts) {
+      const StatsPartial p = partial[t * parts + lane];
+      r.s = p.s;
+      r.w = p.w;
+      r.m = p.m;
+    }
+    join_lanes(r, max_lanes(r.m), a.c);
+    e = finish_stats(r, (float)(static_cast<const T*>(a.l.x) + (uint64_t)t * a.l.x_stride)[y64], a.c.inv_tau);
+  }
+  write_stats(a, t, e, list, lane);
+}
+
+// The gradient: -p / tau (g + h (log p + H)), and g / tau more at the label.
+struct StatsBack {
+  Logits l;
+  Scale c;
+  const float* lse;
+  const float* entropy;
+  const float* g;
+  const float* ge;
+};
+
+__device__ __forceinline__ float back_of(float x, const Scale& c, float lse, float h, float g, float ge) {
+  float z = exponent(x, c, lse);
+  z = z < -1024.0f ? -1024.0f : z;  // a masked element has no weight, nor an infinite distance
+  return exp2_fast(z * kLog2e) * fmaf(-ge, z + h, -g);
+}
+
+template <typename T>
+__device__ __forceinline__ u32x4 back_vec(u32x4 raw, const Scale& c, float lse, float h, float g, float ge) {
+  constexpr int K = Io<T>::K;
+  float f[K];
+  Io<T>::unpack(raw, f);
+#pragma unroll
+  for (int i = 0; i < K; ++i) f[i] = back_of(f[i], c, lse, h, g, ge);
+  return Io<T>::pack(f);
+}
+
+template <typename T, int NT>
+__global__ __launch_bounds__(Team<NT>::kBlock) void stats_backward_kernel(const StatsBack a, uint32_t parts, uint32_t first) {
+  using Tm = Team<NT>;
+  const uint32_t tid = Tm::thread(), t = Tm::row(first, blockIdx.x / parts);
+  if (t >= a.l.rows) return;
+  const T* row = static_cast<const T*>(a.l.x) + (uint64_t)t * a.l.x_stride;
+  T* out = static_cast<T*>(a.l.dx) + (uint64_t)t * a.l.dx_stride;
+  const Cut<T, NT> cut(out, a.l.vocab, blockIdx.x % parts, Part<NT>::kVecs);
+  const int64_t y64 = a.l.labels[t];
+  const float lse = a.lse[t];
+  float g = a.g ? (float)(a.g[t] * a.c.inv_tau) : 0.0f;
+  const float ge = a.ge ? (float)(a.ge[t] * a.c.inv_tau) : 0.0f;
+  const float h = ge == 0.0f ? 0.0f : a.entropy[t];
+  if (y64 < 0 || lse == -kInf || (g == 0.0f && ge == 0.0f)) {
+    zero_row<T, NT>(out, cut, tid);
+    return;
+  }
+  if (y64 >= (int64_t)a.l.vocab) g = __builtin_nanf("");
+  const uint32_t y = y64 >= (int64_t)a.l.vocab ? 0u : (uint32_t)y64;
+  // the label's thread, the only one that writes its place, reads it first
+  const uint32_t owner = cut.owner(y);
+  const float fy = tid == owner ? (float)row[y] : 0.0f;
+  for_vecs<T, NT, Part<NT>::kRounds>(row + cut.head, cut.begin, cut.end, tid, [&](u32x4 raw, uint32_t v) {
+    store_vec(out + cut.head, v, back_vec<T>(raw, a.c, lse, h, g, ge));
+  });
+  for (uint32_t j = tid; j < cut.singles(); j += NT) {
+    const uint32_t i = cut.single(j);
+    out[i] = (T)back_of((float)row[i], a.c, lse, h, g, ge);
+  }
+  if (tid == owner)
+    out[y] = (T)(float)((double)g * rest_of_label(fy, a.c, lse) + (double)back_of(fy, a.c, lse, h, 0.0f, ge));
+}
+
+template <typename T, int NT, int NV>
+hipError_t stats_n(const StatsArgs& a, hipStream_t s) {
+  return for_rows<NT>(a.l.rows, 1, [&](uint32_t first, uint32_t grid) {
+    StatsArgs slice = a;
+    slice.first = first;
+    if (a.out.k)
+      stats_kernel<T, NT, NV, true><<<grid, Team<NT>::kBlock, 0, s>>>(slice);
+    else
+      stats_kernel<T, NT, NV, false><<<grid, Team<NT>::kBlock, 0, s>>>(slice);
+  });
+}
+
+bool shared_stats(const Logits& l) {
+  return l.rows < kSharedRows && l.vocab / (l.kind == kF32 ? 4 : 8) > 256 * 4;
+}
+
+uint32_t stats_parts(const Logits& l) { return std::min(l.vocab / (l.kind == kF32 ? 4 : 8) / 512, kStatsParts); }
+
+template <typename T>
+hipError_t stats_t(const StatsArgs& a, void* ws, hipStream_t s) {
+  const uint32_t nv = a.l.vocab / Io<T>::K;
+  if (shared_stats(a.l)) {
+    const uint32_t parts = stats_parts(a.l), size = (nv - 1) / parts + 1;
+    Workspace w{static_cast<char*>(ws)};
+    StatsPartial* partial = w.take<StatsPartial>((uint64_t)a.l.rows * parts);
+    Key* lists = w.take<Key>(a.out.k ? (uint64_t)a.l.rows * parts * 64 : 0);
+    const uint32_t grid = a.l.rows * parts;
+    if (a.out.k)
+      stats_part_kernel<T, true><<<grid, 256, 0, s>>>(a, parts, size, partial, lists);
+    else
+      stats_part_kernel<T, false><<<grid, 256, 0, s>>>(a, parts, size, partial, lists);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (a.out.k)
+      stats_join_kernel<T, true><<<a.l.rows, 512, 0, s>>>(a, parts, partial, lists);
+    else
+      stats_join_kernel<T, false><<<a.l.rows, 512, 0, s>>>(a, parts, partial, lists);
+    return hipGetLastError();
+  }
+  if (nv <= 64 * 4) return stats_n<T, 64, 4>(a, s);
+  if (nv <= 256 * 4) return stats_n<T, 256, 4>(a, s);
+  return stats_n<T, 512, 8>(a, s);
+}
+
+template <typename T, int NT>
+hipError_t stats_backward_n(const StatsBack& a, hipStream_t s) {
+  const uint32_t parts = Part<NT>::parts(a.l.vocab / Io<T>::K);
+  return for_rows<NT>(a.l.rows, parts, [&](uint32_t first, uint32_t grid) {
+    stats_backward_kernel<T, NT><<<grid, Team<NT>::kBlock, 0, s>>>(a, parts, first);
+  });
+}
+
+// Teams as in the gradient of the log-probabilities, which moves the same bytes.
+template <typename T>
+hipError_t stats_backward_t(const StatsBack& a, hipStream_t s) {
+  const uint32_t nv = a.l.vocab / Io<T>::K;
+  if (nv <= 16 * 4) return stats_backward_n<T, 16>(a, s);
+  if (nv <= 64 * 8) return stats_backward_n<T, 64>(a, s);
+  return stats_backward_n<T, 128>(a, s);
+}
+
+}  // namespace
+
+uint64_t stats_workspace_bytes(const Logits& l, uint32_t k) {
+  if (!shared_stats(l)) return 0;
+  const uint64_t n = (uint64_t)l.rows * stats_parts(l);
+  return up16(n * sizeof(StatsPartial)) + (k ? n * 64 * sizeof(Key) : 0);
+}
+
+hipError_t launch_stats(const Logits& l, const Stats& out, void* ws, hipStream_t s) {
+  const StatsArgs a{l, make_scale(l.tau), out, 0};
+  if (l.kind == kF32) return stats_t<float>(a, ws, s);
+  if (l.kind == kBF16) return stats_t<__bf16>(a, ws, s);
+  return stats_t<_Float16>(a, ws, s);
+}
+
+hipError_t launch_stats_backward(const Logits& l, const float* lse, const float* entropy, const float* g,
+                                 const float* ge, hipStream_t s) {
+  const StatsBack a{l, make_scale(l.tau), lse, entropy, g, ge};
+  if (l.kind == kF32) return stats_backward_t<float>(a, s);
+  if (l.kind == kBF16) return stats_backward_t<__bf16>(a, s);
+  return stats_backward_t<_Float16>(a, s);
+}
+
+}  // namespace hkvt

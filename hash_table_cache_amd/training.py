@@ -34,6 +34,9 @@ EXPORTS = (
     "hkv_train_workspace_bytes",
     "hkv_token_logprobs",
     "hkv_token_logprobs_backward",
+    "hkv_token_stats_workspace_bytes",
+    "hkv_token_stats",
+    "hkv_token_stats_backward",
     "hkv_preference_loss",
     "hkv_policy_loss",
     "hkv_clip_grad_norm",
@@ -41,6 +44,14 @@ EXPORTS = (
 )
 
 KINDS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class TokenStats(NamedTuple):
+    logp: torch.Tensor  # [rows] float32
+    lse: torch.Tensor  # [rows] float32
+    entropy: torch.Tensor  # [rows] float32
+    top_logp: torch.Tensor  # [rows, k] float32, falling
+    top_ids: torch.Tensor  # [rows, k] int64, -1 past a row's last candidate
 
 
 class PreferenceLoss(NamedTuple):
@@ -73,6 +84,12 @@ def _load() -> ctypes.CDLL:
     L.hkv_token_logprobs.restype = st
     L.hkv_token_logprobs_backward.argtypes = [*logits, vp, vp, vp, u64, vp]
     L.hkv_token_logprobs_backward.restype = st
+    L.hkv_token_stats_workspace_bytes.argtypes = [u64, u64, u32, u32]
+    L.hkv_token_stats_workspace_bytes.restype = u64
+    L.hkv_token_stats.argtypes = [*logits, u32, vp, vp, vp, vp, vp, vp, u64, vp]
+    L.hkv_token_stats.restype = st
+    L.hkv_token_stats_backward.argtypes = [*logits, vp, vp, vp, vp, vp, u64, vp]
+    L.hkv_token_stats_backward.restype = st
     L.hkv_preference_loss.argtypes = [*logits, u64, vp, vp, f32, f32, f32, vp, vp, vp, vp, vp, u64, vp, u64, vp]
     L.hkv_preference_loss.restype = st
     L.hkv_policy_loss.argtypes = [*logits, vp, vp, vp, vp, f32, f32, f32, f32, vp, vp, vp, vp, vp, u64, vp, u64, vp]
@@ -226,6 +243,63 @@ def token_logprobs_backward(logits, labels, lse, grad_logp, *, temperature: floa
     _check(load().hkv_token_logprobs_backward(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride,
                                               labels.data_ptr(), temperature, z, g, grad_out.data_ptr(), gstride,
                                               _current_stream(dev)))
+    return grad_out
+
+
+@functools.lru_cache(maxsize=256)
+def _stats_workspace_bytes(rows, vocab, kind, k):
+    return load().hkv_token_stats_workspace_bytes(rows, vocab, kind, k)
+
+
+def token_stats(logits, labels, k: int = 0, *, temperature: float = 1.0, stream=None) -> TokenStats:
+    """token_logprobs with the entropy of each row's distribution and its k
+    largest logits (k <= 64), as log-probabilities with their indices, the
+    lowest index first among equal ones. Masked logits (-inf) are no
+    alternatives: past a row's last candidate, and in rows that are left out,
+    top_ids is -1 and top_logp -inf."""
+    if stream is not None:
+        with _on(stream, logits.device):
+            return token_stats(logits, labels, k, temperature=temperature)
+    rows, vocab, stride = _logits(logits, labels)
+    k = operator.index(k)
+    if not 0 <= k <= 64:
+        raise ValueError(f"k = {k} is outside 0 .. 64")
+    dev, kind = logits.device, KINDS[logits.dtype]
+    logp, lse, entropy = _floats(rows, dev), _floats(rows, dev), _floats(rows, dev)
+    top_logp = _floats((rows, k), dev)
+    top_ids = torch.empty((rows, k), dtype=torch.int64, device=dev)
+    nb = _stats_workspace_bytes(rows, vocab, kind, k)
+    ws = _workspace(nb, dev) if nb else None
+    _check(load().hkv_token_stats(rows, vocab, kind, logits.data_ptr(), stride, labels.data_ptr(), temperature, k,
+                                  logp.data_ptr(), lse.data_ptr(), entropy.data_ptr(), top_logp.data_ptr(),
+                                  top_ids.data_ptr(), ws if ws is None else ws.data_ptr(), nb, _current_stream(dev)))
+    return TokenStats(logp, lse, entropy, top_logp, top_ids)
+
+
+def token_stats_backward(logits, labels, lse, entropy=None, grad_logp=None, grad_entropy=None, *,
+                         temperature: float = 1.0, grad_out=None, stream=None):
+    """The gradient of (grad_logp * logp).sum() + (grad_entropy *
+    entropy).sum() with respect to the logits. lse and entropy are
+    token_stats's; one of the two gradients may be left out, and without
+    grad_entropy entropy too. grad_out as in token_logprobs_backward."""
+    if stream is not None:
+        with _on(stream, logits.device):
+            return token_stats_backward(logits, labels, lse, entropy, grad_logp, grad_entropy,
+                                        temperature=temperature, grad_out=grad_out)
+    rows, vocab, stride = _logits(logits, labels)
+    dev = logits.device
+    if grad_logp is None and grad_entropy is None:
+        raise ValueError("grad_logp or grad_entropy is required")
+    z = _vector(lse, torch.float32, rows, "lse", dev)
+    g = None if grad_logp is None else _vector(grad_logp, torch.float32, rows, "grad_logp", dev)
+    h = ge = None
+    if grad_entropy is not None:
+        ge = _vector(grad_entropy, torch.float32, rows, "grad_entropy", dev)
+        h = _vector(entropy, torch.float32, rows, "entropy", dev)
+    grad_out, gstride = _grad(logits, grad_out)
+    _check(load().hkv_token_stats_backward(rows, vocab, KINDS[logits.dtype], logits.data_ptr(), stride,
+                                           labels.data_ptr(), temperature, z, h, g, ge, grad_out.data_ptr(), gstride,
+                                           _current_stream(dev)))
     return grad_out
 
 

@@ -5,6 +5,8 @@
  * Rows found in a table score candidates: logits x[t][v], one row a decision.
  * The operators turn logits and feedback into gradients and bound them:
  *   - hkv_token_logprobs / _backward: log-probability of each row's label;
+ *   - hkv_token_stats / _backward: the same with the row's entropy and its k
+ *     largest logits; gradient through log-probability and entropy;
  *   - hkv_preference_loss: loss on pairs of sequences, of which one was
  *     preferred, from the ratios to a reference; value and gradient;
  *   - hkv_policy_loss: clipped policy-gradient loss with a divergence (KL)
@@ -87,6 +89,47 @@ hkv_status hkv_token_logprobs_backward(uint64_t rows, uint64_t vocab, uint32_t d
                                        uint64_t logits_stride, const int64_t* labels, float temperature,
                                        const float* lse, const float* grad_logp, void* grad_out,
                                        uint64_t grad_stride, hipStream_t stream);
+
+/*
+ * hkv_token_stats - logp_t and lse_t, the entropy
+ *   H_t = - sum_v p_v log p_v,   p_v = exp(x[t][v] / tau - lse_t),
+ * and the k largest logits of each row as log-probabilities with their indices:
+ * in order, of equal ones (0 and -0 are equal) the lowest index first. A masked
+ * logit (-inf) is no alternative: where a row has fewer than k others, and in a
+ * row that is left out, the rest have index -1 and log-probability -inf. A row
+ * that is left out has entropy 0. A row whose results are NaN has NaN
+ * log-probabilities and indices -1.
+ *   k            0 .. 64 (more than vocab is allowed)
+ *   logp_out     [rows] float32, output
+ *   lse_out      [rows] float32, output, nullable
+ *   entropy_out  [rows] float32, output
+ *   top_logp_out [rows][k] float32, output (not looked at for k = 0)
+ *   top_ids_out  [rows][k] int64, output (not looked at for k = 0)
+ * workspace: hkv_token_stats_workspace_bytes(...) bytes, which is 0 unless few
+ * long rows are shared by workgroups; then it may be NULL.
+ */
+uint64_t hkv_token_stats_workspace_bytes(uint64_t rows, uint64_t vocab, uint32_t dtype, uint32_t k);
+hkv_status hkv_token_stats(uint64_t rows, uint64_t vocab, uint32_t dtype, const void* logits, uint64_t logits_stride,
+                           const int64_t* labels, float temperature, uint32_t k, float* logp_out, float* lse_out,
+                           float* entropy_out, float* top_logp_out, int64_t* top_ids_out, void* workspace,
+                           uint64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * hkv_token_stats_backward - gradient of sum_t g_t logp_t + h_t H_t:
+ *   dx[t][v] = (g_t ([v = y] - p_v) - h_t p_v (log p_v + H_t)) / tau,
+ * with log p_v = min(x[t][v] / tau - lse_t, 1). A row whose g_t and h_t are both
+ * exactly 0 gets zeros whatever its logits are.
+ *   lse          [rows] float32, input: what hkv_token_stats gave
+ *   entropy      [rows] float32, input: what it gave (looked at with grad_entropy only)
+ *   grad_logp    [rows] float32, input, nullable (all 0): g_t
+ *   grad_entropy [rows] float32, input, nullable (all 0; one of the two is needed): h_t
+ *   grad_out     [rows][vocab] dtype, output
+ */
+hkv_status hkv_token_stats_backward(uint64_t rows, uint64_t vocab, uint32_t dtype, const void* logits,
+                                    uint64_t logits_stride, const int64_t* labels, float temperature,
+                                    const float* lse, const float* entropy, const float* grad_logp,
+                                    const float* grad_entropy, void* grad_out, uint64_t grad_stride,
+                                    hipStream_t stream);
 
 /*
  * hkv_preference_loss - sequences 2p (preferred) and 2p+1 (not preferred) are
