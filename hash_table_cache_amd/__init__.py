@@ -4,7 +4,8 @@ The table and every operation on it live in the HIP library ``libhkv.so``
 behind the C ABI of ``include/hkv.h``; this package is its Python binding.
 ``HashTable`` owns one table and allocates output tensors; the functions of
 ``hash_table_cache_amd._native`` mirror the C entry points one to one. The
-training operators (losses on logits, gradient clipping) are functions of
+training operators (losses and statistics of logits, gradient clipping, updates
+of dense weights) are functions of
 ``hash_table_cache_amd.training`` on the library ``libhkv_train.so``.
 """
 
@@ -42,6 +43,8 @@ from .training import (
     PreferenceLoss,
     TokenStats,
     clip_grad_norm,
+    muon_update,
+    orthogonalize,
     policy_loss,
     preference_loss,
     token_logprobs,
@@ -52,8 +55,8 @@ from .training import (
 
 __all__ = ["HashTable", "HkvError", "BUCKET_SLOTS", "EMPTY_KEY", "LOCKED_KEY", "HKV_FLAG_SERIAL_INSERT",
            "HKV_FLAG_RW_LOCK", "HKV_FLAG_UNIQUE_KEYS", "PolicyLoss", "PreferenceLoss", "TokenStats",
-           "clip_grad_norm", "policy_loss", "preference_loss", "token_logprobs", "token_logprobs_backward", "token_stats",
-           "token_stats_backward"]
+           "clip_grad_norm", "muon_update", "orthogonalize", "policy_loss", "preference_loss", "token_logprobs",
+           "token_logprobs_backward", "token_stats", "token_stats_backward"]
 
 
 class HashTable:

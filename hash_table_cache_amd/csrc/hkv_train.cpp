@@ -197,6 +197,120 @@ hkv_status check_workspace(Buffers& buffers, const void* ws, uint64_t bytes, uin
   return HKV_OK;
 }
 
+// Whether the singular values and what a step makes of them stay in the range
+// that the kernels hold: they start in [0, 1], and over the interval that a step
+// can reach, |s| < 3.9 (A = s^2 < 16) and |b s^2 + c s^4| < 15.5 are required.
+hkv_status check_coefficients(uint32_t steps, const double* c) {
+  if (steps == 0 || steps > hkvt::kMostSteps)
+    return fail(HKV_EINVAL, "steps = %u is outside 1 .. %u", steps, hkvt::kMostSteps);
+  if (!c) return fail(HKV_EINVAL, "coefficients is NULL");
+  double most = 1.0;
+  for (uint32_t k = 0; k < steps; ++k) {
+    const double a = c[3 * k], b = c[3 * k + 1], d = c[3 * k + 2];
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(d))
+      return fail(HKV_EINVAL, "coefficients of step %u are not finite", k);
+    const double s = most * (1.0 + 1.0 / 256), end = s * s;  // rounding included
+    double value = 0.0, inner = 0.0;
+    const auto at = [&](double square) {
+      if (!(square >= 0.0 && square <= end)) return;
+      inner = std::max(inner, std::fabs(square * (b + d * square)));
+      value = std::max(value, std::fabs(std::sqrt(square) * (a + square * (b + d * square))));
+    };
+    at(end);
+    if (d != 0.0) {
+      at(-b / (2.0 * d));
+      const double root = std::sqrt(std::max(0.0, 9.0 * b * b - 20.0 * a * d));
+      at((-3.0 * b + root) / (10.0 * d));
+      at((-3.0 * b - root) / (10.0 * d));
+    } else if (b != 0.0) {
+      at(-a / (3.0 * b));
+    }
+    if (!(s < 3.9) || !(inner < 15.5))
+      return fail(HKV_EINVAL, "coefficients of step %u take singular values out of range (up to %g, inner part %g)", k,
+                  s, inner);
+    most = std::max(value, 1e-6);
+  }
+  if (!(most < 3.9)) return fail(HKV_EINVAL, "coefficients take singular values out of range (up to %g)", most);
+  return HKV_OK;
+}
+
+// The memory of matrices: no written one may share an element with another. Two
+// whose ranges overlap may lie in different columns of the same wider rows.
+class Places {
+ public:
+  void add(const void* p, uint64_t rows, uint64_t cols, uint64_t stride, uint64_t es, bool written) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    list_.push_back({a, a + ((rows - 1) * stride + cols) * es, stride * es, cols * es, written});
+  }
+  bool clash() {
+    std::sort(list_.begin(), list_.end(), [](const Place& a, const Place& b) { return a.begin < b.begin; });
+    std::vector<Place> written, read;  // those that may reach further
+    for (const Place& p : list_) {
+      const auto over = [&](const Place& o) { return o.end <= p.begin; };
+      written.erase(std::remove_if(written.begin(), written.end(), over), written.end());
+      for (const Place& o : written)
+        if (!apart(o, p)) return true;
+      if (p.written) {
+        read.erase(std::remove_if(read.begin(), read.end(), over), read.end());
+        for (const Place& o : read)
+          if (!apart(o, p)) return true;
+      }
+      (p.written ? written : read).push_back(p);
+    }
+    return false;
+  }
+
+ private:
+  struct Place {
+    uintptr_t begin, end;
+    uint64_t stride, width;
+    bool written;
+  };
+  // o begins first and reaches past p's beginning.
+  static bool apart(const Place& o, const Place& p) {
+    if (o.stride != p.stride) return false;
+    const uint64_t column = (p.begin - o.begin) % o.stride;
+    return column >= o.width && column + p.width <= o.stride;
+  }
+  std::vector<Place> list_;
+};
+
+hkv_status check_layout(uint64_t cols, uint64_t stride, uint64_t dtype, const char* what, uint64_t i, uint64_t* es) {
+  if (dtype > hkvt::kF16 || !kind_size((uint32_t)dtype, es))
+    return fail(HKV_EINVAL, "%s[%llu]: dtype %llu", what, (unsigned long long)i, (unsigned long long)dtype);
+  if (stride < cols || stride > (1ull << 40))
+    return fail(HKV_EINVAL, "%s[%llu]: stride = %llu with %llu columns", what, (unsigned long long)i,
+                (unsigned long long)stride, (unsigned long long)cols);
+  return HKV_OK;
+}
+
+hkv_status check_place(Buffers& buffers, const void* p, uint64_t rows, uint64_t cols, uint64_t stride, uint64_t es,
+                       const char* what, uint64_t i) {
+  HKV_TRY(buffers.check(p, ((rows - 1) * stride + cols) * es, what, (int64_t)i));
+  if (reinterpret_cast<uintptr_t>(p) % es)
+    return fail(HKV_EINVAL, "%s[%llu] is not aligned to its type", what, (unsigned long long)i);
+  return HKV_OK;
+}
+
+hkv_status check_sides(uint64_t rows, uint64_t cols, uint64_t i) {
+  if (rows > (1ull << 24) || cols > (1ull << 24) || rows * cols > (1ull << 32) || std::min(rows, cols) > (1ull << 15))
+    return fail(HKV_EINVAL, "matrix %llu: %llu x %llu is past 2^24 a side, 2^15 for the shorter one or 2^32 elements",
+                (unsigned long long)i, (unsigned long long)rows, (unsigned long long)cols);
+  return HKV_OK;
+}
+
+hkv_status run_polar(Buffers& buffers, const std::vector<hkvt::PolarMatrix>& list, const hkvt::PolarRule& rule,
+                     uint32_t steps, const double* coefficients, void* workspace, uint64_t workspace_bytes,
+                     hipStream_t stream, const char* what) {
+  if (list.empty()) return HKV_OK;
+  const uint32_t n = (uint32_t)list.size();
+  HKV_TRY(check_workspace(buffers, workspace, workspace_bytes, hkvt::polar_workspace_bytes(list.data(), n)));
+  DeviceGuard dg(buffers.device());
+  if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
+  const hipError_t e = hkvt::launch_polar(list.data(), n, rule, coefficients, steps, workspace, stream);
+  return e == hipSuccess ? HKV_OK : fail_hip(e, what);
+}
+
 }  // namespace
 
 HKV_API uint64_t hkv_train_workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tensors) {
@@ -438,6 +552,102 @@ HKV_API hkv_status hkv_clip_grad_norm(uint64_t tensors, void* const* grads, void
     if (dg.error() != hipSuccess) return fail_hip(dg.error(), "hipSetDevice");
     const hipError_t e = hkvt::launch_clip(list.data(), (uint32_t)list.size(), max_norm, norm_out, workspace, stream);
     return e == hipSuccess ? HKV_OK : fail_hip(e, "hkv_clip_grad_norm launch");
+  });
+}
+
+HKV_API uint64_t hkv_orthogonalize_workspace_bytes(uint64_t matrices, const uint64_t* rows, const uint64_t* cols,
+                                                   const uint8_t* out_dtypes) {
+  try {
+    if (!rows || !cols || !out_dtypes || matrices >= (1ull << 20)) return 0;
+    std::vector<hkvt::PolarMatrix> list;
+    for (uint64_t i = 0; i < matrices; ++i) {
+      if (rows[i] == 0 || cols[i] == 0) continue;
+      if (rows[i] > (1ull << 24) || cols[i] > (1ull << 24)) return 0;
+      hkvt::PolarMatrix m{};
+      m.rows = (uint32_t)rows[i];
+      m.cols = (uint32_t)cols[i];
+      m.out_kind = out_dtypes[i];
+      list.push_back(m);
+    }
+    return list.empty() ? 0 : hkvt::polar_workspace_bytes(list.data(), (uint32_t)list.size());
+  } catch (...) {
+    return 0;
+  }
+}
+
+HKV_API hkv_status hkv_orthogonalize(uint64_t matrices, const hkv_matrix* list, uint32_t steps,
+                                     const double* coefficients, double eps, void* workspace,
+                                     uint64_t workspace_bytes, hipStream_t stream) {
+  return guarded([&]() -> hkv_status {
+    if (matrices >= (1ull << 20))
+      return fail(HKV_EINVAL, "matrices = %llu, the limit is 2^20 - 1", (unsigned long long)matrices);
+    if (matrices && !list) return fail(HKV_EINVAL, "list is NULL");
+    HKV_TRY(check_coefficients(steps, coefficients));
+    if (!(eps > 0.0) || !std::isfinite(eps)) return fail(HKV_EINVAL, "eps = %g has to be a positive finite number", eps);
+    Buffers buffers;
+    Places places;
+    std::vector<hkvt::PolarMatrix> todo;
+    todo.reserve(matrices);
+    for (uint64_t i = 0; i < matrices; ++i) {
+      const hkv_matrix& m = list[i];
+      if (m.rows == 0 || m.cols == 0) continue;
+      HKV_TRY(check_sides(m.rows, m.cols, i));
+      uint64_t in_size = 0, out_size = 0;
+      HKV_TRY(check_layout(m.cols, m.in_stride, m.in_dtype, "in", i, &in_size));
+      HKV_TRY(check_layout(m.cols, m.out_stride, m.out_dtype, "out", i, &out_size));
+      HKV_TRY(check_place(buffers, m.in, m.rows, m.cols, m.in_stride, in_size, "in", i));
+      HKV_TRY(check_place(buffers, m.out, m.rows, m.cols, m.out_stride, out_size, "out", i));
+      const bool same = m.in == m.out && m.in_stride == m.out_stride && m.in_dtype == m.out_dtype;
+      if (!same) places.add(m.in, m.rows, m.cols, m.in_stride, in_size, false);
+      places.add(m.out, m.rows, m.cols, m.out_stride, out_size, true);
+      todo.push_back({m.in, m.out, nullptr, m.in_stride, m.out_stride, 0, 0.0, 1.0, (uint32_t)m.rows, (uint32_t)m.cols,
+                      (uint32_t)m.in_dtype, (uint32_t)m.out_dtype});
+    }
+    if (places.clash()) return fail(HKV_EINVAL, "two matrices overlap, and one of them is written");
+    return run_polar(buffers, todo, hkvt::PolarRule{0.0, eps, 0}, steps, coefficients, workspace, workspace_bytes,
+                     stream, "hkv_orthogonalize launch");
+  });
+}
+
+HKV_API hkv_status hkv_muon_update(uint64_t matrices, const hkv_muon_matrix* list, double momentum, uint32_t nesterov,
+                                   double weight_decay, uint32_t steps, const double* coefficients, double eps,
+                                   void* workspace, uint64_t workspace_bytes, hipStream_t stream) {
+  return guarded([&]() -> hkv_status {
+    if (matrices >= (1ull << 20))
+      return fail(HKV_EINVAL, "matrices = %llu, the limit is 2^20 - 1", (unsigned long long)matrices);
+    if (matrices && !list) return fail(HKV_EINVAL, "list is NULL");
+    if (!(momentum >= 0.0 && momentum < 1.0)) return fail(HKV_EINVAL, "momentum = %g is outside 0 .. 1", momentum);
+    if (nesterov > 1) return fail(HKV_EINVAL, "nesterov = %u is neither 0 nor 1", nesterov);
+    if (!std::isfinite(weight_decay)) return fail(HKV_EINVAL, "weight_decay = %g is not finite", weight_decay);
+    HKV_TRY(check_coefficients(steps, coefficients));
+    if (!(eps > 0.0) || !std::isfinite(eps)) return fail(HKV_EINVAL, "eps = %g has to be a positive finite number", eps);
+    Buffers buffers;
+    Places places;
+    std::vector<hkvt::PolarMatrix> todo;
+    todo.reserve(matrices);
+    for (uint64_t i = 0; i < matrices; ++i) {
+      const hkv_muon_matrix& m = list[i];
+      if (m.rows == 0 || m.cols == 0) continue;
+      HKV_TRY(check_sides(m.rows, m.cols, i));
+      if (!std::isfinite(m.lr) || !std::isfinite(m.scale))
+        return fail(HKV_EINVAL, "matrix %llu: lr = %g, scale = %g", (unsigned long long)i, m.lr, m.scale);
+      uint64_t ws = 0, gs = 0, ms = 0;
+      HKV_TRY(check_layout(m.cols, m.weight_stride, m.weight_dtype, "weight", i, &ws));
+      HKV_TRY(check_layout(m.cols, m.grad_stride, m.grad_dtype, "grad", i, &gs));
+      HKV_TRY(check_layout(m.cols, m.momentum_stride, HKV_F32, "momentum", i, &ms));
+      HKV_TRY(check_place(buffers, m.weight, m.rows, m.cols, m.weight_stride, ws, "weight", i));
+      HKV_TRY(check_place(buffers, m.grad, m.rows, m.cols, m.grad_stride, gs, "grad", i));
+      HKV_TRY(check_place(buffers, m.momentum, m.rows, m.cols, m.momentum_stride, ms, "momentum", i));
+      places.add(m.weight, m.rows, m.cols, m.weight_stride, ws, true);
+      places.add(m.grad, m.rows, m.cols, m.grad_stride, gs, false);
+      places.add(m.momentum, m.rows, m.cols, m.momentum_stride, ms, true);
+      todo.push_back({m.grad, m.weight, m.momentum, m.grad_stride, m.weight_stride, m.momentum_stride,
+                      1.0 - m.lr * weight_decay, -m.lr * m.scale, (uint32_t)m.rows, (uint32_t)m.cols,
+                      (uint32_t)m.grad_dtype, (uint32_t)m.weight_dtype});
+    }
+    if (places.clash()) return fail(HKV_EINVAL, "two matrices overlap, and one of them is written");
+    return run_polar(buffers, todo, hkvt::PolarRule{momentum, eps, nesterov}, steps, coefficients, workspace,
+                     workspace_bytes, stream, "hkv_muon_update launch");
   });
 }
 

@@ -82,6 +82,26 @@ struct Tensor {
   uint32_t first;  // number of its first chunk among all tensors' chunks
 };
 
+// One matrix to orthogonalise. With a momentum, the update made of both goes to
+// the weights `out`: out = keep * out + step * O; without, out = O.
+struct PolarMatrix {
+  const void* in;  // the matrix, or the gradient
+  void* out;
+  float* momentum;
+  uint64_t in_stride, out_stride, momentum_stride;  // elements
+  double keep, step;
+  uint32_t rows, cols;  // neither is 0
+  uint32_t in_kind, out_kind;
+};
+
+struct PolarRule {
+  double momentum;
+  double eps;
+  uint32_t nesterov;
+};
+
+constexpr uint32_t kMostSteps = 64;
+
 // Bytes of workspace of a call (every part 16-byte aligned).
 uint64_t workspace_bytes(uint64_t rows, uint64_t pairs, uint64_t tensors);
 // launch_logprobs: 0 unless workgroups share the rows.
@@ -102,5 +122,11 @@ constexpr uint64_t kChunkBytes = 32768;
 __host__ __device__ constexpr uint64_t chunk_elems(uint32_t kind) { return kChunkBytes / (kind == kF32 ? 4 : 2); }
 // `first` is filled in here.
 hipError_t launch_clip(Tensor* t, uint32_t tensors, double max_norm, float* norm, void* ws, hipStream_t s);
+
+
+uint64_t polar_workspace_bytes(const PolarMatrix* m, uint32_t n);
+// coefficients: three numbers a step, in host memory.
+hipError_t launch_polar(const PolarMatrix* m, uint32_t n, const PolarRule& r, const double* coefficients,
+                        uint32_t steps, void* ws, hipStream_t s);
 
 }  // namespace hkvt

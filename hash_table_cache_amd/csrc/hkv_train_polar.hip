@@ -1,0 +1,565 @@
+// gfx950 kernels that orthogonalise matrices, and the momentum update that uses
+// it (include/hkv_train.h).
+//
+// With X = u / |u|, oriented so that its rows are its shorter side (p rows of q),
+// a step is
+//   A = X X^T,  B = b A + c A A,  X <- a X + B X.
+// All three are products of matrices whose rows are read along the inner
+// dimension once X is also held transposed: A from rows of X, A A from rows of A
+// (A is symmetric), and (B X)^T = X^T B from rows of X^T and rows of B. Of the
+// first two only the tiles on and above the diagonal are computed.
+//
+// The matrix cores multiply halves and add in 32 bits. Everything is held scaled
+// by 2^12: |X| <= 2, |A| < 16, |B| < 16 (the host checks it for the coefficients)
+// keep halves finite, and elements down to 2^-26 of |X| keep their digits. Two
+// precisions:
+//   - split: a number is the sum of two halves, and a product three products of
+//     halves (what is left out is 2^-22 of it): as precise as float32.
+//   - single: one product of halves. Rounding would still cost most where it
+//     counts: a X, which alone carries the small singular values, and the
+//     diagonals of A and B, which near the end are nearly all of them. So X
+//     keeps both halves for a X, the diagonals are kept out of the halves in 32
+//     bits, D = diag A, E = diag B:
+//       B X = E X + (B - E) X,  A A = (A - D)(A - D) + D (A - D) + (A - D) D + D D.
+//     Results are off by 4e-4 to 9e-4 of their size (2-norm), less than their
+//     rounding to bf16 (1.7e-3); with A, B and X rounded as they are, by 1.3e-3
+//     for a full spectrum and by 4e-2 for one of 8 directions among 512.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+#include "hkv_train_internal.h"
+#include "hkv_train_rows.h"
+
+namespace hkvt {
+namespace {
+
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kUnit = 4096.0f;  // what 1 is held as
+constexpr int kPolarThreads = 256;
+constexpr uint32_t kNormParts = 1024;  // partial sums of a matrix at most
+constexpr uint32_t kNormRows = 64, kNormCols = 256;
+constexpr uint32_t kUploads = 16;
+
+// One matrix of a launch, as the kernels see it. Halves lie in planes: the
+// upper halves, then the lower ones.
+struct PolarItem {
+  PolarMatrix m;
+  _Float16* x;     // [p][q]
+  _Float16* t[2];  // [q][p], both halves: of this step and of the next
+  _Float16* a;     // [p][p]
+  _Float16* b;     // [p][p]
+  float* d;        // [p]: diagonal of A
+  float* e;        // [p]: diagonal of B
+  double* partial;
+  uint32_t p, q;        // padded to the tile
+  uint32_t flip;        // rows > cols: X is the transpose
+  uint32_t parts;       // partial sums
+  uint32_t part_tiles;  // tiles that each has
+  uint32_t first_part, first_pack, first_gram, first_next;  // numbers among all items' workgroups
+};
+
+struct PolarUpload {
+  PolarItem item[kUploads];
+};
+static_assert(sizeof(PolarUpload) <= 4000, "kernel arguments");
+
+__global__ void polar_upload_kernel(const PolarUpload u, PolarItem* to, uint32_t n) {
+  const uint32_t words = n * sizeof(PolarItem) / 4;
+  for (uint32_t i = threadIdx.x; i < words; i += kPolarThreads)
+    reinterpret_cast<uint32_t*>(to)[i] = reinterpret_cast<const uint32_t*>(&u)[i];
+}
+
+// The last of n items whose first workgroup is `block` or an earlier one.
+__device__ __forceinline__ const PolarItem& find_item(const PolarItem* items, uint32_t n, uint32_t block,
+                                                      uint32_t PolarItem::* first) {
+  uint32_t lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (items[mid].*first <= block)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return items[__builtin_amdgcn_readfirstlane(lo)];
+}
+
+__device__ __forceinline__ double load_kind(const void* p, uint32_t kind, uint64_t i) {
+  if (kind == kF32) return static_cast<const float*>(p)[i];
+  if (kind == kBF16) return (float)static_cast<const __bf16*>(p)[i];
+  return (float)static_cast<const _Float16*>(p)[i];
+}
+
+__device__ __forceinline__ void store_kind(void* p, uint32_t kind, uint64_t i, double v) {
+  if (kind == kF32)
+    static_cast<float*>(p)[i] = (float)v;
+  else if (kind == kBF16)
+    static_cast<__bf16*>(p)[i] = (__bf16)(float)v;
+  else
+    static_cast<_Float16*>(p)[i] = (_Float16)(float)v;
+}
+
+// The update that is orthogonalised, at one place, once the momentum is there.
+__device__ __forceinline__ double update_at(const PolarMatrix& m, const PolarRule& r, uint64_t row, uint64_t col) {
+  if (!m.momentum) return load_kind(m.in, m.in_kind, row * m.in_stride + col);
+  const double s = m.momentum[row * m.momentum_stride + col];
+  if (!r.nesterov) return s;
+  return (1.0 - r.momentum) * load_kind(m.in, m.in_kind, row * m.in_stride + col) + r.momentum * s;
+}
+
+// The momentum, and partial sums of the squares of the update, in 64 bits.
+__global__ __launch_bounds__(kPolarThreads) void polar_norm_kernel(const PolarItem* items, uint32_t n, const PolarRule r) {
+  __shared__ double sh[kPolarThreads / 64];
+  const PolarItem& it = find_item(items, n, blockIdx.x, &PolarItem::first_part);
+  const PolarMatrix m = it.m;
+  const uint32_t part = blockIdx.x - it.first_part, across = (m.cols - 1) / kNormCols + 1;
+  const uint32_t tiles = across * ((m.rows - 1) / kNormRows + 1);
+  double sum = 0.0;
+  for (uint32_t k = 0; k < it.part_tiles; ++k) {
+    const uint32_t tile = part * it.part_tiles + k;
+    if (tile >= tiles) break;
+    const uint32_t c0 = tile % across * kNormCols + threadIdx.x;
+    const uint32_t r0 = tile / across * kNormRows, r1 = min(r0 + kNormRows, m.rows);
+    if (c0 < m.cols) {
+      for (uint64_t row = r0; row < r1; ++row) {
+        if (m.momentum) {
+          float* s = m.momentum + row * m.momentum_stride + c0;
+          *s = (float)(r.momentum * (double)*s + (1.0 - r.momentum) * load_kind(m.in, m.in_kind, row * m.in_stride + c0));
+        }
+        const double u = update_at(m, r, row, c0);
+        sum += u * u;
+      }
+    }
+  }
+  sum = block_sum<kPolarThreads>(sum, sh);
+  if (threadIdx.x == 0) it.partial[part] = sum;
+}
+
+// What a float is held as: the nearest half, and the half nearest to the rest.
+__device__ __forceinline__ void split_half(float v, _Float16* hi, _Float16* lo) {
+  *hi = (_Float16)v;
+  *lo = (_Float16)(v - (float)*hi);
+}
+
+// X and its transpose from the update, 64 x 64 elements a workgroup, zeros where
+// the tiles reach past the matrix. A matrix whose norm is not finite becomes NaN.
+template <bool SPLIT>
+__global__ __launch_bounds__(kPolarThreads) void polar_pack_kernel(const PolarItem* items, uint32_t n, const PolarRule r) {
+  __shared__ double sh[kPolarThreads / 64];
+  __shared__ float tile[64][65];
+  const PolarItem& it = find_item(items, n, blockIdx.x, &PolarItem::first_pack);
+  const PolarMatrix m = it.m;
+  const uint32_t block = blockIdx.x - it.first_pack, across = it.q / 64;
+  const uint32_t i0 = block / across * 64, j0 = block % across * 64;  // of X
+  double sum = 0.0;
+  for (uint32_t i = threadIdx.x; i < it.parts; i += kPolarThreads) sum += it.partial[i];
+  const double norm = sqrt(block_sum<kPolarThreads>(sum, sh));
+  const double scale = norm < (double)kInf ? kUnit / fmax(norm, r.eps) : __builtin_nan("");
+  const uint32_t row0 = it.flip ? j0 : i0, col0 = it.flip ? i0 : j0;  // of the matrix
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (uint32_t k = wave; k < 64; k += kPolarThreads / 64) {
+    const uint32_t row = row0 + k, col = col0 + lane;
+    float v = 0.0f;
+    if (row < m.rows && col < m.cols) v = (float)(update_at(m, r, row, col) * scale);
+    if (it.flip)
+      tile[lane][k] = v;
+    else
+      tile[k][lane] = v;
+  }
+  __syncthreads();
+  const uint64_t plane = (uint64_t)it.p * it.q;
+  for (uint32_t k = wave; k < 64; k += kPolarThreads / 64) {
+    _Float16 hi, lo;
+    split_half(tile[k][lane], &hi, &lo);
+    const uint64_t ix = (uint64_t)(i0 + k) * it.q + j0 + lane;
+    it.x[ix] = hi;
+    if (SPLIT) it.x[plane + ix] = lo;
+    split_half(tile[lane][k], &hi, &lo);
+    const uint64_t tx = (uint64_t)(j0 + k) * it.p + i0 + lane;
+    it.t[0][tx] = hi;
+    it.t[0][plane + tx] = lo;
+  }
+}
+
+// One T x T tile of a product of rows: acc[i][j] = sum over k of a[i][k] b[j][k],
+// K inner elements, rows K apart. Four waves of a quarter each; 64 inner elements
+// at a time go through LDS, two buffers, rows of 8 pieces of 16 bytes whose order
+// is shuffled by the row so that a wave's reads of one column of pieces meet all
+// banks. SPLIT: lower x upper, upper x lower and upper x upper halves, one after
+// the other, `plane_a` and `plane_b` elements apart.
+template <int T, bool SPLIT>
+struct Product {
+  static constexpr int W = T / 2;    // of a wave
+  static constexpr int F = W / 32;   // fragments of a wave, each way
+  static constexpr int L = T * 8 / kPolarThreads;  // pieces that a thread brings, of each side
+  struct Shared {
+    f16x8 a[2][T * 8], b[2][T * 8];
+  };
+  f32x16 acc[F][F];
+
+  __device__ __forceinline__ void run(const _Float16* a, const _Float16* b, uint32_t K, uint64_t plane_a,
+                                      uint64_t plane_b, Shared& sh) {
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint32_t piece = tid & 7, row = tid >> 3;
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j) acc[i][j] = f32x16{};
+    const uint32_t blocks = K / 64, rounds = SPLIT ? 3 * blocks : blocks;
+    f16x8 ra[L], rb[L];
+    auto fetch = [&](uint32_t r) {
+      const uint32_t seg = SPLIT ? r / blocks : 2, k = (SPLIT ? r % blocks : r) * 64 + piece * 8;
+      const _Float16* pa = a + (seg == 0 ? plane_a : 0) + k;
+      const _Float16* pb = b + (seg == 1 ? plane_b : 0) + k;
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        ra[i] = *reinterpret_cast<const f16x8*>(pa + (uint64_t)(row + i * (kPolarThreads / 8)) * K);
+        rb[i] = *reinterpret_cast<const f16x8*>(pb + (uint64_t)(row + i * (kPolarThreads / 8)) * K);
+      }
+    };
+    auto keep = [&](int buf) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        const uint32_t at = row + i * (kPolarThreads / 8), slot = at * 8 + (piece ^ (at & 7));
+        sh.a[buf][slot] = ra[i];
+        sh.b[buf][slot] = rb[i];
+      }
+    };
+    fetch(0);
+    keep(0);
+    const uint32_t ar = wave / 2 * W + (lane & 31), br = wave % 2 * W + (lane & 31);
+    for (uint32_t r = 0; r < rounds; ++r) {
+      const int buf = r & 1;
+      __syncthreads();
+      if (r + 1 < rounds) fetch(r + 1);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint32_t pc = ks * 2 + (lane >> 5);
+        f16x8 fa[F], fb[F];
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+          fa[i] = sh.a[buf][(ar + i * 32) * 8 + (pc ^ ((ar + i * 32) & 7))];
+          fb[i] = sh.b[buf][(br + i * 32) * 8 + (pc ^ ((br + i * 32) & 7))];
+        }
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+          for (int j = 0; j < F; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      }
+      if (r + 1 < rounds) keep(buf ^ 1);
+    }
+  }
+
+  // use(row, column, four values of rows row .. row + 3) for each of a thread's quads.
+  template <typename Use>
+  __device__ __forceinline__ void each(Use&& use) const {
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int j = 0; j < F; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = acc[i][j][g * 4 + k];
+          use(wave / 2 * W + i * 32 + g * 8 + (lane >> 5) * 4, wave % 2 * W + j * 32 + (lane & 31), v);
+        }
+  }
+};
+
+// Number of a tile on or above the diagonal -> its place: 0 (0,0), 1 (0,1), 2 (1,1), 3 (0,2) ...
+__device__ __forceinline__ void upper_tile(uint32_t tile, uint32_t* i, uint32_t* j) {
+  uint32_t c = (uint32_t)((__builtin_sqrtf(8.0f * (float)tile + 1.0f) - 1.0f) * 0.5f);
+  while (c * (c + 1) / 2 > tile) --c;
+  while ((c + 1) * (c + 2) / 2 <= tile) ++c;
+  *j = c;
+  *i = tile - c * (c + 1) / 2;
+}
+
+// Writes a quad of a symmetric matrix at both its places, as halves.
+template <bool SPLIT>
+__device__ __forceinline__ void store_both(_Float16* to, uint64_t p, uint64_t row, uint64_t col, const float* v) {
+  f16x4 hi, lo;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    _Float16 h, l;
+    split_half(v[k], &h, &l);
+    hi[k] = h;
+    lo[k] = l;
+  }
+  *reinterpret_cast<f16x4*>(to + col * p + row) = hi;
+  if (SPLIT) *reinterpret_cast<f16x4*>(to + p * p + col * p + row) = lo;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    to[(row + k) * p + col] = hi[k];
+    if (SPLIT) to[p * p + (row + k) * p + col] = lo[k];
+  }
+}
+
+// A without its diagonal, and D.
+template <int T, bool SPLIT>
+__global__ __launch_bounds__(kPolarThreads) void polar_gram_kernel(const PolarItem* items, uint32_t n) {
+  __shared__ typename Product<T, SPLIT>::Shared sh;
+  const PolarItem& it = find_item(items, n, blockIdx.x, &PolarItem::first_gram);
+  uint32_t ti, tj;
+  upper_tile(blockIdx.x - it.first_gram, &ti, &tj);
+  const uint64_t p = it.p, q = it.q;
+  Product<T, SPLIT> m;
+  m.run(it.x + ti * T * q, it.x + tj * T * q, it.q, p * q, p * q, sh);
+  m.each([&](uint32_t r, uint32_t c, float* v) {
+    const uint64_t row = (uint64_t)ti * T + r, col = (uint64_t)tj * T + c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] *= 1.0f / kUnit;
+      if (row + k == col) {
+        it.d[col] = v[k] * (1.0f / kUnit);
+        v[k] = 0.0f;
+      }
+    }
+    store_both<SPLIT>(it.a, p, row, col, v);
+  });
+}
+
+// B without its diagonal, and E.
+template <int T, bool SPLIT>
+__global__ __launch_bounds__(kPolarThreads) void polar_square_kernel(const PolarItem* items, uint32_t n, float b, float c2) {
+  __shared__ typename Product<T, SPLIT>::Shared sh;
+  const PolarItem& it = find_item(items, n, blockIdx.x, &PolarItem::first_gram);
+  uint32_t ti, tj;
+  upper_tile(blockIdx.x - it.first_gram, &ti, &tj);
+  const uint64_t p = it.p;
+  Product<T, SPLIT> m;
+  m.run(it.a + ti * T * p, it.a + tj * T * p, it.p, p * p, p * p, sh);
+  m.each([&](uint32_t r, uint32_t c, float* v) {
+    const uint64_t row = (uint64_t)ti * T + r, col = (uint64_t)tj * T + c;
+    const _Float16* at = it.a + col * p + row;  // A is symmetric
+    const float dc = it.d[col];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float a = (float)at[k];
+      if (SPLIT) a += (float)at[p * p + k];
+      v[k] = fmaf(b, a, c2 * fmaf(it.d[row + k] + dc, a, v[k] * (1.0f / kUnit)));
+      if (row + k == col) {
+        it.e[col] = fmaf(c2, dc * dc, fmaf(b, dc, v[k] * (1.0f / kUnit)));
+        v[k] = 0.0f;
+      }
+    }
+    store_both<SPLIT>(it.b, p, row, col, v);
+  });
+}
+
+// a X + B X, transposed, of step `k`; the last one's goes to its destination.
+template <int T, bool SPLIT>
+__global__ __launch_bounds__(kPolarThreads) void polar_next_kernel(const PolarItem* items, uint32_t n, float a,
+                                                                   uint32_t step, bool last) {
+  __shared__ typename Product<T, SPLIT>::Shared sh;
+  const PolarItem& it = find_item(items, n, blockIdx.x, &PolarItem::first_next);
+  const uint64_t p = it.p, q = it.q;
+  const uint32_t tile = blockIdx.x - it.first_next, across = it.p / T;
+  const uint32_t ti = tile / across, tj = tile % across;
+  const _Float16* from = it.t[step & 1];
+  _Float16* to = it.t[~step & 1];
+  Product<T, SPLIT> m;
+  m.run(from + ti * T * p, it.b + tj * T * p, it.p, p * q, p * p, sh);
+  m.each([&](uint32_t rr, uint32_t c, float* v) {
+    const uint64_t row = (uint64_t)ti * T + rr, col = (uint64_t)tj * T + c;  // of X^T
+    const float f = a + it.e[col];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t i = (row + k) * p + col;
+      v[k] = fmaf(f, (float)from[i] + (float)from[p * q + i], v[k] * (1.0f / kUnit));
+    }
+    if (last) {
+      const PolarMatrix& w = it.m;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t wr = it.flip ? row + k : col, wc = it.flip ? col : row + k;
+        if (wr >= w.rows || wc >= w.cols) continue;
+        const uint64_t i = wr * w.out_stride + wc;
+        double o = (double)v[k] * (1.0 / kUnit);
+        if (w.momentum) o = w.keep * load_kind(w.out, w.out_kind, i) + w.step * o;
+        store_kind(w.out, w.out_kind, i, o);
+      }
+      return;
+    }
+    f16x4 hi, lo;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      _Float16 h, l;
+      split_half(v[k], &h, &l);
+      hi[k] = h;
+      lo[k] = l;
+      const uint64_t i = (row + k) * p + col;
+      to[i] = h;
+      to[p * q + i] = l;
+    }
+    *reinterpret_cast<f16x4*>(it.x + col * q + row) = hi;
+    if (SPLIT) *reinterpret_cast<f16x4*>(it.x + p * q + col * q + row) = lo;
+  });
+}
+
+// How a call's matrices are worked on: in groups whose scratch fits into
+// kGroupBytes, of one precision and tile each.
+constexpr uint64_t kGroupBytes = 4ull << 30;
+constexpr uint32_t kGroupTiles = 1u << 22;
+
+struct Group {
+  uint32_t begin, end;  // of the order
+  uint32_t tile;
+  bool split;
+  uint64_t bytes;
+};
+
+uint64_t up256(uint64_t b) { return (b + 255) & ~255ull; }
+
+uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
+
+// Takes an item's scratch, from `at` on where that is memory; returns its bytes.
+uint64_t lay_out(const PolarMatrix& m, uint32_t tile, bool split, char* at, PolarItem* it) {
+  uint64_t used = 0;
+  auto take = [&](uint64_t bytes) {
+    char* p = at ? at + used : nullptr;
+    used += up256(bytes);
+    return p;
+  };
+  const uint64_t p = up(std::min(m.rows, m.cols), tile), q = up(std::max(m.rows, m.cols), tile), planes = split ? 2 : 1;
+  it->x = reinterpret_cast<_Float16*>(take(p * q * 2 * planes));
+  for (auto& t : it->t) t = reinterpret_cast<_Float16*>(take(p * q * 4));
+  it->a = reinterpret_cast<_Float16*>(take(p * p * 2 * planes));
+  it->b = reinterpret_cast<_Float16*>(take(p * p * 2 * planes));
+  it->d = reinterpret_cast<float*>(take(p * 4));
+  it->e = reinterpret_cast<float*>(take(p * 4));
+  const uint64_t tiles = (uint64_t)((m.cols - 1) / kNormCols + 1) * ((m.rows - 1) / kNormRows + 1);
+  it->part_tiles = (uint32_t)((tiles - 1) / kNormParts + 1);
+  it->parts = (uint32_t)((tiles - 1) / it->part_tiles + 1);
+  it->partial = reinterpret_cast<double*>(take(it->parts * 8));
+  it->p = (uint32_t)p;
+  it->q = (uint32_t)q;
+  it->flip = m.rows > m.cols;
+  it->m = m;
+  return used;
+}
+
+bool splits(const PolarMatrix& m) { return m.out_kind != kBF16; }
+
+// A tile of 128 feeds the matrix cores better, one of 64 gives twice to four
+// times as many workgroups.
+constexpr uint64_t kManyTiles = 512;
+
+struct Plan {
+  std::vector<uint32_t> order;
+  std::vector<Group> groups;
+  uint64_t bytes = 0;  // of the largest group, the items' list included
+};
+
+Plan make_plan(const PolarMatrix* m, uint32_t n) {
+  Plan plan;
+  plan.order.reserve(n);
+  for (int kind = 0; kind < 4; ++kind) {  // precision, and whether the shorter side fits a tile of 64
+    const uint32_t begin = (uint32_t)plan.order.size();
+    uint64_t tiles = 0;
+    const bool split = kind & 1, small = kind & 2;
+    for (uint32_t i = 0; i < n; ++i) {
+      if (splits(m[i]) != split || (std::min(m[i].rows, m[i].cols) <= 64) != small) continue;
+      plan.order.push_back(i);
+      tiles += up(m[i].rows, 128) / 128 * (up(m[i].cols, 128) / 128);
+    }
+    const uint32_t tile = !small && tiles >= kManyTiles ? 128 : 64;
+    for (uint32_t at = begin; at < plan.order.size();) {
+      Group g{at, at, tile, split, 0};
+      uint64_t count = 0;
+      while (g.end < plan.order.size()) {
+        PolarItem it;
+        const PolarMatrix& x = m[plan.order[g.end]];
+        const uint64_t bytes = lay_out(x, tile, split, nullptr, &it) + up256(sizeof(PolarItem));
+        const uint64_t more = (uint64_t)(it.p / 64) * (it.q / 64);
+        if (g.end > at && (g.bytes + bytes > kGroupBytes || count + more > kGroupTiles)) break;
+        g.bytes += bytes;
+        count += more;
+        ++g.end;
+      }
+      plan.bytes = std::max(plan.bytes, g.bytes);
+      plan.groups.push_back(g);
+      at = g.end;
+    }
+  }
+  return plan;
+}
+
+template <int T, bool SPLIT>
+hipError_t steps_t(const PolarItem* items, uint32_t n, uint32_t gram, uint32_t next, const double* c,
+                   uint32_t steps, hipStream_t s) {
+  for (uint32_t k = 0; k < steps; ++k, c += 3) {
+    polar_gram_kernel<T, SPLIT><<<gram, kPolarThreads, 0, s>>>(items, n);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    polar_square_kernel<T, SPLIT><<<gram, kPolarThreads, 0, s>>>(items, n, (float)c[1], (float)c[2]);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    polar_next_kernel<T, SPLIT><<<next, kPolarThreads, 0, s>>>(items, n, (float)c[0], k, k + 1 == steps);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t run_group(const PolarMatrix* m, const uint32_t* order, const Group& g, const PolarRule& r, const double* c,
+                     uint32_t steps, char* ws, hipStream_t s) {
+  const uint32_t n = g.end - g.begin;
+  PolarItem* items = reinterpret_cast<PolarItem*>(ws);
+  char* at = ws + up256((uint64_t)n * sizeof(PolarItem));
+  uint32_t parts = 0, packs = 0, gram = 0, next = 0;
+  for (uint32_t i = 0; i < n; i += kUploads) {
+    PolarUpload u;
+    const uint32_t many = std::min(kUploads, n - i);
+    for (uint32_t j = 0; j < many; ++j) {
+      PolarItem& it = u.item[j];
+      at += lay_out(m[order[g.begin + i + j]], g.tile, g.split, at, &it);
+      it.first_part = parts;
+      it.first_pack = packs;
+      it.first_gram = gram;
+      it.first_next = next;
+      parts += it.parts;
+      packs += it.p / 64 * (it.q / 64);
+      const uint32_t pt = it.p / g.tile, qt = it.q / g.tile;
+      gram += pt * (pt + 1) / 2;
+      next += pt * qt;
+    }
+    polar_upload_kernel<<<1, kPolarThreads, 0, s>>>(u, items + i, many);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  polar_norm_kernel<<<parts, kPolarThreads, 0, s>>>(items, n, r);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (g.split)
+    polar_pack_kernel<true><<<packs, kPolarThreads, 0, s>>>(items, n, r);
+  else
+    polar_pack_kernel<false><<<packs, kPolarThreads, 0, s>>>(items, n, r);
+  if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (g.tile == 128)
+    return g.split ? steps_t<128, true>(items, n, gram, next, c, steps, s)
+                   : steps_t<128, false>(items, n, gram, next, c, steps, s);
+  return g.split ? steps_t<64, true>(items, n, gram, next, c, steps, s)
+                 : steps_t<64, false>(items, n, gram, next, c, steps, s);
+}
+
+}  // namespace
+
+uint64_t polar_workspace_bytes(const PolarMatrix* m, uint32_t n) { return make_plan(m, n).bytes; }
+
+hipError_t launch_polar(const PolarMatrix* m, uint32_t n, const PolarRule& r, const double* coefficients,
+                        uint32_t steps, void* ws, hipStream_t s) {
+  const Plan plan = make_plan(m, n);
+  for (const Group& g : plan.groups) {
+    const hipError_t e = run_group(m, plan.order.data(), g, r, coefficients, steps, static_cast<char*>(ws), s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace hkvt

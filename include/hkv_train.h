@@ -11,7 +11,9 @@
  *     preferred, from the ratios to a reference; value and gradient;
  *   - hkv_policy_loss: clipped policy-gradient loss with a divergence (KL)
  *     term; value and gradient;
- *   - hkv_clip_grad_norm: global norm of many gradient tensors, and clipping.
+ *   - hkv_clip_grad_norm: global norm of many gradient tensors, and clipping;
+ *   - hkv_orthogonalize: the nearest orthogonal matrix, by Newton-Schulz products;
+ *   - hkv_muon_update: momentum, orthogonalised, applied to dense weights.
  *
  * Notation: tau = temperature, y = labels[t],
  *   lse_t  = log sum_v exp(x[t][v] / tau),   logp_t = x[t][y] / tau - lse_t.
@@ -199,6 +201,65 @@ hkv_status hkv_policy_loss(uint64_t rows, uint64_t vocab, uint32_t dtype, const 
 hkv_status hkv_clip_grad_norm(uint64_t tensors, void* const* grads, void* const* outs, const uint64_t* numel,
                               const uint8_t* dtypes, float max_norm, float* norm_out, void* workspace,
                               uint64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * hkv_orthogonalize - for each matrix u of a list
+ *   X = u / max(|u|, eps) (2-norm over its elements, held in 64 bits);
+ *   `steps` times: A = X X^T, X <- a X + (b A + c A A) X   (on the shorter side:
+ *   where u has more rows than columns, its transpose is taken);
+ *   out = X.
+ * With coefficients that draw singular values towards 1, X nears U V^T of u = U S
+ * V^T. Products are taken by the matrix cores, added in 32 bits, of numbers held
+ * as halves: where out is HKV_BF16 one half each, which leaves results off by
+ * less than their rounding (2-norm), elsewhere two, as precise as float32. A
+ * matrix of zeros gives zeros, one that holds NaN or infinities NaN throughout.
+ *   list         array of `matrices` entries in HOST memory, read during the call;
+ *                matrices without an element are passed over
+ *   coefficients [3 * steps] in HOST memory: a, b, c of each step. Refused where
+ *                they would take singular values out of the range that is held
+ *                (up to 3.9, |b s^2 + c s^4| up to 15.5).
+ *   steps 1 .. 64, eps > 0
+ * A matrix's rows are *_stride elements apart. out may be the matrix itself (same
+ * address, stride and type); no other written matrix may share an element with
+ * another one of the list (columns of the same wider rows are separate matrices).
+ * Sides up to 2^24, the shorter one up to 2^15, up to 2^32 elements.
+ * workspace: hkv_orthogonalize_workspace_bytes(...) of the same matrices (in hkv_muon_update the
+ * weights' types).
+ */
+typedef struct hkv_matrix {
+  const void* in;
+  void* out;
+  uint64_t rows, cols;
+  uint64_t in_stride, out_stride;
+  uint64_t in_dtype, out_dtype;
+} hkv_matrix;
+
+uint64_t hkv_orthogonalize_workspace_bytes(uint64_t matrices, const uint64_t* rows, const uint64_t* cols,
+                                           const uint8_t* out_dtypes);
+hkv_status hkv_orthogonalize(uint64_t matrices, const hkv_matrix* list, uint32_t steps, const double* coefficients,
+                             double eps, void* workspace, uint64_t workspace_bytes, hipStream_t stream);
+
+/*
+ * hkv_muon_update - for each weight matrix W with gradient G and momentum M:
+ *   M <- momentum M + (1 - momentum) G
+ *   u = (1 - momentum) G + momentum M with nesterov, M without
+ *   W <- (1 - lr weight_decay) W - lr scale O,   O = hkv_orthogonalize's of u.
+ * M is float32; each M and W is rounded once, to its type.
+ *   0 <= momentum < 1
+ */
+typedef struct hkv_muon_matrix {
+  void* weight;
+  const void* grad;
+  float* momentum;
+  uint64_t rows, cols;
+  uint64_t weight_stride, grad_stride, momentum_stride;
+  uint64_t weight_dtype, grad_dtype;
+  double lr, scale;
+} hkv_muon_matrix;
+
+hkv_status hkv_muon_update(uint64_t matrices, const hkv_muon_matrix* list, double momentum, uint32_t nesterov,
+                           double weight_decay, uint32_t steps, const double* coefficients, double eps,
+                           void* workspace, uint64_t workspace_bytes, hipStream_t stream);
 
 /* Description of the last failure of a call in this header on the calling thread. */
 const char* hkv_train_last_error(void);
