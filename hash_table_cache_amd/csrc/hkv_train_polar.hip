@@ -46,6 +46,12 @@ constexpr uint32_t kNormParts = 1024;  // partial sums of a matrix at most
 constexpr uint32_t kNormRows = 64, kNormCols = 256;
 constexpr uint32_t kUploads = 16;
 
+// 16 bytes a lane from memory to LDS, to where the wave's first lane points and on.
+__device__ __forceinline__ void bring(const _Float16* from, f16x8* to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
 // One matrix of a launch, as the kernels see it. Halves lie in planes: the
 // upper halves, then the lower ones.
 struct PolarItem {
@@ -186,92 +192,214 @@ __global__ __launch_bounds__(kPolarThreads) void polar_pack_kernel(const PolarIt
   }
 }
 
-// One T x T tile of a product of rows: acc[i][j] = sum over k of a[i][k] b[j][k],
-// K inner elements, rows K apart. Four waves of a quarter each; 64 inner elements
-// at a time go through LDS, two buffers, rows of 8 pieces of 16 bytes whose order
-// is shuffled by the row so that a wave's reads of one column of pieces meet all
-// banks. SPLIT: lower x upper, upper x lower and upper x upper halves, one after
-// the other, `plane_a` and `plane_b` elements apart.
-template <int T, bool SPLIT>
-struct Product {
-  static constexpr int W = T / 2;    // of a wave
-  static constexpr int F = W / 32;   // fragments of a wave, each way
-  static constexpr int L = T * 8 / kPolarThreads;  // pieces that a thread brings, of each side
-  struct Shared {
-    f16x8 a[2][T * 8], b[2][T * 8];
-  };
-  f32x16 acc[F][F];
+// A tile of T x T of a product of rows, acc[i][j] = sum over k of a[i][k] b[j][k],
+// by WM x WN waves of FM x FN fragments of 32 x 32 each.
+template <int T>
+struct Shape;
+template <>
+struct Shape<64> {
+  static constexpr int WM = 2, WN = 2, FM = 1, FN = 1, kBlocks = 4;
+};
+template <>
+struct Shape<128> {
+  static constexpr int WM = 2, WN = 2, FM = 2, FN = 2, kBlocks = 2;
+};
+template <>
+struct Shape<256> {
+  static constexpr int WM = 2, WN = 4, FM = 4, FN = 2, kBlocks = 2;
+};
 
-  __device__ __forceinline__ void run(const _Float16* a, const _Float16* b, uint32_t K, uint64_t plane_a,
-                                      uint64_t plane_b, Shared& sh) {
-    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const uint32_t piece = tid & 7, row = tid >> 3;
+// 64 inner elements at a time go through LDS, two buffers, written by memory
+// itself, 16 bytes a lane. A row of a buffer is 8 pieces of 16 bytes, and their
+// order is shuffled by the row: a wave reads one piece of 32 rows at once, 16 rows
+// at a time, and two rows of 128 bytes share the 64 banks, so that rows 2 i and 2 i
+// + 1 have piece k at k ^ (i % 8). (By the row itself, half of LDS's cycles were
+// conflicts.) The next buffer's loads are issued between the products, a quarter
+// with each sixteen inner elements: all at once they hold the waves up for as long
+// as half of the products take (4096 x 4096 x 2048, T = 256: 1008 TFLOP/s against
+// 950; T = 128: 854 against 830; more buffers, or fragments read one step ahead,
+// were no faster).
+template <int T>
+struct Product {
+  using S = Shape<T>;
+  static constexpr int FM = S::FM, FN = S::FN;
+  static constexpr int kThreads = S::WM * S::WN * 64;
+  static constexpr int L = T * 8 / kThreads;  // pieces that a thread brings, of each side
+  static constexpr int kStage = 2 * T * 8;
+  typedef f16x8 Shared[2 * kStage];
+  f32x16 acc[FM][FN];
+
+  // `to` and `from` are buffers apart, which the compiler has to know: it would
+  // otherwise wait for the loads before it reads.
+  __device__ __forceinline__ void stage(f16x8* __restrict to, const f16x8* __restrict from, const _Float16* a,
+                                        const _Float16* b, uint32_t off, uint64_t hop, bool more, uint32_t wave,
+                                        uint32_t ar, uint32_t br, uint32_t key) {
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+    for (int ks = 0; ks < 4; ++ks) {
+      f16x8 fa[FM], fb[FN];
+      const uint32_t pc = (ks * 2) ^ key;
 #pragma unroll
-      for (int j = 0; j < F; ++j) acc[i][j] = f32x16{};
-    const uint32_t blocks = K / 64, rounds = SPLIT ? 3 * blocks : blocks;
-    f16x8 ra[L], rb[L];
-    auto fetch = [&](uint32_t r) {
-      const uint32_t seg = SPLIT ? r / blocks : 2, k = (SPLIT ? r % blocks : r) * 64 + piece * 8;
-      const _Float16* pa = a + (seg == 0 ? plane_a : 0) + k;
-      const _Float16* pb = b + (seg == 1 ? plane_b : 0) + k;
+      for (int i = 0; i < FM; ++i) fa[i] = from[ar + i * 256 + pc];
 #pragma unroll
-      for (int i = 0; i < L; ++i) {
-        ra[i] = *reinterpret_cast<const f16x8*>(pa + (uint64_t)(row + i * (kPolarThreads / 8)) * K);
-        rb[i] = *reinterpret_cast<const f16x8*>(pb + (uint64_t)(row + i * (kPolarThreads / 8)) * K);
-      }
-    };
-    auto keep = [&](int buf) {
+      for (int i = 0; i < FN; ++i) fb[i] = from[T * 8 + br + i * 256 + pc];
+      if (more) {
 #pragma unroll
-      for (int i = 0; i < L; ++i) {
-        const uint32_t at = row + i * (kPolarThreads / 8), slot = at * 8 + (piece ^ (at & 7));
-        sh.a[buf][slot] = ra[i];
-        sh.b[buf][slot] = rb[i];
-      }
-    };
-    fetch(0);
-    keep(0);
-    const uint32_t ar = wave / 2 * W + (lane & 31), br = wave % 2 * W + (lane & 31);
-    for (uint32_t r = 0; r < rounds; ++r) {
-      const int buf = r & 1;
-      __syncthreads();
-      if (r + 1 < rounds) fetch(r + 1);
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        const uint32_t pc = ks * 2 + (lane >> 5);
-        f16x8 fa[F], fb[F];
-#pragma unroll
-        for (int i = 0; i < F; ++i) {
-          fa[i] = sh.a[buf][(ar + i * 32) * 8 + (pc ^ ((ar + i * 32) & 7))];
-          fb[i] = sh.b[buf][(br + i * 32) * 8 + (pc ^ ((br + i * 32) & 7))];
+        for (int i = ks * L / 2; i < (ks + 1) * L / 2; ++i) {
+          if (i < L)
+            bring(a + i * hop + off, to + i * kThreads + wave * 64);
+          else
+            bring(b + (i - L) * hop + off, to + T * 8 + (i - L) * kThreads + wave * 64);
         }
-#pragma unroll
-        for (int i = 0; i < F; ++i)
-#pragma unroll
-          for (int j = 0; j < F; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
       }
-      if (r + 1 < rounds) keep(buf ^ 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
-  // use(row, column, four values of rows row .. row + 3) for each of a thread's quads.
+  // Rows K apart, K inner elements from the first one. SPLIT: lower x upper,
+  // upper x lower and upper x upper halves, one after the other, whose planes are
+  // plane_a and plane_b elements apart.
+  template <bool SPLIT>
+  __device__ __forceinline__ void run(const _Float16* a, const _Float16* b, uint32_t stride, uint32_t K, uint64_t plane_a,
+                                      uint64_t plane_b, Shared& sh) {
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = f32x16{};
+    const uint32_t row = tid >> 3, off = row * stride + ((tid & 7) ^ ((row >> 1) & 7)) * 8;
+    const uint64_t hop = (uint64_t)(kThreads / 8) * stride;
+    const uint32_t fr = lane & 31, key = (lane >> 5) ^ ((fr >> 1) & 7);
+    const uint32_t ar = (wave / S::WN * FM * 32 + fr) * 8, br = (wave % S::WN * FN * 32 + fr) * 8;
+    const uint32_t blocks = K / 64, rounds = SPLIT ? 3 * blocks : blocks;
+    const _Float16 *pa = SPLIT ? a + plane_a : a, *pb = b;
+    uint32_t left = blocks, seg = SPLIT ? 0 : 2;
+#pragma unroll
+    for (int i = 0; i < L; ++i) bring(pa + i * hop + off, sh + i * kThreads + wave * 64);
+#pragma unroll
+    for (int i = 0; i < L; ++i) bring(pb + i * hop + off, sh + T * 8 + i * kThreads + wave * 64);
+#pragma unroll 1
+    for (uint32_t r = 0; r < rounds; ++r) {
+      pa += 64;
+      pb += 64;
+      if (SPLIT && --left == 0 && seg < 2) {
+        pa = a;
+        pb = seg == 0 ? b + plane_b : b;
+        ++seg;
+        left = blocks;
+      }
+      __syncthreads();  // waits for the loads as well
+      f16x8* from = sh + (r & 1) * kStage;
+      stage(sh + (~r & 1) * kStage, from, pa, pb, off, hop, r + 1 < rounds, wave, ar, br, key);
+    }
+  }
+
+  // use(row, column, four values of rows row .. row + 3) for each of a thread's
+  // quads, few of them at a time: registers are full.
   template <typename Use>
-  __device__ __forceinline__ void each(Use&& use) const {
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __device__ __forceinline__ void each(Use&& use) {
+    uint32_t lane = threadIdx.x & 63;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    asm volatile("" : "+v"(lane));  // neither addresses nor halves are kept from one use to the next
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < F; ++j)
+      for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
+          if (T == 256 && g % 2 == 0) __builtin_amdgcn_sched_barrier(0);
           float v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[k] = acc[i][j][g * 4 + k];
-          use(wave / 2 * W + i * 32 + g * 8 + (lane >> 5) * 4, wave % 2 * W + j * 32 + (lane & 31), v);
+          use(wave / S::WN * FM * 32 + i * 32 + g * 8 + (lane >> 5) * 4, wave % S::WN * FN * 32 + j * 32 + (lane & 31), v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[i][j][g * 4 + k] = v[k];
         }
   }
+
+  // A tile of halves in LDS, T columns of T, on its way from or to memory by 16
+  // bytes a lane; a quad of a column is 8 bytes of it. Pieces are shuffled by the
+  // column as above.
+  static __device__ __forceinline__ uint32_t place(uint32_t r, uint32_t c) {
+    return c * T + (((r >> 3) ^ c) % (T / 8)) * 8 + (r & 7);
+  }
+  static __device__ __forceinline__ f16x4& quad(Shared& sh, uint32_t r, uint32_t c) {
+    return *reinterpret_cast<f16x4*>(reinterpret_cast<_Float16*>(sh) + place(r, c));
+  }
+
+  // Brings a tile, columns `stride` apart in memory.
+  static __device__ __forceinline__ void load_tile(const _Float16* from, uint64_t stride, Shared& sh) {
+    const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    __syncthreads();
+#pragma unroll
+    for (uint32_t i = 0; i < T * T / 8 / kThreads; ++i) {
+      const uint32_t at = i * kThreads + tid, c = at / (T / 8), piece = (at ^ c) % (T / 8);
+      bring(from + c * stride + piece * 8, sh + i * kThreads + wave * 64);
+    }
+    __syncthreads();
+  }
+
+  // value(quad) is written to a tile of columns `stride` apart.
+  template <typename Value>
+  __device__ __forceinline__ void store_tile(_Float16* to, uint64_t stride, Shared& sh, Value&& value) {
+    __syncthreads();
+    each([&](uint32_t r, uint32_t c, float* v) { quad(sh, r, c) = value(v); });
+    __syncthreads();
+#pragma unroll 4
+    for (uint32_t i = 0; i < T * T / 8 / kThreads; ++i) {
+      const uint32_t at = i * kThreads + threadIdx.x, c = at / (T / 8), piece = (at ^ c) % (T / 8);
+      *reinterpret_cast<f16x8*>(to + c * stride + piece * 8) = sh[at];
+    }
+  }
+
+  // The same as rows, `stride` apart.
+  template <typename Value>
+  __device__ __forceinline__ void store_rows(_Float16* to, uint64_t stride, Shared& sh, Value&& value) {
+    _Float16* lds = reinterpret_cast<_Float16*>(sh);
+    __syncthreads();
+    each([&](uint32_t r, uint32_t c, float* v) {
+      const f16x4 h = value(v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) lds[(r + k) * T + c] = h[k];
+    });
+    __syncthreads();
+#pragma unroll 4
+    for (uint32_t i = 0; i < T * T / 8 / kThreads; ++i) {
+      const uint32_t at = i * kThreads + threadIdx.x, r = at / (T / 8), piece = at % (T / 8);
+      *reinterpret_cast<f16x8*>(to + r * stride + piece * 8) = sh[at];
+    }
+  }
 };
+
+__device__ __forceinline__ f16x4 upper_halves(const float* v) {
+  f16x4 h;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) h[k] = (_Float16)v[k];
+  return h;
+}
+
+__device__ __forceinline__ f16x4 lower_halves(const float* v) {
+  f16x4 h;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) h[k] = (_Float16)(v[k] - (float)(_Float16)v[k]);
+  return h;
+}
+
+// Consecutive workgroups go to the 8 dies in turn; each die takes a range of the
+// tiles, whose rows its cache then holds (8 products of 4096 x 2048 x 2048: 282 us
+// against 285 us; 4 of 1024 cubed 18.0 us against 20.8 us).
+__device__ __forceinline__ uint32_t tile_of(uint32_t block, uint32_t blocks) {
+  const uint32_t die = block % 8, each = blocks / 8, more = blocks % 8;
+  return die * each + min(die, more) + block / 8;
+}
 
 // Number of a tile on or above the diagonal -> its place: 0 (0,0), 1 (0,1), 2 (1,1), 3 (0,2) ...
 __device__ __forceinline__ void upper_tile(uint32_t tile, uint32_t* i, uint32_t* j) {
@@ -282,38 +410,31 @@ __device__ __forceinline__ void upper_tile(uint32_t tile, uint32_t* i, uint32_t*
   *i = tile - c * (c + 1) / 2;
 }
 
-// Writes a quad of a symmetric matrix at both its places, as halves.
-template <bool SPLIT>
-__device__ __forceinline__ void store_both(_Float16* to, uint64_t p, uint64_t row, uint64_t col, const float* v) {
-  f16x4 hi, lo;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    _Float16 h, l;
-    split_half(v[k], &h, &l);
-    hi[k] = h;
-    lo[k] = l;
-  }
-  *reinterpret_cast<f16x4*>(to + col * p + row) = hi;
-  if (SPLIT) *reinterpret_cast<f16x4*>(to + p * p + col * p + row) = lo;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    to[(row + k) * p + col] = hi[k];
-    if (SPLIT) to[p * p + (row + k) * p + col] = lo[k];
-  }
+// Writes a tile of a symmetric matrix at both its places, as halves.
+template <int T, bool SPLIT>
+__device__ __forceinline__ void store_both(Product<T>& m, _Float16* to, uint64_t p, uint32_t ti, uint32_t tj,
+                                           typename Product<T>::Shared& sh) {
+  m.store_tile(to + (uint64_t)tj * T * p + ti * T, p, sh, upper_halves);
+  if (ti != tj) m.store_rows(to + (uint64_t)ti * T * p + tj * T, p, sh, upper_halves);
+  if (!SPLIT) return;
+  to += p * p;
+  m.store_tile(to + (uint64_t)tj * T * p + ti * T, p, sh, lower_halves);
+  if (ti != tj) m.store_rows(to + (uint64_t)ti * T * p + tj * T, p, sh, lower_halves);
 }
 
 // A without its diagonal, and D.
 template <int T, bool SPLIT>
-__global__ __launch_bounds__(kPolarThreads) void polar_gram_kernel(const PolarItem* items, uint32_t n) {
-  __shared__ typename Product<T, SPLIT>::Shared sh;
-  const PolarItem& it = find_item(items, n, blockIdx.x, &PolarItem::first_gram);
+__global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar_gram_kernel(const PolarItem* items, uint32_t n) {
+  __shared__ typename Product<T>::Shared sh;
+  const uint32_t block = tile_of(blockIdx.x, gridDim.x);
+  const PolarItem& it = find_item(items, n, block, &PolarItem::first_gram);
   uint32_t ti, tj;
-  upper_tile(blockIdx.x - it.first_gram, &ti, &tj);
+  upper_tile(block - it.first_gram, &ti, &tj);
   const uint64_t p = it.p, q = it.q;
-  Product<T, SPLIT> m;
-  m.run(it.x + ti * T * q, it.x + tj * T * q, it.q, p * q, p * q, sh);
+  Product<T> m;
+  m.template run<SPLIT>(it.x + ti * T * q, it.x + tj * T * q, it.q, it.q, p * q, p * q, sh);
   m.each([&](uint32_t r, uint32_t c, float* v) {
-    const uint64_t row = (uint64_t)ti * T + r, col = (uint64_t)tj * T + c;
+    const uint32_t row = ti * T + r, col = tj * T + c;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       v[k] *= 1.0f / kUnit;
@@ -322,86 +443,117 @@ __global__ __launch_bounds__(kPolarThreads) void polar_gram_kernel(const PolarIt
         v[k] = 0.0f;
       }
     }
-    store_both<SPLIT>(it.a, p, row, col, v);
   });
+  store_both<T, SPLIT>(m, it.a, p, ti, tj, sh);
 }
 
 // B without its diagonal, and E.
 template <int T, bool SPLIT>
-__global__ __launch_bounds__(kPolarThreads) void polar_square_kernel(const PolarItem* items, uint32_t n, float b, float c2) {
-  __shared__ typename Product<T, SPLIT>::Shared sh;
-  const PolarItem& it = find_item(items, n, blockIdx.x, &PolarItem::first_gram);
+__global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar_square_kernel(const PolarItem* items, uint32_t n,
+                                                                                           float b, float c2) {
+  __shared__ typename Product<T>::Shared sh;
+  const uint32_t block = tile_of(blockIdx.x, gridDim.x);
+  const PolarItem& it = find_item(items, n, block, &PolarItem::first_gram);
   uint32_t ti, tj;
-  upper_tile(blockIdx.x - it.first_gram, &ti, &tj);
+  upper_tile(block - it.first_gram, &ti, &tj);
   const uint64_t p = it.p;
-  Product<T, SPLIT> m;
-  m.run(it.a + ti * T * p, it.a + tj * T * p, it.p, p * p, p * p, sh);
+  Product<T> m;
+  m.template run<SPLIT>(it.a + ti * T * p, it.a + tj * T * p, it.p, it.p, p * p, p * p, sh);
+  const _Float16* tile = it.a + (uint64_t)tj * T * p + ti * T;  // A is symmetric
+  const float *dr = it.d + ti * T, *dc = it.d + tj * T;
+  for (int plane = SPLIT ? 1 : 0; plane >= 0; --plane) {
+    m.load_tile(tile + plane * p * p, p, sh);
+    m.each([&](uint32_t r, uint32_t c, float* v) {
+      const f16x4 a = m.quad(sh, r, c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = fmaf(c2, dr[r + k] + dc[c], b);  // of A - D
+        v[k] = fmaf(f, (float)a[k], plane == (SPLIT ? 1 : 0) ? v[k] * (c2 / kUnit) : v[k]);
+      }
+    });
+  }
   m.each([&](uint32_t r, uint32_t c, float* v) {
-    const uint64_t row = (uint64_t)ti * T + r, col = (uint64_t)tj * T + c;
-    const _Float16* at = it.a + col * p + row;  // A is symmetric
-    const float dc = it.d[col];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      float a = (float)at[k];
-      if (SPLIT) a += (float)at[p * p + k];
-      v[k] = fmaf(b, a, c2 * fmaf(it.d[row + k] + dc, a, v[k] * (1.0f / kUnit)));
-      if (row + k == col) {
-        it.e[col] = fmaf(c2, dc * dc, fmaf(b, dc, v[k] * (1.0f / kUnit)));
+      if (ti * T + r + k == tj * T + c) {
+        const float d = dc[c];
+        it.e[tj * T + c] = fmaf(c2, d * d, fmaf(b, d, v[k] * (1.0f / kUnit)));
         v[k] = 0.0f;
       }
     }
-    store_both<SPLIT>(it.b, p, row, col, v);
   });
+  store_both<T, SPLIT>(m, it.b, p, ti, tj, sh);
 }
 
-// a X + B X, transposed, of step `k`; the last one's goes to its destination.
-template <int T, bool SPLIT>
-__global__ __launch_bounds__(kPolarThreads) void polar_next_kernel(const PolarItem* items, uint32_t n, float a,
-                                                                   uint32_t step, bool last) {
-  __shared__ typename Product<T, SPLIT>::Shared sh;
-  const PolarItem& it = find_item(items, n, blockIdx.x, &PolarItem::first_next);
+// The tile (ti, tj) of the result, to the matrix or into the weights: by way of
+// LDS, 32 columns of every wave at a time, so that lanes lie next to each other
+// in memory.
+template <int T>
+__device__ __forceinline__ void write_out(Product<T>& m, const PolarItem& it, uint32_t ti, uint32_t tj,
+                                          typename Product<T>::Shared& sh) {
+  using S = Shape<T>;
+  constexpr uint32_t W = S::WN * 32;  // columns at a time
+  float* lds = reinterpret_cast<float*>(sh);
+  const PolarMatrix w = it.m;
+  const bool flip = it.flip;
+#pragma unroll
+  for (int j = 0; j < S::FN; ++j) {
+    __syncthreads();
+    m.each([&](uint32_t r, uint32_t c, float* v) {
+      if (c / 32 % S::FN != (uint32_t)j) return;
+      const uint32_t cc = c / 32 / S::FN * 32 + c % 32;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) lds[flip ? cc * T + ((r + k) ^ (cc * 4 % T)) : (r + k) * W + cc] = v[k];
+    });
+    __syncthreads();
+#pragma unroll 2
+    for (uint32_t i = threadIdx.x; i < T * W; i += Product<T>::kThreads) {
+      const uint32_t cc = flip ? i / T : i % W, r = flip ? (i % T) ^ (cc * 4 % T) : i / W;
+      const uint32_t row = ti * T + r, col = tj * T + (cc / 32 * S::FN + j) * 32 + cc % 32;  // of X
+      const uint32_t wr = flip ? col : row, wc = flip ? row : col;
+      if (wr >= w.rows || wc >= w.cols) continue;
+      const uint64_t at = wr * w.out_stride + wc;
+      double o = (double)lds[i] * (1.0 / kUnit);
+      if (w.momentum) o = w.keep * load_kind(w.out, w.out_kind, at) + w.step * o;
+      store_kind(w.out, w.out_kind, at, o);
+    }
+  }
+}
+
+// a X + B X of step `k`; the last one's goes to its destination. Columns of the
+// tile are rows of X^T.
+template <int T, bool SPLIT, bool LAST>
+__global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar_next_kernel(const PolarItem* items, uint32_t n,
+                                                                                         float a, uint32_t step) {
+  __shared__ typename Product<T>::Shared sh;
+  const uint32_t block = tile_of(blockIdx.x, gridDim.x);
+  const PolarItem& it = find_item(items, n, block, &PolarItem::first_next);
   const uint64_t p = it.p, q = it.q;
-  const uint32_t tile = blockIdx.x - it.first_next, across = it.p / T;
-  const uint32_t ti = tile / across, tj = tile % across;
+  const uint32_t tile = block - it.first_next, across = it.p / T;
+  const uint32_t ti = tile % across, tj = tile / across;
   const _Float16* from = it.t[step & 1];
+  Product<T> m;
+  m.template run<SPLIT>(it.b + ti * T * p, from + tj * T * p, it.p, it.p, p * p, p * q, sh);
+  const uint64_t at = (uint64_t)tj * T * p + ti * T;
+  const float* e = it.e + ti * T;
+  for (int plane = 1; plane >= 0; --plane) {
+    m.load_tile(from + plane * p * q + at, p, sh);
+    m.each([&](uint32_t r, uint32_t c, float* v) {
+      const f16x4 x = m.quad(sh, r, c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = fmaf(a + e[r + k], (float)x[k], plane ? v[k] * (1.0f / kUnit) : v[k]);
+    });
+  }
+  if (LAST) {
+    write_out(m, it, ti, tj, sh);
+    return;
+  }
   _Float16* to = it.t[~step & 1];
-  Product<T, SPLIT> m;
-  m.run(from + ti * T * p, it.b + tj * T * p, it.p, p * q, p * p, sh);
-  m.each([&](uint32_t rr, uint32_t c, float* v) {
-    const uint64_t row = (uint64_t)ti * T + rr, col = (uint64_t)tj * T + c;  // of X^T
-    const float f = a + it.e[col];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint64_t i = (row + k) * p + col;
-      v[k] = fmaf(f, (float)from[i] + (float)from[p * q + i], v[k] * (1.0f / kUnit));
-    }
-    if (last) {
-      const PolarMatrix& w = it.m;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint64_t wr = it.flip ? row + k : col, wc = it.flip ? col : row + k;
-        if (wr >= w.rows || wc >= w.cols) continue;
-        const uint64_t i = wr * w.out_stride + wc;
-        double o = (double)v[k] * (1.0 / kUnit);
-        if (w.momentum) o = w.keep * load_kind(w.out, w.out_kind, i) + w.step * o;
-        store_kind(w.out, w.out_kind, i, o);
-      }
-      return;
-    }
-    f16x4 hi, lo;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      _Float16 h, l;
-      split_half(v[k], &h, &l);
-      hi[k] = h;
-      lo[k] = l;
-      const uint64_t i = (row + k) * p + col;
-      to[i] = h;
-      to[p * q + i] = l;
-    }
-    *reinterpret_cast<f16x4*>(it.x + col * q + row) = hi;
-    if (SPLIT) *reinterpret_cast<f16x4*>(it.x + p * q + col * q + row) = lo;
-  });
+  m.store_tile(to + at, p, sh, upper_halves);
+  m.store_tile(to + p * q + at, p, sh, lower_halves);
+  _Float16* x = it.x + (uint64_t)ti * T * q + tj * T;
+  m.store_rows(x, q, sh, upper_halves);
+  if (SPLIT) m.store_rows(x + p * q, q, sh, lower_halves);
 }
 
 // How a call's matrices are worked on: in groups whose scratch fits into
@@ -463,14 +615,15 @@ Plan make_plan(const PolarMatrix* m, uint32_t n) {
   plan.order.reserve(n);
   for (int kind = 0; kind < 4; ++kind) {  // precision, and whether the shorter side fits a tile of 64
     const uint32_t begin = (uint32_t)plan.order.size();
-    uint64_t tiles = 0;
+    uint64_t tiles = 0, big = 0;
     const bool split = kind & 1, small = kind & 2;
     for (uint32_t i = 0; i < n; ++i) {
       if (splits(m[i]) != split || (std::min(m[i].rows, m[i].cols) <= 64) != small) continue;
       plan.order.push_back(i);
       tiles += up(m[i].rows, 128) / 128 * (up(m[i].cols, 128) / 128);
+      big += up(m[i].rows, 256) / 256 * (up(m[i].cols, 256) / 256);
     }
-    const uint32_t tile = !small && tiles >= kManyTiles ? 128 : 64;
+    const uint32_t tile = small ? 64 : big >= kManyTiles ? 256 : tiles >= kManyTiles ? 128 : 64;
     for (uint32_t at = begin; at < plan.order.size();) {
       Group g{at, at, tile, split, 0};
       uint64_t count = 0;
@@ -496,12 +649,15 @@ template <int T, bool SPLIT>
 hipError_t steps_t(const PolarItem* items, uint32_t n, uint32_t gram, uint32_t next, const double* c,
                    uint32_t steps, hipStream_t s) {
   for (uint32_t k = 0; k < steps; ++k, c += 3) {
-    polar_gram_kernel<T, SPLIT><<<gram, kPolarThreads, 0, s>>>(items, n);
+    polar_gram_kernel<T, SPLIT><<<gram, Product<T>::kThreads, 0, s>>>(items, n);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    polar_square_kernel<T, SPLIT><<<gram, kPolarThreads, 0, s>>>(items, n, (float)c[1], (float)c[2]);
+    polar_square_kernel<T, SPLIT><<<gram, Product<T>::kThreads, 0, s>>>(items, n, (float)c[1], (float)c[2]);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    polar_next_kernel<T, SPLIT><<<next, kPolarThreads, 0, s>>>(items, n, (float)c[0], k, k + 1 == steps);
+    if (k + 1 < steps)
+      polar_next_kernel<T, SPLIT, false><<<next, Product<T>::kThreads, 0, s>>>(items, n, (float)c[0], k);
+    else
+      polar_next_kernel<T, SPLIT, true><<<next, Product<T>::kThreads, 0, s>>>(items, n, (float)c[0], k);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;
@@ -541,6 +697,9 @@ hipError_t run_group(const PolarMatrix* m, const uint32_t* order, const Group& g
   else
     polar_pack_kernel<false><<<packs, kPolarThreads, 0, s>>>(items, n, r);
   if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (g.tile == 256)
+    return g.split ? steps_t<256, true>(items, n, gram, next, c, steps, s)
+                   : steps_t<256, false>(items, n, gram, next, c, steps, s);
   if (g.tile == 128)
     return g.split ? steps_t<128, true>(items, n, gram, next, c, steps, s)
                    : steps_t<128, false>(items, n, gram, next, c, steps, s);
