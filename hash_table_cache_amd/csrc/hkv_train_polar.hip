@@ -45,6 +45,7 @@ constexpr int kPolarThreads = 256;
 constexpr uint32_t kNormParts = 1024;  // partial sums of a matrix at most
 constexpr uint32_t kNormRows = 64, kNormCols = 256;
 constexpr uint32_t kUploads = 16;
+constexpr uint32_t kDies = 8;
 
 // 16 bytes a lane from memory to LDS, to where the wave's first lane points and on.
 __device__ __forceinline__ void bring(const _Float16* from, f16x8* to) {
@@ -67,7 +68,9 @@ struct PolarItem {
   uint32_t flip;        // rows > cols: X is the transpose
   uint32_t parts;       // partial sums
   uint32_t part_tiles;  // tiles that each has
-  uint32_t first_part, first_pack, first_gram, first_next;  // numbers among all items' workgroups
+  uint32_t first_part, first_pack;  // numbers among all items' workgroups
+  uint32_t first_gram, first_next;  // among a die's tiles
+  uint32_t each_gram, each_next;    // tiles that a die has at most
 };
 
 struct PolarUpload {
@@ -393,12 +396,20 @@ __device__ __forceinline__ f16x4 lower_halves(const float* v) {
   return h;
 }
 
-// Consecutive workgroups go to the 8 dies in turn; each die takes a range of the
-// tiles, whose rows its cache then holds (8 products of 4096 x 2048 x 2048: 282 us
-// against 285 us; 4 of 1024 cubed 18.0 us against 20.8 us).
-__device__ __forceinline__ uint32_t tile_of(uint32_t block, uint32_t blocks) {
-  const uint32_t die = block % 8, each = blocks / 8, more = blocks % 8;
-  return die * each + min(die, more) + block / 8;
+// Consecutive workgroups go to the 8 dies in turn. Each die takes an eighth of
+// every matrix's tiles, next to each other: their rows are in its cache, and long
+// and short products are spread alike. `first` and `each`: the matrix's begin and
+// number of tiles in every die's list.
+struct DieTile {
+  const PolarItem& item;
+  uint32_t tile;
+};
+
+__device__ __forceinline__ DieTile find_tile(const PolarItem* items, uint32_t n, uint32_t PolarItem::* first,
+                                             uint32_t PolarItem::* each) {
+  const uint32_t die = blockIdx.x % kDies, at = blockIdx.x / kDies;
+  const PolarItem& it = find_item(items, n, at, first);
+  return DieTile{it, die * (it.*each) + at - it.*first};
 }
 
 // Number of a tile on or above the diagonal -> its place: 0 (0,0), 1 (0,1), 2 (1,1), 3 (0,2) ...
@@ -426,10 +437,11 @@ __device__ __forceinline__ void store_both(Product<T>& m, _Float16* to, uint64_t
 template <int T, bool SPLIT>
 __global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar_gram_kernel(const PolarItem* items, uint32_t n) {
   __shared__ typename Product<T>::Shared sh;
-  const uint32_t block = tile_of(blockIdx.x, gridDim.x);
-  const PolarItem& it = find_item(items, n, block, &PolarItem::first_gram);
+  const DieTile found = find_tile(items, n, &PolarItem::first_gram, &PolarItem::each_gram);
+  const PolarItem& it = found.item;
   uint32_t ti, tj;
-  upper_tile(block - it.first_gram, &ti, &tj);
+  upper_tile(found.tile, &ti, &tj);
+  if (tj >= it.p / T) return;
   const uint64_t p = it.p, q = it.q;
   Product<T> m;
   m.template run<SPLIT>(it.x + ti * T * q, it.x + tj * T * q, it.q, it.q, p * q, p * q, sh);
@@ -452,10 +464,11 @@ template <int T, bool SPLIT>
 __global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar_square_kernel(const PolarItem* items, uint32_t n,
                                                                                            float b, float c2) {
   __shared__ typename Product<T>::Shared sh;
-  const uint32_t block = tile_of(blockIdx.x, gridDim.x);
-  const PolarItem& it = find_item(items, n, block, &PolarItem::first_gram);
+  const DieTile found = find_tile(items, n, &PolarItem::first_gram, &PolarItem::each_gram);
+  const PolarItem& it = found.item;
   uint32_t ti, tj;
-  upper_tile(block - it.first_gram, &ti, &tj);
+  upper_tile(found.tile, &ti, &tj);
+  if (tj >= it.p / T) return;
   const uint64_t p = it.p;
   Product<T> m;
   m.template run<SPLIT>(it.a + ti * T * p, it.a + tj * T * p, it.p, it.p, p * p, p * p, sh);
@@ -526,11 +539,11 @@ template <int T, bool SPLIT, bool LAST>
 __global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar_next_kernel(const PolarItem* items, uint32_t n,
                                                                                          float a, uint32_t step) {
   __shared__ typename Product<T>::Shared sh;
-  const uint32_t block = tile_of(blockIdx.x, gridDim.x);
-  const PolarItem& it = find_item(items, n, block, &PolarItem::first_next);
+  const DieTile found = find_tile(items, n, &PolarItem::first_next, &PolarItem::each_next);
+  const PolarItem& it = found.item;
   const uint64_t p = it.p, q = it.q;
-  const uint32_t tile = block - it.first_next, across = it.p / T;
-  const uint32_t ti = tile % across, tj = tile / across;
+  const uint32_t across = it.p / T, ti = found.tile % across, tj = found.tile / across;
+  if (tj >= it.q / T) return;
   const _Float16* from = it.t[step & 1];
   Product<T> m;
   m.template run<SPLIT>(it.b + ti * T * p, from + tj * T * p, it.p, it.p, p * p, p * q, sh);
@@ -623,6 +636,10 @@ Plan make_plan(const PolarMatrix* m, uint32_t n) {
       tiles += up(m[i].rows, 128) / 128 * (up(m[i].cols, 128) / 128);
       big += up(m[i].rows, 256) / 256 * (up(m[i].cols, 256) / 256);
     }
+    // long products first, so that the last ones to end are short
+    std::stable_sort(plan.order.begin() + begin, plan.order.end(), [&](uint32_t a, uint32_t b) {
+      return std::min(m[a].rows, m[a].cols) > std::min(m[b].rows, m[b].cols);
+    });
     const uint32_t tile = small ? 64 : big >= kManyTiles ? 256 : tiles >= kManyTiles ? 128 : 64;
     for (uint32_t at = begin; at < plan.order.size();) {
       Group g{at, at, tile, split, 0};
@@ -649,15 +666,15 @@ template <int T, bool SPLIT>
 hipError_t steps_t(const PolarItem* items, uint32_t n, uint32_t gram, uint32_t next, const double* c,
                    uint32_t steps, hipStream_t s) {
   for (uint32_t k = 0; k < steps; ++k, c += 3) {
-    polar_gram_kernel<T, SPLIT><<<gram, Product<T>::kThreads, 0, s>>>(items, n);
+    polar_gram_kernel<T, SPLIT><<<gram * kDies, Product<T>::kThreads, 0, s>>>(items, n);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    polar_square_kernel<T, SPLIT><<<gram, Product<T>::kThreads, 0, s>>>(items, n, (float)c[1], (float)c[2]);
+    polar_square_kernel<T, SPLIT><<<gram * kDies, Product<T>::kThreads, 0, s>>>(items, n, (float)c[1], (float)c[2]);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (k + 1 < steps)
-      polar_next_kernel<T, SPLIT, false><<<next, Product<T>::kThreads, 0, s>>>(items, n, (float)c[0], k);
+      polar_next_kernel<T, SPLIT, false><<<next * kDies, Product<T>::kThreads, 0, s>>>(items, n, (float)c[0], k);
     else
-      polar_next_kernel<T, SPLIT, true><<<next, Product<T>::kThreads, 0, s>>>(items, n, (float)c[0], k);
+      polar_next_kernel<T, SPLIT, true><<<next * kDies, Product<T>::kThreads, 0, s>>>(items, n, (float)c[0], k);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   return hipSuccess;
@@ -682,8 +699,10 @@ hipError_t run_group(const PolarMatrix* m, const uint32_t* order, const Group& g
       parts += it.parts;
       packs += it.p / 64 * (it.q / 64);
       const uint32_t pt = it.p / g.tile, qt = it.q / g.tile;
-      gram += pt * (pt + 1) / 2;
-      next += pt * qt;
+      it.each_gram = (pt * (pt + 1) / 2 - 1) / kDies + 1;
+      it.each_next = (pt * qt - 1) / kDies + 1;
+      gram += it.each_gram;
+      next += it.each_next;
     }
     polar_upload_kernel<<<1, kPolarThreads, 0, s>>>(u, items + i, many);
     const hipError_t e = hipGetLastError();
