@@ -43,7 +43,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr float kUnit = 4096.0f;  // what 1 is held as
 constexpr int kPolarThreads = 256;
 constexpr uint32_t kNormParts = 1024;  // partial sums of a matrix at most
-constexpr uint32_t kNormRows = 64, kNormCols = 256;
+constexpr uint32_t kNormRows = 16, kNormCols = 256;
 constexpr uint32_t kUploads = 16;
 constexpr uint32_t kDies = 8;
 
@@ -98,51 +98,120 @@ __device__ __forceinline__ const PolarItem& find_item(const PolarItem* items, ui
   return items[__builtin_amdgcn_readfirstlane(lo)];
 }
 
-__device__ __forceinline__ double load_kind(const void* p, uint32_t kind, uint64_t i) {
-  if (kind == kF32) return static_cast<const float*>(p)[i];
-  if (kind == kBF16) return (float)static_cast<const __bf16*>(p)[i];
-  return (float)static_cast<const _Float16*>(p)[i];
+// Up to four elements next to each other, of a matrix of any type, as floats and
+// back. Rows begin at any element: single accesses of 16 or 8 bytes at such
+// addresses are gfx950's.
+typedef u32x4 Quad32 __attribute__((aligned(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef u32x2 Quad16 __attribute__((aligned(2)));
+
+template <typename T>
+__device__ __forceinline__ void load_few(const T* p, uint32_t n, float* v) {
+  if (n == 4) {
+    if constexpr (sizeof(T) == 4) {
+      const u32x4 x = *reinterpret_cast<const Quad32*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = as_float(x[i]);
+    } else {
+      const u32x2 x = *reinterpret_cast<const Quad16*>(p);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint16_t h = (uint16_t)(x[i / 2] >> (i % 2 * 16));
+        v[i] = (float)__builtin_bit_cast(T, h);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = (uint32_t)i < n ? (float)p[i] : 0.0f;
 }
 
-__device__ __forceinline__ void store_kind(void* p, uint32_t kind, uint64_t i, double v) {
+template <typename T>
+__device__ __forceinline__ void store_few(T* p, uint32_t n, const float* v) {
+  if (n == 4) {
+    if constexpr (sizeof(T) == 4) {
+      u32x4 x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = __builtin_bit_cast(uint32_t, v[i]);
+      *reinterpret_cast<Quad32*>(p) = x;
+    } else {
+      u32x2 x{0, 0};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, (T)v[i]) << (i % 2 * 16);
+      *reinterpret_cast<Quad16*>(p) = x;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if ((uint32_t)i < n) p[i] = (T)v[i];
+}
+
+__device__ __forceinline__ void load_kind(const void* p, uint32_t kind, uint64_t i, uint32_t n, float* v) {
   if (kind == kF32)
-    static_cast<float*>(p)[i] = (float)v;
+    load_few(static_cast<const float*>(p) + i, n, v);
   else if (kind == kBF16)
-    static_cast<__bf16*>(p)[i] = (__bf16)(float)v;
+    load_few(static_cast<const __bf16*>(p) + i, n, v);
   else
-    static_cast<_Float16*>(p)[i] = (_Float16)(float)v;
+    load_few(static_cast<const _Float16*>(p) + i, n, v);
 }
 
-// The update that is orthogonalised, at one place, once the momentum is there.
-__device__ __forceinline__ double update_at(const PolarMatrix& m, const PolarRule& r, uint64_t row, uint64_t col) {
-  if (!m.momentum) return load_kind(m.in, m.in_kind, row * m.in_stride + col);
-  const double s = m.momentum[row * m.momentum_stride + col];
-  if (!r.nesterov) return s;
-  return (1.0 - r.momentum) * load_kind(m.in, m.in_kind, row * m.in_stride + col) + r.momentum * s;
+__device__ __forceinline__ void store_kind(void* p, uint32_t kind, uint64_t i, uint32_t n, const float* v) {
+  if (kind == kF32)
+    store_few(static_cast<float*>(p) + i, n, v);
+  else if (kind == kBF16)
+    store_few(static_cast<__bf16*>(p) + i, n, v);
+  else
+    store_few(static_cast<_Float16*>(p) + i, n, v);
 }
 
-// The momentum, and partial sums of the squares of the update, in 64 bits.
+// The update that is orthogonalised, n elements of a row, in 64 bits. MOVE: the
+// momentum takes the gradient in first.
+template <bool MOVE>
+__device__ __forceinline__ void update_few(const PolarMatrix& m, const PolarRule& r, uint64_t row, uint64_t col, uint32_t n,
+                                           double* u) {
+  float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (MOVE || !m.momentum || r.nesterov) load_kind(m.in, m.in_kind, row * m.in_stride + col, n, g);
+  if (!m.momentum) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = g[i];
+    return;
+  }
+  float s[4];
+  float* at = m.momentum + row * m.momentum_stride + col;
+  load_few(at, n, s);
+  if (MOVE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = (float)(r.momentum * (double)s[i] + (1.0 - r.momentum) * (double)g[i]);
+    store_few(at, n, s);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = r.nesterov ? (1.0 - r.momentum) * (double)g[i] + r.momentum * (double)s[i] : (double)s[i];
+}
+
+// The momentum, and partial sums of the squares of the update, in 64 bits: a wave
+// takes 256 elements of a row at a time.
 __global__ __launch_bounds__(kPolarThreads) void polar_norm_kernel(const PolarItem* items, uint32_t n, const PolarRule r) {
   __shared__ double sh[kPolarThreads / 64];
   const PolarItem& it = find_item(items, n, blockIdx.x, &PolarItem::first_part);
   const PolarMatrix m = it.m;
   const uint32_t part = blockIdx.x - it.first_part, across = (m.cols - 1) / kNormCols + 1;
   const uint32_t tiles = across * ((m.rows - 1) / kNormRows + 1);
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   double sum = 0.0;
   for (uint32_t k = 0; k < it.part_tiles; ++k) {
     const uint32_t tile = part * it.part_tiles + k;
     if (tile >= tiles) break;
-    const uint32_t c0 = tile % across * kNormCols + threadIdx.x;
+    const uint32_t c0 = tile % across * kNormCols + lane * 4;
     const uint32_t r0 = tile / across * kNormRows, r1 = min(r0 + kNormRows, m.rows);
-    if (c0 < m.cols) {
-      for (uint64_t row = r0; row < r1; ++row) {
-        if (m.momentum) {
-          float* s = m.momentum + row * m.momentum_stride + c0;
-          *s = (float)(r.momentum * (double)*s + (1.0 - r.momentum) * load_kind(m.in, m.in_kind, row * m.in_stride + c0));
-        }
-        const double u = update_at(m, r, row, c0);
-        sum += u * u;
-      }
+    if (c0 >= m.cols) continue;
+    const uint32_t few = min(m.cols - c0, 4u);
+#pragma unroll 4
+    for (uint32_t row = r0 + wave; row < r1; row += kPolarThreads / 64) {
+      double u[4];
+      update_few<true>(m, r, row, c0, few, u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum += (uint32_t)i < few ? u[i] * u[i] : 0.0;
     }
   }
   sum = block_sum<kPolarThreads>(sum, sh);
@@ -150,9 +219,18 @@ __global__ __launch_bounds__(kPolarThreads) void polar_norm_kernel(const PolarIt
 }
 
 // What a float is held as: the nearest half, and the half nearest to the rest.
-__device__ __forceinline__ void split_half(float v, _Float16* hi, _Float16* lo) {
-  *hi = (_Float16)v;
-  *lo = (_Float16)(v - (float)*hi);
+__device__ __forceinline__ f16x4 upper_halves(const float* v) {
+  f16x4 h;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) h[k] = (_Float16)v[k];
+  return h;
+}
+
+__device__ __forceinline__ f16x4 lower_halves(const float* v) {
+  f16x4 h;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) h[k] = (_Float16)(v[k] - (float)(_Float16)v[k]);
+  return h;
 }
 
 // X and its transpose from the update, 64 x 64 elements a workgroup, zeros where
@@ -160,38 +238,52 @@ __device__ __forceinline__ void split_half(float v, _Float16* hi, _Float16* lo) 
 template <bool SPLIT>
 __global__ __launch_bounds__(kPolarThreads) void polar_pack_kernel(const PolarItem* items, uint32_t n, const PolarRule r) {
   __shared__ double sh[kPolarThreads / 64];
-  __shared__ float tile[64][65];
+  __shared__ float tile[64][65];  // of the matrix
   const PolarItem& it = find_item(items, n, blockIdx.x, &PolarItem::first_pack);
   const PolarMatrix m = it.m;
   const uint32_t block = blockIdx.x - it.first_pack, across = it.q / 64;
   const uint32_t i0 = block / across * 64, j0 = block % across * 64;  // of X
+  const uint32_t row0 = it.flip ? j0 : i0, col0 = it.flip ? i0 : j0;  // of the matrix
+  const uint32_t c = threadIdx.x % 16 * 4, r0 = threadIdx.x / 16;
+  double u[4][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t row = row0 + r0 + k * 16, col = col0 + c;
+    if (row < m.rows && col < m.cols) {
+      update_few<false>(m, r, row, col, min(m.cols - col, 4u), u[k]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[k][i] = 0.0;
+    }
+  }
   double sum = 0.0;
   for (uint32_t i = threadIdx.x; i < it.parts; i += kPolarThreads) sum += it.partial[i];
   const double norm = sqrt(block_sum<kPolarThreads>(sum, sh));
   const double scale = norm < (double)kInf ? kUnit / fmax(norm, r.eps) : __builtin_nan("");
-  const uint32_t row0 = it.flip ? j0 : i0, col0 = it.flip ? i0 : j0;  // of the matrix
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (uint32_t k = wave; k < 64; k += kPolarThreads / 64) {
-    const uint32_t row = row0 + k, col = col0 + lane;
-    float v = 0.0f;
-    if (row < m.rows && col < m.cols) v = (float)(update_at(m, r, row, col) * scale);
-    if (it.flip)
-      tile[lane][k] = v;
-    else
-      tile[k][lane] = v;
-  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = row0 + r0 + k * 16 < m.rows && col0 + c + i < m.cols;
+      tile[r0 + k * 16][c + i] = in ? (float)(u[k][i] * scale) : 0.0f;
+    }
   __syncthreads();
   const uint64_t plane = (uint64_t)it.p * it.q;
-  for (uint32_t k = wave; k < 64; k += kPolarThreads / 64) {
-    _Float16 hi, lo;
-    split_half(tile[k][lane], &hi, &lo);
-    const uint64_t ix = (uint64_t)(i0 + k) * it.q + j0 + lane;
-    it.x[ix] = hi;
-    if (SPLIT) it.x[plane + ix] = lo;
-    split_half(tile[lane][k], &hi, &lo);
-    const uint64_t tx = (uint64_t)(j0 + k) * it.p + i0 + lane;
-    it.t[0][tx] = hi;
-    it.t[0][plane + tx] = lo;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t a = r0 + k * 16;
+    float v[4], w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = tile[a][c + i];
+      w[i] = tile[c + i][a];
+    }
+    const float *x = it.flip ? w : v, *t = it.flip ? v : w;
+    const uint64_t ix = (uint64_t)(i0 + a) * it.q + j0 + c, tx = (uint64_t)(j0 + a) * it.p + i0 + c;
+    *reinterpret_cast<f16x4*>(it.x + ix) = upper_halves(x);
+    if (SPLIT) *reinterpret_cast<f16x4*>(it.x + plane + ix) = lower_halves(x);
+    *reinterpret_cast<f16x4*>(it.t[0] + tx) = upper_halves(t);
+    *reinterpret_cast<f16x4*>(it.t[0] + plane + tx) = lower_halves(t);
   }
 }
 
@@ -201,19 +293,19 @@ template <int T>
 struct Shape;
 template <>
 struct Shape<64> {
-  static constexpr int WM = 2, WN = 2, FM = 1, FN = 1, kBlocks = 4;
+  static constexpr int WM = 2, WN = 2, FM = 1, FN = 1, kBuffers = 4, kBlocks = 2;
 };
 template <>
 struct Shape<128> {
-  static constexpr int WM = 2, WN = 2, FM = 2, FN = 2, kBlocks = 2;
+  static constexpr int WM = 2, WN = 2, FM = 2, FN = 2, kBuffers = 2, kBlocks = 2;
 };
 template <>
 struct Shape<256> {
-  static constexpr int WM = 2, WN = 4, FM = 4, FN = 2, kBlocks = 2;
+  static constexpr int WM = 2, WN = 4, FM = 4, FN = 2, kBuffers = 2, kBlocks = 2;
 };
 
-// 64 inner elements at a time go through LDS, two buffers, written by memory
-// itself, 16 bytes a lane. A row of a buffer is 8 pieces of 16 bytes, and their
+// 64 inner elements at a time go through LDS, in buffers that memory itself
+// writes, 16 bytes a lane. A row of a buffer is 8 pieces of 16 bytes, and their
 // order is shuffled by the row: a wave reads one piece of 32 rows at once, 16 rows
 // at a time, and two rows of 128 bytes share the 64 banks, so that rows 2 i and 2 i
 // + 1 have piece k at k ^ (i % 8). (By the row itself, half of LDS's cycles were
@@ -229,7 +321,8 @@ struct Product {
   static constexpr int kThreads = S::WM * S::WN * 64;
   static constexpr int L = T * 8 / kThreads;  // pieces that a thread brings, of each side
   static constexpr int kStage = 2 * T * 8;
-  typedef f16x8 Shared[2 * kStage];
+  static constexpr int B = S::kBuffers;
+  typedef f16x8 Shared[B * kStage];
   f32x16 acc[FM][FN];
 
   // `to` and `from` are buffers apart, which the compiler has to know: it would
@@ -280,24 +373,43 @@ struct Product {
     const uint32_t ar = (wave / S::WN * FM * 32 + fr) * 8, br = (wave % S::WN * FN * 32 + fr) * 8;
     const uint32_t blocks = K / 64, rounds = SPLIT ? 3 * blocks : blocks;
     const _Float16 *pa = SPLIT ? a + plane_a : a, *pb = b;
-    uint32_t left = blocks, seg = SPLIT ? 0 : 2;
-#pragma unroll
-    for (int i = 0; i < L; ++i) bring(pa + i * hop + off, sh + i * kThreads + wave * 64);
-#pragma unroll
-    for (int i = 0; i < L; ++i) bring(pb + i * hop + off, sh + T * 8 + i * kThreads + wave * 64);
-#pragma unroll 1
-    for (uint32_t r = 0; r < rounds; ++r) {
+    uint32_t left = blocks, seg = 0;
+    auto advance = [&]() {
       pa += 64;
       pb += 64;
-      if (SPLIT && --left == 0 && seg < 2) {
+      if (SPLIT && --left == 0) {
         pa = a;
         pb = seg == 0 ? b + plane_b : b;
         ++seg;
         left = blocks;
       }
-      __syncthreads();  // waits for the loads as well
-      f16x8* from = sh + (r & 1) * kStage;
-      stage(sh + (~r & 1) * kStage, from, pa, pb, off, hop, r + 1 < rounds, wave, ar, br, key);
+    };
+#pragma unroll
+    for (int s = 0; s < B - 1; ++s) {
+      if ((uint32_t)s < rounds) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) bring(pa + i * hop + off, sh + s * kStage + i * kThreads + wave * 64);
+#pragma unroll
+        for (int i = 0; i < L; ++i) bring(pb + i * hop + off, sh + s * kStage + T * 8 + i * kThreads + wave * 64);
+        advance();
+      }
+    }
+    uint32_t at = 0, to = B - 1;
+#pragma unroll 1
+    for (uint32_t r = 0; r < rounds; ++r) {
+      // This wave's loads of this round's buffer are there, those of later ones may
+      // be on their way; behind the barrier the others' are there too, and nobody
+      // reads the buffer of the round before any more.
+      if (r + B - 2 < rounds)
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((B - 2) * 2 * L) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      stage(sh + to * kStage, sh + at * kStage, pa, pb, off, hop, r + B - 1 < rounds, wave, ar, br, key);
+      advance();
+      at = at + 1 == B ? 0 : at + 1;
+      to = to + 1 == B ? 0 : to + 1;
     }
   }
 
@@ -381,20 +493,6 @@ struct Product {
     }
   }
 };
-
-__device__ __forceinline__ f16x4 upper_halves(const float* v) {
-  f16x4 h;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) h[k] = (_Float16)v[k];
-  return h;
-}
-
-__device__ __forceinline__ f16x4 lower_halves(const float* v) {
-  f16x4 h;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) h[k] = (_Float16)(v[k] - (float)(_Float16)v[k]);
-  return h;
-}
 
 // Consecutive workgroups go to the 8 dies in turn. Each die takes an eighth of
 // every matrix's tiles, next to each other: their rows are in its cache, and long
@@ -519,16 +617,23 @@ __device__ __forceinline__ void write_out(Product<T>& m, const PolarItem& it, ui
       for (int k = 0; k < 4; ++k) lds[flip ? cc * T + ((r + k) ^ (cc * 4 % T)) : (r + k) * W + cc] = v[k];
     });
     __syncthreads();
-#pragma unroll 2
-    for (uint32_t i = threadIdx.x; i < T * W; i += Product<T>::kThreads) {
+    for (uint32_t i = threadIdx.x * 4; i < T * W; i += Product<T>::kThreads * 4) {
       const uint32_t cc = flip ? i / T : i % W, r = flip ? (i % T) ^ (cc * 4 % T) : i / W;
       const uint32_t row = ti * T + r, col = tj * T + (cc / 32 * S::FN + j) * 32 + cc % 32;  // of X
       const uint32_t wr = flip ? col : row, wc = flip ? row : col;
       if (wr >= w.rows || wc >= w.cols) continue;
+      const uint32_t few = min(w.cols - wc, 4u);
       const uint64_t at = wr * w.out_stride + wc;
-      double o = (double)lds[i] * (1.0 / kUnit);
-      if (w.momentum) o = w.keep * load_kind(w.out, w.out_kind, at) + w.step * o;
-      store_kind(w.out, w.out_kind, at, o);
+      float o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = lds[i + k] * (1.0f / kUnit);
+      if (w.momentum) {
+        float old[4];
+        load_kind(w.out, w.out_kind, at, few, old);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = (float)(w.keep * (double)old[k] + w.step * (double)o[k]);
+      }
+      store_kind(w.out, w.out_kind, at, few, o);
     }
   }
 }
