@@ -22,6 +22,40 @@ namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// The value of the lane whose number differs in bit W: by the ways that lanes of a
+// wave have to each other's registers, a third of the time of one through LDS.
+template <int W>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t v) {
+  if constexpr (W == 1) return __builtin_amdgcn_update_dpp(0, v, 0xB1, 0xF, 0xF, true);  // quad_perm 1 0 3 2
+  if constexpr (W == 2) return __builtin_amdgcn_update_dpp(0, v, 0x4E, 0xF, 0xF, true);  // quad_perm 2 3 0 1
+  if constexpr (W == 4) {  // the mirror of 8 lanes, then of 4
+    const uint32_t m = __builtin_amdgcn_update_dpp(0, v, 0x141, 0xF, 0xF, true);
+    return __builtin_amdgcn_update_dpp(0, m, 0x1B, 0xF, 0xF, true);
+  }
+  if constexpr (W == 8) return __builtin_amdgcn_update_dpp(0, v, 0x128, 0xF, 0xF, true);  // 16 lanes turned by 8
+  if constexpr (W == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return threadIdx.x & 16 ? r[0] : r[1];
+  }
+  const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return threadIdx.x & 32 ? r[0] : r[1];
+}
+
+template <int W>
+__device__ __forceinline__ float lane_xor(float v) {
+  return as_float(lane_xor<W>(__builtin_bit_cast(uint32_t, v)));
+}
+
+template <int W>
+__device__ __forceinline__ unsigned long long lane_xor(unsigned long long v) {
+  return (unsigned long long)lane_xor<W>((uint32_t)(v >> 32)) << 32 | lane_xor<W>((uint32_t)v);
+}
+
+template <int W>
+__device__ __forceinline__ double lane_xor(double v) {
+  return __builtin_bit_cast(double, lane_xor<W>(__builtin_bit_cast(unsigned long long, v)));
+}
+
 // Running maximum and sums of the elements a thread has seen; w is in units of
 // log 2, as the exponents are.
 struct Spread {
@@ -71,23 +105,33 @@ struct Spread {
   }
 };
 
-// Joins a wave's lanes, whose largest maximum is `top`; every lane gets the sums.
-__device__ __forceinline__ void join_lanes(Spread& r, float top, const Scale& c) {
-  const float base = top == -kInf ? 0.0f : top;
-  const float t = r.m - base;
-  r.rescale(fmaf(t, c.k_hi, t * c.k_lo));
-  r.m = top;
-#pragma unroll
-  for (int w = 32; w > 0; w /= 2) {
-    r.s += __shfl_xor(r.s, w);
-    r.w += __shfl_xor(r.w, w);
-  }
+template <typename V>
+__device__ __forceinline__ V sum_lanes(V v) {
+  v += lane_xor<1>(v);
+  v += lane_xor<2>(v);
+  v += lane_xor<4>(v);
+  v += lane_xor<8>(v);
+  v += lane_xor<16>(v);
+  return v + lane_xor<32>(v);
 }
 
 __device__ __forceinline__ float max_lanes(float v) {
-#pragma unroll
-  for (int w = 32; w > 0; w /= 2) v = fmaxf(v, __shfl_xor(v, w));
-  return v;
+  v = fmaxf(v, lane_xor<1>(v));
+  v = fmaxf(v, lane_xor<2>(v));
+  v = fmaxf(v, lane_xor<4>(v));
+  v = fmaxf(v, lane_xor<8>(v));
+  v = fmaxf(v, lane_xor<16>(v));
+  return fmaxf(v, lane_xor<32>(v));
+}
+
+// Joins a wave's lanes; every lane gets the sums.
+__device__ __forceinline__ void join_lanes(Spread& r, const Scale& c) {
+  const float top = max_lanes(r.m), base = top == -kInf ? 0.0f : top;
+  const float t = r.m - base;
+  r.rescale(fmaf(t, c.k_hi, t * c.k_lo));
+  r.m = top;
+  r.s = sum_lanes(r.s);
+  r.w = sum_lanes(r.w);
 }
 
 struct StatsEnd {
@@ -139,32 +183,39 @@ __device__ __forceinline__ float value_of(Key k) {
 
 __device__ __forceinline__ uint32_t index_of(Key k) { return ~(uint32_t)k; }
 
-// The lanes' values sorted downwards within blocks of SIZE lanes from blocks
-// that go up and down: the steps of a bitonic sort.
-template <typename V, int SIZE>
-__device__ __forceinline__ V sort_step(V v, bool down, int lane) {
-#pragma unroll
-  for (int w = SIZE / 2; w > 0; w /= 2) {
-    const V o = __shfl_xor(v, w);
-    v = (((lane & w) == 0) == down) == (v > o) ? v : o;
-  }
-  return v;
+// A step of a bitonic sort: the larger of two lanes' values goes to the lower one
+// where `down`.
+template <int W, typename V>
+__device__ __forceinline__ V sort_step(V v, bool down) {
+  const V o = lane_xor<W>(v);
+  return (((threadIdx.x & W) == 0) == down) == (v > o) ? v : o;
 }
 
+// Blocks of SIZE lanes that go up and then down, sorted.
+template <int SIZE, typename V>
+__device__ __forceinline__ V sort_blocks(V v, bool down) {
+  if constexpr (SIZE >= 64) v = sort_step<32>(v, down);
+  if constexpr (SIZE >= 32) v = sort_step<16>(v, down);
+  if constexpr (SIZE >= 16) v = sort_step<8>(v, down);
+  if constexpr (SIZE >= 8) v = sort_step<4>(v, down);
+  if constexpr (SIZE >= 4) v = sort_step<2>(v, down);
+  return sort_step<1>(v, down);
+}
+
+// The lanes' values, falling.
 template <typename V>
-__device__ __forceinline__ V sort_lanes(V v, int lane) {
-  v = sort_step<V, 2>(v, (lane & 2) == 0, lane);
-  v = sort_step<V, 4>(v, (lane & 4) == 0, lane);
-  v = sort_step<V, 8>(v, (lane & 8) == 0, lane);
-  v = sort_step<V, 16>(v, (lane & 16) == 0, lane);
-  v = sort_step<V, 32>(v, (lane & 32) == 0, lane);
-  return sort_step<V, 64>(v, true, lane);
+__device__ __forceinline__ V sort_lanes(V v) {
+  const uint32_t lane = threadIdx.x;
+  v = sort_blocks<2>(v, (lane & 2) == 0);
+  v = sort_blocks<4>(v, (lane & 4) == 0);
+  v = sort_blocks<8>(v, (lane & 8) == 0);
+  v = sort_blocks<16>(v, (lane & 16) == 0);
+  v = sort_blocks<32>(v, (lane & 32) == 0);
+  return sort_blocks<64>(v, true);
 }
 
 // The 64 largest of two sorted lists. `other` comes in reverse.
-__device__ __forceinline__ Key merge_lanes(Key v, Key other, int lane) {
-  return sort_step<Key, 64>(v > other ? v : other, true, lane);
-}
+__device__ __forceinline__ Key merge_lanes(Key v, Key other) { return sort_blocks<64>(v > other ? v : other, true); }
 
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -172,31 +223,66 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The k <= 64 largest elements that a wave has seen, sorted, one a lane, and a
-// bound under which no element comes among them. Elements that pass the bound
-// are gathered in LDS and join the list 64 at a time. N: how many may be added
-// before the list takes them.
-template <int N>
+// What the W waves of a team share while they look for the k <= 64 largest
+// elements: what each has gathered, H elements at most, and the bounds that
+// they found.
+template <int W, int H>
+struct TopsShared {
+  Key held[W][H];
+  float bound[W];
+  uint32_t count[W];
+};
+
+// The k largest elements that a wave has seen, sorted, one a lane, and a bound
+// under which no element comes among the team's. Elements that pass the bound are
+// gathered in LDS and join the list 64 at a time.
+// The bound: a wave knows j = ceil(k / W) lanes that have seen an element of at
+// least b_w; then k elements are at least the ceil(k / j)-th largest of the b_w. Of a row of
+// random order few more than k elements pass it (64 of 131072 by 8 waves: about
+// 270, where each wave's own 64th lane lets 4000 pass), and waves need not wait for
+// each other's bounds but in the first round: an old one is only lower.
+template <int W, int H>
 struct Tops {
-  static constexpr int kHeld = N + 64;
+  using Shared = TopsShared<W, H>;
   Key list = 0;
-  float bound = -kInf;      // an element of this value passes
-  uint32_t bound_at = 0;    // if its index is lower
-  uint32_t count = 0;       // gathered
-  Key* held;
-  uint32_t k;
+  float bound = -kInf;    // an element of this value passes
+  uint32_t bound_at = 0;  // if its index is lower
+  uint32_t count = 0;     // gathered
+  float seen = -kInf;     // by this lane
+  bool first = true, taken = false;
+  Shared& sh;
+  uint32_t k, wave;
   int lane;
 
-  __device__ __forceinline__ Tops(Key* lds, uint32_t k_) : held(lds), k(k_), lane(threadIdx.x & 63) {}
+  __device__ __forceinline__ Tops(Shared& sh_, uint32_t k_, uint32_t wave_)
+      : sh(sh_), k(k_), wave(wave_), lane(threadIdx.x & 63) {}
 
-  // A bound from the lanes' maxima of what comes next: k lanes have an element
-  // of at least the k-th largest of them.
+  // The bound that lanes of largest elements `mx` in the next round give.
   __device__ __forceinline__ void expect(float mx) {
-    if (__popcll(__ballot(mx > bound)) < 16 && bound > -kInf) return;
-    const float v = sort_lanes(mx, lane);
-    const float at = __shfl(v, (int)k - 1);
-    if (at > bound) {
-      bound = at;
+    seen = fmaxf(seen, mx);
+    if (!first && __popcll(__ballot(mx > bound)) < 4) return;
+    const uint32_t j = (k + W - 1) / W, m = (k + j - 1) / j;
+    const float own = j == 1 ? max_lanes(seen) : __shfl(sort_lanes(seen), (int)j - 1);
+    float least = own;
+    if (W > 1) {
+      if (lane == 0) sh.bound[wave] = own;
+      if (first)
+        __syncthreads();
+      else
+        wave_sync();
+      const float mine = *(volatile float*)&sh.bound[lane % W];
+      uint32_t above = 0;  // of the others' bounds
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float o = __shfl(mine, w);
+        above += o > mine || (o == mine && w < lane % W) ? 1 : 0;
+      }
+      least = __shfl(mine, __builtin_ctzll(__ballot(above == m - 1) | 1ull << 63));
+    }
+    first = false;
+    if (least == -kInf && W > 1) least = __shfl(sort_lanes(seen), (int)k - 1);  // a wave without candidates
+    if (least > bound) {
+      bound = least;
       bound_at = ~0u;
     }
   }
@@ -210,8 +296,9 @@ struct Tops {
     const uint64_t who = __ballot(in);
     if (who == 0) return;
     const uint32_t below = __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
-    if (in) held[count + below] = key_of(f, i);
+    if (in) sh.held[wave][count + below] = key_of(f, i);
     count += __popcll(who);
+    if (count >= 64) take();
   }
 
   // Joins the last 64 gathered ones, or all of fewer.
@@ -219,9 +306,9 @@ struct Tops {
     const uint32_t n = min(count, 64u);
     count -= n;
     wave_sync();
-    Key v = (uint32_t)lane < n ? held[count + lane] : 0;
-    v = sort_lanes(v, lane);
-    list = merge_lanes(list, __shfl(v, 63 - lane), lane);
+    const Key v = sort_lanes((uint32_t)lane < n ? sh.held[wave][count + lane] : 0);
+    list = taken ? merge_lanes(list, __shfl(v, 63 - lane)) : v;
+    taken = true;
     const Key last = __shfl(list, (int)k - 1);
     if (last) {
       const float at = value_of(last);
@@ -231,6 +318,50 @@ struct Tops {
       }
     }
     wave_sync();
+  }
+
+  // The team's list, in its first wave. Few elements are that wave's to sort;
+  // of many, every wave sorts its own, and pairs of lists are merged.
+  __device__ __forceinline__ void join() {
+    if (W == 1) {
+      while (count) take();
+      return;
+    }
+    if (lane == 0) sh.count[wave] = taken ? 1u << 16 : count;
+    __syncthreads();
+    uint32_t total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) total += sh.count[w];
+    if (total <= 128) {
+      if (wave) return;
+      for (uint32_t from = 0; from < total; from += 64) {
+        uint32_t at = from + lane;
+        Key v = 0;
+        bool found = false;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          if (!found && at < sh.count[w]) {
+            v = sh.held[w][at];
+            found = true;
+          }
+          if (!found) at -= sh.count[w];
+        }
+        v = sort_lanes(v);
+        list = from ? merge_lanes(list, __shfl(v, 63 - lane)) : v;
+      }
+      return;
+    }
+    while (count) take();
+    sh.held[wave][lane] = list;
+    __syncthreads();
+#pragma unroll
+    for (int n = W / 2; n > 0; n /= 2) {
+      if (wave < n) {
+        list = merge_lanes(list, sh.held[wave + n][63 - lane]);
+        if (n > 1) sh.held[wave][lane] = list;
+      }
+      if (n > 1) __syncthreads();
+    }
   }
 };
 
@@ -256,10 +387,13 @@ __device__ __forceinline__ void write_stats(const StatsArgs& a, uint32_t t, cons
   }
 }
 
+template <int NT, bool TOP>
+using TopsOf = Tops<NT / 64, TOP ? 128 : 1>;
+
 // One row, or a part of it, by a team: sums in r, the largest in the waves' lists.
 template <typename T, int NT, int NV, bool TOP>
 __device__ __forceinline__ void scan_row(const T* row, const Cut<T, NT>& cut, uint32_t y, uint32_t tid, const Scale& c,
-                                         Spread& r, Tops<64 * Io<T>::K>& tops) {
+                                         Spread& r, TopsOf<NT, TOP>& tops) {
   constexpr int K = Io<T>::K;
   const T* vecs = row + cut.head;
   const uint32_t yv = cut.vec_of(y), el = (y - cut.head) % K;
@@ -294,9 +428,11 @@ __device__ __forceinline__ void scan_row(const T* row, const Cut<T, NT>& cut, ui
       }
     }
     if (TOP) {
-      uint32_t some = 0;  // vectors in which some lane's maximum may pass
+      // vectors in which some lane's maximum may pass; the bound only rises
+      const float bound = fmaxf(tops.bound, -__FLT_MAX__);
+      uint32_t some = 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) some |= __any(mx[i] >= tops.bound && mx[i] > -kInf) ? 1u << i : 0u;
+      for (int i = 0; i < NV; ++i) some |= __any(mx[i] >= bound) ? 1u << i : 0u;
       while (some) {
         const int at = __builtin_ctz(some);
         some &= some - 1;
@@ -306,10 +442,18 @@ __device__ __forceinline__ void scan_row(const T* row, const Cut<T, NT>& cut, ui
           if (at == i) x = raw[i];
         float f[K];
         Io<T>::unpack(x, f);
-        const uint32_t v = c0 + at * NT + tid, base = cut.head + v * K;
+        uint32_t may = 0;  // this lane's elements
 #pragma unroll
-        for (int j = 0; j < K; ++j) tops.add(f[j], base + j, v < cut.end);
-        while (tops.count >= 64) tops.take();
+        for (int j = 0; j < K; ++j) may |= f[j] >= bound ? 1u << j : 0u;
+        const uint32_t base = cut.head + (c0 + at * NT + tid) * K;
+        while (__any(may != 0)) {
+          const uint32_t j = __builtin_ctz(may | 1u << 31);
+          float one = f[0];
+#pragma unroll
+          for (int i = 1; i < K; ++i) one = j == (uint32_t)i ? f[i] : one;
+          tops.add(one, base + j, may != 0);
+          may &= may - 1;
+        }
       }
     }
   }
@@ -318,30 +462,25 @@ __device__ __forceinline__ void scan_row(const T* row, const Cut<T, NT>& cut, ui
     float f = j < cut.singles() ? (float)row[i] : -kInf;
     if (TOP) {
       tops.add(f, i, j < cut.singles());
-      while (tops.count >= 64) tops.take();
     }
     if (i == y) f = -kInf;
     r.raise(f, c);
     r.sum<1, 1>(&f, c);
   }
-  if (TOP)
-    while (tops.count) tops.take();
+  if (TOP) tops.join();
 }
 
-template <int NT, bool TOP, int HELD>
+template <int W>
 struct StatsShared {
-  static constexpr int kWaves = Team<NT>::kBlock / 64;
-  float m[kWaves];
-  double s[kWaves], w[kWaves];
-  Key held[TOP ? kWaves : 1][TOP ? HELD : 1];
+  float m[W];
+  double s[W], w[W];
 };
 
 // Joins the waves of a team; the first wave gets it all.
-template <int NT, bool TOP, typename Sh>
-__device__ __forceinline__ void join_waves(Spread& r, Key& list, const Scale& c, Sh& sh) {
+template <int NT>
+__device__ __forceinline__ void join_waves(Spread& r, const Scale& c, StatsShared<NT / 64>& sh) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const float top = max_lanes(r.m);
-  join_lanes(r, top, c);
+  join_lanes(r, c);
   if (NT == 64) return;
   constexpr int W = NT / 64;
   if (lane == 0) {
@@ -349,33 +488,30 @@ __device__ __forceinline__ void join_waves(Spread& r, Key& list, const Scale& c,
     sh.s[wave] = r.s;
     sh.w[wave] = r.w;
   }
-  if (TOP) sh.held[wave][lane] = list;
   __syncthreads();
-  if (TOP) {
-#pragma unroll
-    for (int n = W / 2; n > 0; n /= 2) {
-      if (wave < n) {
-        list = merge_lanes(list, sh.held[wave + n][63 - lane], lane);
-        if (n > 1) sh.held[wave][lane] = list;
-      }
-      if (n > 1) __syncthreads();
-    }
-  }
   if (wave == 0) {
     r.m = lane < W ? sh.m[lane] : -kInf;
     r.s = lane < W ? sh.s[lane] : 0.0;
     r.w = lane < W ? sh.w[lane] : 0.0;
-    join_lanes(r, max_lanes(r.m), c);  // every lane gets it
+    join_lanes(r, c);  // every lane gets it
   }
 }
+
+// The teams' waves' LDS; without alternatives there is no list.
+template <int NT, bool TOP>
+struct StatsLds {
+  static constexpr int kTeams = NT == 64 ? Team<NT>::kBlock / 64 : 1;
+  StatsShared<NT / 64> sums;
+  typename TopsOf<NT, TOP>::Shared tops[TOP ? kTeams : 1];
+};
 
 template <typename T, int NT, int NV, bool TOP>
 __global__ __launch_bounds__(Team<NT>::kBlock) void stats_kernel(const StatsArgs a) {
   using Tm = Team<NT>;
-  constexpr int N = 64 * Io<T>::K;
-  __shared__ StatsShared<NT, TOP, Tops<N>::kHeld> sh;
+  __shared__ StatsLds<NT, TOP> sh;
   const uint32_t tid = Tm::thread(), t = Tm::row(a.first, blockIdx.x);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (t >= a.l.rows) return;  // a whole team
   const T* row = static_cast<const T*>(a.l.x) + (uint64_t)t * a.l.x_stride;
   const int64_t y64 = a.l.labels[t];
@@ -389,10 +525,10 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void stats_kernel(const StatsArgs
     const float xy = (float)row[y64];
     const Cut<T, NT> cut(row, a.l.vocab);
     Spread r;
-    Tops<N> tops(TOP ? sh.held[wave] : nullptr, a.out.k);
+    TopsOf<NT, TOP> tops(sh.tops[NT == 64 && TOP ? wave : 0], a.out.k, NT == 64 ? 0 : wave);
     scan_row<T, NT, NV, TOP>(row, cut, (uint32_t)y64, tid, a.c, r, tops);
     list = tops.list;
-    join_waves<NT, TOP>(r, list, a.c, sh);
+    join_waves<NT>(r, a.c, sh.sums);
     e = finish_stats(r, xy, a.c.inv_tau);
   }
   if (tid < 64) write_stats(a, t, e, list, lane);
@@ -409,21 +545,19 @@ constexpr uint32_t kStatsParts = 64;
 template <typename T, bool TOP>
 __global__ __launch_bounds__(256) void stats_part_kernel(const StatsArgs a, uint32_t parts, uint32_t size,
                                                          StatsPartial* partial, Key* lists) {
-  constexpr int NT = 256, NV = 4, N = 64 * Io<T>::K;
-  __shared__ StatsShared<NT, TOP, Tops<N>::kHeld> sh;
+  constexpr int NT = 256, NV = 4;
+  __shared__ StatsLds<NT, TOP> sh;
   const uint32_t tid = threadIdx.x, t = blockIdx.x / parts;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t y64 = a.l.labels[t];
   if (y64 < 0 || y64 >= (int64_t)a.l.vocab) return;
   const T* row = static_cast<const T*>(a.l.x) + (uint64_t)t * a.l.x_stride;
   const Cut<T, NT> cut(row, a.l.vocab, blockIdx.x % parts, size);
   Spread r;
-  Tops<N> tops(TOP ? sh.held[wave] : nullptr, a.out.k);
+  TopsOf<NT, TOP> tops(sh.tops[0], a.out.k, __builtin_amdgcn_readfirstlane(tid >> 6));
   scan_row<T, NT, NV, TOP>(row, cut, (uint32_t)y64, tid, a.c, r, tops);
-  Key list = tops.list;
-  join_waves<NT, TOP>(r, list, a.c, sh);
+  join_waves<NT>(r, a.c, sh.sums);
   if (tid == 0) partial[blockIdx.x] = StatsPartial{r.s, r.w, r.m};
-  if (TOP && tid < 64) lists[(uint64_t)blockIdx.x * 64 + lane] = list;
+  if (TOP && tid < 64) lists[(uint64_t)blockIdx.x * 64 + tid] = tops.list;
 }
 
 template <typename T, bool TOP>
@@ -438,13 +572,13 @@ __global__ __launch_bounds__(512) void stats_join_kernel(const StatsArgs a, uint
   Key list = 0;
   if (TOP && reads) {
     for (uint32_t p = wave; p < parts; p += W)
-      list = merge_lanes(list, lists[((uint64_t)t * parts + p) * 64 + 63 - lane], lane);
+      list = merge_lanes(list, lists[((uint64_t)t * parts + p) * 64 + 63 - lane]);
     held[wave][lane] = list;
     __syncthreads();
 #pragma unroll
     for (int n = W / 2; n > 0; n /= 2) {
       if (wave < n) {
-        list = merge_lanes(list, held[wave + n][63 - lane], lane);
+        list = merge_lanes(list, held[wave + n][63 - lane]);
         held[wave][lane] = list;
       }
       __syncthreads();
@@ -464,7 +598,7 @@ __global__ __launch_bounds__(512) void stats_join_kernel(const StatsArgs a, uint
       r.w = p.w;
       r.m = p.m;
     }
-    join_lanes(r, max_lanes(r.m), a.c);
+    join_lanes(r, a.c);
     e = finish_stats(r, (float)(static_cast<const T*>(a.l.x) + (uint64_t)t * a.l.x_stride)[y64], a.c.inv_tau);
   }
   write_stats(a, t, e, list, lane);
@@ -541,11 +675,21 @@ hipError_t stats_n(const StatsArgs& a, hipStream_t s) {
   });
 }
 
+// Whether rows are shared by workgroups: so few that one to a row leaves much of
+// the chip idle, and longer than one of 1024 threads takes in a round (1 x 32768
+// bf16: 15.5 us by one workgroup, 18.5 us shared). Calls with 20 alternatives,
+// shared against not: 64 x 131072 bf16 21.5 us against 32.5 us, 100 rows 24.8
+// against 32.8, but 200 rows 34.2 against 32.6.
+constexpr uint32_t kStatsShared = 128;
+constexpr uint32_t kOneRound = 4096;  // vectors
+
 bool shared_stats(const Logits& l) {
-  return l.rows < kSharedRows && l.vocab / (l.kind == kF32 ? 4 : 8) > 256 * 4;
+  return l.rows < kStatsShared && l.vocab / (l.kind == kF32 ? 4 : 8) > kOneRound;
 }
 
-uint32_t stats_parts(const Logits& l) { return std::min(l.vocab / (l.kind == kF32 ? 4 : 8) / 512, kStatsParts); }
+uint32_t stats_parts(const Logits& l) {
+  return std::min({l.vocab / (l.kind == kF32 ? 4 : 8) / 512, kStatsParts, 2048 / std::max(l.rows, 1u)});
+}
 
 template <typename T>
 hipError_t stats_t(const StatsArgs& a, void* ws, hipStream_t s) {
@@ -569,7 +713,16 @@ hipError_t stats_t(const StatsArgs& a, void* ws, hipStream_t s) {
     return hipGetLastError();
   }
   if (nv <= 64 * 4) return stats_n<T, 64, 4>(a, s);
+  // Small teams where rows are many, as for log-probabilities: more of them are in
+  // a compute unit while others sort (20 alternatives, teams of 64 threads against
+  // 256: 30000 x 2500 bf16 77 us against 194 us, 8000 x 8000 53 against 70; of 256
+  // against 512: 4096 x 131072 fp16 250 against 300, but 300 x 131072 64 against 46).
+  if (a.l.rows >= 1024) {
+    if (nv <= 64 * 16) return stats_n<T, 64, 8>(a, s);
+    return stats_n<T, 256, 8>(a, s);
+  }
   if (nv <= 256 * 4) return stats_n<T, 256, 4>(a, s);
+  if (a.l.rows < kFewRows && nv <= kOneRound) return stats_n<T, 1024, 4>(a, s);
   return stats_n<T, 512, 8>(a, s);
 }
 
