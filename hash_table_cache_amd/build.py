@@ -29,7 +29,7 @@ MIXED_LIB_PATH = PKG / "_lib" / "libhkv_mixed.so"
 # the training operators (include/hkv_train.h), a library of their own: they
 # work on logits and gradients and hold no table
 TRAIN_SOURCES = [CSRC / "hkv_train_kernels.hip", CSRC / "hkv_train_stats.hip", CSRC / "hkv_train_polar.hip",
-                 CSRC / "hkv_train.cpp"]
+                 CSRC / "hkv_train_narrow.hip", CSRC / "hkv_train.cpp"]
 TRAIN_LIB_PATH = PKG / "_lib" / "libhkv_train.so"
 ARCH = "gfx950"
 

@@ -124,9 +124,18 @@ __host__ __device__ constexpr uint64_t chunk_elems(uint32_t kind) { return kChun
 hipError_t launch_clip(Tensor* t, uint32_t tensors, double max_norm, float* norm, void* ws, hipStream_t s);
 
 
+// Whether a result is computed with two halves a number.
+inline bool splits(const PolarMatrix& m) { return m.out_kind != kBF16; }
+
 uint64_t polar_workspace_bytes(const PolarMatrix* m, uint32_t n);
 // coefficients: three numbers a step, in host memory.
 hipError_t launch_polar(const PolarMatrix* m, uint32_t n, const PolarRule& r, const double* coefficients,
                         uint32_t steps, void* ws, hipStream_t s);
+
+// Matrices whose shorter side is at most 64 have kernels of their own.
+bool is_narrow(const PolarMatrix& m);
+uint64_t narrow_workspace_bytes(const PolarMatrix* m, uint32_t n);
+hipError_t launch_narrow(const PolarMatrix* m, uint32_t n, const PolarRule& r, const double* coefficients,
+                         uint32_t steps, void* ws, hipStream_t s);
 
 }  // namespace hkvt
