@@ -4,9 +4,8 @@
 // The steps are those of the general kernels, which would take three launches for
 // each, of a few workgroups that wait for memory most of their time. With p <= 64
 // rows, A and B fit one workgroup's LDS, and the columns of X need each other only
-// in A: a wave keeps 64 columns of X in registers, in 32 bits, from step to step,
-//   A = sum over the waves of X_w X_w^T,   X_w <- a X_w + B X_w.
-// Up to 256 columns are one workgroup's: all steps in one launch (64 x 64 bf16: 23
+// in A: a wave keeps 16 columns of X in registers, in 32 bits, from step to step.
+// Up to 256 columns are one workgroup's: all steps in one launch (64 x 64 bf16: 18
 // us against 87 us of 18 launches). Longer rows are blocks of 256 columns. A launch
 // takes all blocks through the end of one step and the beginning of the next, A's
 // partial sums go through memory, and every workgroup squares A for itself; from
@@ -27,13 +26,15 @@ constexpr uint32_t kBlockCols = 256;
 constexpr uint32_t kManyBlocks = 4;
 constexpr uint32_t kMostBlocks = 256;
 constexpr uint32_t kDirectItems = 16;
-constexpr uint32_t kElems = 64 * 64;  // of A
+constexpr int kNarrowThreads = 1024;
+constexpr uint32_t kFragments = 10 * 64;  // A's fragments on and above the diagonal, four elements a lane
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 struct NarrowItem {
   PolarMatrix m;
   float* image;   // X between launches, as the threads hold it
-  float* sums;    // [2][blocks][64][64]: partial sums of A, of this step and of the next
-  float* joined;  // [64][64]: A
+  f32x4* sums;    // [2][blocks][kFragments]: partial sums of A, of this step and of the next
+  f32x4* joined;  // [kFragments]: A
   double* partial;
   uint32_t flip;  // rows > cols: X is the transpose
   uint32_t blocks;
@@ -73,122 +74,97 @@ __global__ void narrow_upload_kernel(const DirectItems u, NarrowItem* to, uint32
     reinterpret_cast<uint32_t*>(to)[i] = reinterpret_cast<const uint32_t*>(&u)[i];
 }
 
-// A workgroup's block: 4 waves of 64 columns, R * 32 rows. A thread holds, of each
-// fragment (i, j) of 32 x 32, column j * 32 + lane % 32 and four rows at a time.
-template <int R, bool SPLIT>
+// A workgroup's block: 16 waves of 16 columns, F * 16 rows. A thread holds, of each
+// fragment of 16 x 16, column lane % 16 and rows 4 (lane / 16) .. + 3. (4 waves of
+// 64 columns, with a part of A from each, took three times as long: a wave alone on
+// its SIMD issues an instruction every four cycles, and most of a step is bringing
+// X into halves. 64 x 64: 6.5 us a step.)
+template <int F, bool SPLIT>
 struct Narrow {
-  static constexpr int P = R * 32;
-  static constexpr int KS = P / 16;  // sixteens of rows
+  static constexpr int P = F * 16;
+  static constexpr int kUpper = F * (F + 1) / 2;  // fragments of A on and above the diagonal
   static constexpr int planes = SPLIT ? 2 : 1;
   struct Shared {
-    f16x8 wave[4][2][64 * 8];  // halves of a wave's X, by rows or by columns; or its part of A
+    union {
+      float cells[64 * kBlockCols];        // X on its way from or to memory
+      f16x8 rows[2][64 * kBlockCols / 8];  // halves of X by rows, for A
+      f16x8 cols[2][64 * kBlockCols / 8];  // by columns, for B X
+    };
     f16x8 a[2][64 * 8], b[2][64 * 8];
     float d[64], e[64];
-    double sum[4];
+    double sum[kNarrowThreads / 64];
   };
-  f32x16 x[R][2];
+  f32x4 x[F];
   Shared& sh;
-  uint32_t lane, wave, n0;
+  uint32_t lane, wave, block, cols;  // cols: of this block
 
-  __device__ __forceinline__ Narrow(Shared& sh_, uint32_t block)
-      : sh(sh_), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) {
-    n0 = block * kBlockCols + wave * 64;
+  __device__ __forceinline__ Narrow(Shared& sh_, const NarrowItem& it, uint32_t block_)
+      : sh(sh_), lane(threadIdx.x & 63), wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), block(block_) {
+    cols = min((it.flip ? it.m.rows : it.m.cols) - block * kBlockCols, kBlockCols);
   }
+  __device__ __forceinline__ uint32_t row(int i) const { return i * 16 + (lane >> 4) * 4; }
+  __device__ __forceinline__ uint32_t col() const { return wave * 16 + (lane & 15); }
 
-  // use(row, column of the wave, fragment, quad) for a thread's quads.
+  // use(row and column of the matrix, cell of X) for a thread's elements of the
+  // block: lanes go along rows of memory, which are rows or, flip, columns of X.
+  static __device__ __forceinline__ uint32_t cell(uint32_t r, uint32_t c) { return r * kBlockCols + (c ^ (r & 31)); }
+
   template <typename Use>
-  __device__ __forceinline__ void quads(Use&& use) const {
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) use(i * 32 + g * 8 + (lane >> 5) * 4, j * 32 + (lane & 31), i, j, g);
+  __device__ __forceinline__ void cells(const PolarMatrix& m, bool flip, Use&& use) const {
+    const uint32_t across = flip ? 64 : kBlockCols;
+#pragma unroll 8
+    for (uint32_t e = threadIdx.x; e < P * kBlockCols; e += kNarrowThreads) {
+      const uint32_t a = e / across, b = e % across, r = flip ? b : a, c = flip ? a : b;
+      if (c < cols && r < (flip ? m.cols : m.rows))
+        use(flip ? (uint64_t)block * kBlockCols + c : r, flip ? r : block * kBlockCols + c, cell(r, c));
+    }
   }
 
-  // The block's elements of a matrix of X's shape (or, flip, its transpose's).
-  template <typename T>
-  __device__ __forceinline__ void gather(const T* p, uint64_t stride, const PolarMatrix& m, bool flip, f32x16 (&to)[R][2]) const {
-    quads([&](uint32_t r, uint32_t c, int i, int j, int g) {
-      const uint32_t n = n0 + c;
-      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (flip) {
-        if (n < m.rows && r < m.cols) load_few(p + n * stride + r, min(m.cols - r, 4u), v);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (r + k < m.rows && n < m.cols) v[k] = (float)p[(r + k) * stride + n];
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) to[i][j][g * 4 + k] = v[k];
-    });
+  // X from the update, and the sum of its squares over the thread's elements. MOVE:
+  // the momentum takes the gradient in.
+  template <bool MOVE, typename T>
+  __device__ __forceinline__ double update_of(const NarrowItem& it, const PolarRule& r, const T* in) {
+    const PolarMatrix& m = it.m;
+    double sum = 0.0;
+    if (!m.momentum) {
+      cells(m, it.flip, [&](uint64_t row, uint32_t col, uint32_t at) {
+        const double u = (float)in[row * m.in_stride + col];
+        sum += u * u;
+        sh.cells[at] = (float)u;
+      });
+    } else if (MOVE || r.nesterov) {
+      cells(m, it.flip, [&](uint64_t row, uint32_t col, uint32_t at) {
+        const double g = (float)in[row * m.in_stride + col];
+        float* s = m.momentum + row * m.momentum_stride + col;
+        float v = *s;
+        if (MOVE) *s = v = (float)(r.momentum * (double)v + (1.0 - r.momentum) * g);
+        const double u = r.nesterov ? (1.0 - r.momentum) * g + r.momentum * (double)v : (double)v;
+        sum += u * u;
+        sh.cells[at] = (float)u;
+      });
+    } else {
+      cells(m, it.flip, [&](uint64_t row, uint32_t col, uint32_t at) { sh.cells[at] = m.momentum[row * m.momentum_stride + col]; });
+    }
+    return sum;
   }
 
-  template <typename T>
-  __device__ __forceinline__ void scatter(T* p, uint64_t stride, const PolarMatrix& m, bool flip, const f32x16 (&from)[R][2]) const {
-    quads([&](uint32_t r, uint32_t c, int i, int j, int g) {
-      const uint32_t n = n0 + c;
-      float v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = from[i][j][g * 4 + k];
-      if (flip) {
-        if (n < m.rows && r < m.cols) store_few(p + n * stride + r, min(m.cols - r, 4u), v);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (r + k < m.rows && n < m.cols) p[(r + k) * stride + n] = (T)v[k];
-      }
-    });
-  }
-
-  __device__ __forceinline__ void gather_kind(const void* p, uint32_t kind, uint64_t stride, const PolarMatrix& m, bool flip,
-                                              f32x16 (&to)[R][2]) const {
-    if (kind == kF32)
-      gather(static_cast<const float*>(p), stride, m, flip, to);
-    else if (kind == kBF16)
-      gather(static_cast<const __bf16*>(p), stride, m, flip, to);
-    else
-      gather(static_cast<const _Float16*>(p), stride, m, flip, to);
-  }
-
-  // The update, and the sum of its squares over the workgroup. MOVE: the momentum
-  // takes the gradient in.
   template <bool MOVE>
   __device__ __forceinline__ double update(const NarrowItem& it, const PolarRule& r) {
-    const PolarMatrix& m = it.m;
-    if (MOVE || !m.momentum || r.nesterov) gather_kind(m.in, m.in_kind, m.in_stride, m, it.flip, x);
-    double sum = 0.0;
-    if (m.momentum) {
-      f32x16 s[R][2];
-      gather(m.momentum, m.momentum_stride, m, it.flip, s);
-      if (MOVE) {
+    for (uint32_t e = threadIdx.x; e < P * kBlockCols; e += kNarrowThreads) sh.cells[e] = 0.0f;
+    __syncthreads();
+    const void* in = it.m.in;
+    double sum;
+    if (it.m.in_kind == kF32)
+      sum = update_of<MOVE>(it, r, static_cast<const float*>(in));
+    else if (it.m.in_kind == kBF16)
+      sum = update_of<MOVE>(it, r, static_cast<const __bf16*>(in));
+    else
+      sum = update_of<MOVE>(it, r, static_cast<const _Float16*>(in));
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+    for (int i = 0; i < F; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              s[i][j][k] = (float)(r.momentum * (double)s[i][j][k] + (1.0 - r.momentum) * (double)x[i][j][k]);
-        scatter(m.momentum, m.momentum_stride, m, it.flip, s);
-      }
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const double u = r.nesterov ? (1.0 - r.momentum) * (double)x[i][j][k] + r.momentum * (double)s[i][j][k] : (double)s[i][j][k];
-            sum += u * u;
-            x[i][j][k] = (float)u;
-          }
-    } else {
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int k = 0; k < 16; ++k) sum += (double)x[i][j][k] * (double)x[i][j][k];
-    }
+      for (int k = 0; k < 4; ++k) x[i][k] = sh.cells[cell(row(i) + k, col())];
     return sum;
   }
 
@@ -197,235 +173,235 @@ struct Narrow {
     const double norm = sqrt(squares);
     const double f = norm < (double)kInf ? kUnit / fmax(norm, eps) : __builtin_nan("");
 #pragma unroll
-    for (int i = 0; i < R; ++i)
+    for (int i = 0; i < F; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[i][j][k] = (float)((double)x[i][j][k] * f);
+      for (int k = 0; k < 4; ++k) x[i][k] = (float)((double)x[i][k] * f);
   }
 
-  // 16 bytes of halves `piece` of row r of an array of 64 halves a row: shuffled so
-  // that reading one piece of 32 rows meets all banks.
-  static __device__ __forceinline__ uint32_t place(uint32_t r, uint32_t piece) { return r * 8 + (piece ^ ((r >> 1) & 7)); }
-  static __device__ __forceinline__ _Float16& half_at(f16x8* to, uint32_t r, uint32_t c) {
-    return reinterpret_cast<_Float16*>(to + place(r, c >> 3))[c & 7];
+  // Pieces of 16 bytes of rows of halves, shuffled so that reading a piece of each of
+  // 16 rows meets all banks: rows of 256 halves, and of 64.
+  static __device__ __forceinline__ uint32_t wide(uint32_t r, uint32_t piece) { return r * 32 + (piece ^ (r & 15)); }
+  static __device__ __forceinline__ uint32_t slim(uint32_t r, uint32_t piece) { return r * 8 + (piece ^ ((r >> 1) & 7)); }
+  static __device__ __forceinline__ _Float16& half_at(f16x8* to, uint32_t place, uint32_t c) {
+    return reinterpret_cast<_Float16*>(to + place)[c & 7];
   }
   static __device__ __forceinline__ f16x4& quad_at(f16x8* to, uint32_t r, uint32_t c) {
-    return *reinterpret_cast<f16x4*>(reinterpret_cast<_Float16*>(to + place(r, c >> 3)) + (c & 7));
+    return *reinterpret_cast<f16x4*>(reinterpret_cast<_Float16*>(to + slim(r, c >> 3)) + (c & 7));
   }
 
-  static __device__ __forceinline__ f32x16 product(f32x16 acc, const f16x8* a, const f16x8* b) {
+  static __device__ __forceinline__ f32x4 product(f32x4 acc, const f16x8* a, const f16x8* b) {
     if (SPLIT) {
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[1], b[0], acc, 0, 0, 0);
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(a[0], b[1], acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[1], b[0], acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], b[1], acc, 0, 0, 0);
     }
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a[0], b[0], acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], b[0], acc, 0, 0, 0);
   }
 
-  static __device__ __forceinline__ void read(const f16x8 (*from)[64 * 8], uint32_t r, uint32_t piece, f16x8* to) {
+  // Fragment f of A on or above the diagonal.
+  __device__ __forceinline__ void upper(uint32_t f, uint32_t* i, uint32_t* j) const {
+    uint32_t c = 0;
 #pragma unroll
-    for (int p = 0; p < planes; ++p) to[p] = from[p][place(r, piece)];
+    for (uint32_t k = 1; k < F; ++k) c = f >= k * (k + 1) / 2 ? k : c;
+    *j = c;
+    *i = f - c * (c + 1) / 2;
   }
 
-  static __device__ __forceinline__ void wave_sync() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  }
-
-  // The wave's part of A, into its LDS: the fragments on and above the diagonal.
-  __device__ __forceinline__ void gram() {
-    f16x8(*own)[64 * 8] = sh.wave[wave];
-    wave_sync();
-    quads([&](uint32_t r, uint32_t c, int i, int j, int g) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float v = x[i][j][g * 4 + k];
-        const _Float16 hi = (_Float16)v;
-        half_at(own[0], r + k, c) = hi;
-        if (SPLIT) half_at(own[1], r + k, c) = (_Float16)(v - (float)hi);
-      }
-    });
-    wave_sync();
-    f32x16 s[R][R] = {};
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      f16x8 f[R][2];
-#pragma unroll
-      for (int i = 0; i < R; ++i) read(own, i * 32 + (lane & 31), ks * 2 + (lane >> 5), f[i]);
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = i; j < R; ++j) s[i][j] = product(s[i][j], f[i], f[j]);
-    }
-    wave_sync();
-    float* part = reinterpret_cast<float*>(own);
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int j = i; j < R; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            part[(i * 32 + g * 8 + (lane >> 5) * 4 + k) * P + j * 32 + (lane & 31)] = s[i][j][g * 4 + k];
-  }
-
-  // use(row, column, sum over the waves) for a thread's elements of A.
-  template <typename Use>
-  __device__ __forceinline__ void join(Use&& use) {
+  // The block's part of A: a fragment a wave, of all columns. The first waves have one.
+  __device__ __forceinline__ f32x4 gram() {
     __syncthreads();
-#pragma unroll 4
-    for (uint32_t e = threadIdx.x; e < P * P; e += kPolarThreads) {
-      const uint32_t r = e / P, c = e % P;
-      const uint32_t at = r / 32 > c / 32 ? c * P + r : e;
-      float v = 0.0f;
+    if (wave * 16 < cols) {
 #pragma unroll
-      for (int w = 0; w < 4; ++w) v += reinterpret_cast<const float*>(sh.wave[w])[at];
-      use(r, c, v);
+      for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const _Float16 hi = (_Float16)x[i][k];
+          const uint32_t place = wide(row(i) + k, col() >> 3);
+          half_at(sh.rows[0], place, col()) = hi;
+          if (SPLIT) half_at(sh.rows[1], place, col()) = (_Float16)(x[i][k] - (float)hi);
+        }
+    } else if (wave % 2 && wave * 16 < cols + 16) {  // the rest of 32 columns
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t place = wide(row(i) + k, col() >> 3);
+          half_at(sh.rows[0], place, col()) = (_Float16)0.0f;
+          if (SPLIT) half_at(sh.rows[1], place, col()) = (_Float16)0.0f;
+        }
     }
+    __syncthreads();
+    f32x4 s = {};
+    if (wave < kUpper) {
+      uint32_t i, j;
+      upper(wave, &i, &j);
+      const uint32_t ra = i * 16 + (lane & 15), rb = j * 16 + (lane & 15), end = (cols + 31) / 32;
+#pragma unroll 2
+      for (uint32_t ks = 0; ks < end; ++ks) {
+        f16x8 fa[2], fb[2];
+#pragma unroll
+        for (int p = 0; p < planes; ++p) {
+          fa[p] = sh.rows[p][wide(ra, ks * 4 + (lane >> 4))];
+          fb[p] = sh.rows[p][wide(rb, ks * 4 + (lane >> 4))];
+        }
+        s = product(s, fa, fb);
+      }
+    }
+    return s;
   }
 
-  // An element of A goes to LDS as halves, the diagonal apart.
-  __device__ __forceinline__ void take(uint32_t r, uint32_t c, float sum) {
-    float v = sum * (1.0f / kUnit);
-    if (r == c) {
-      sh.d[r] = v * (1.0f / kUnit);
-      v = 0.0f;
+  // The wave's fragment of A, summed over the blocks, goes to LDS as halves, the
+  // diagonal apart.
+  __device__ __forceinline__ void take(f32x4 s) {
+    if (wave >= kUpper) return;
+    uint32_t i, j;
+    upper(wave, &i, &j);
+    const uint32_t r = i * 16 + (lane >> 4) * 4, c = j * 16 + (lane & 15);
+    float v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[k] = s[k] * (1.0f / kUnit);
+      if (r + k == c) {
+        sh.d[c] = v[k] * (1.0f / kUnit);
+        v[k] = 0.0f;
+      }
     }
-    const _Float16 hi = (_Float16)v;
-    half_at(sh.a[0], r, c) = hi;
-    if (SPLIT) half_at(sh.a[1], r, c) = (_Float16)(v - (float)hi);
+    const f16x4 hi = upper_halves(v), lo = lower_halves(v);
+    quad_at(sh.a[0], c, r) = hi;
+    if (SPLIT) quad_at(sh.a[1], c, r) = lo;
+    if (i == j) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      half_at(sh.a[0], slim(r + k, c >> 3), c) = hi[k];
+      if (SPLIT) half_at(sh.a[1], slim(r + k, c >> 3), c) = lo[k];
+    }
   }
 
   // B without its diagonal, and E, from A: a fragment a wave.
   __device__ __forceinline__ void square(float b, float c2) {
     __syncthreads();
-    if (wave < R * R) {
-      const uint32_t i = wave / R, j = wave % R;
-      f32x16 s = {};
+    if (wave < F * F) {
+      const uint32_t i = wave / F, j = wave % F;
+      f32x4 s = {};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
+      for (int ks = 0; ks < P / 32; ++ks) {
         f16x8 fa[2], fb[2];
-        read(sh.a, i * 32 + (lane & 31), ks * 2 + (lane >> 5), fa);
-        read(sh.a, j * 32 + (lane & 31), ks * 2 + (lane >> 5), fb);
+#pragma unroll
+        for (int p = 0; p < planes; ++p) {
+          fa[p] = sh.a[p][slim(i * 16 + (lane & 15), ks * 4 + (lane >> 4))];
+          fb[p] = sh.a[p][slim(j * 16 + (lane & 15), ks * 4 + (lane >> 4))];
+        }
         s = product(s, fa, fb);
       }
-      const uint32_t col = j * 32 + (lane & 31);
-      const float dc = sh.d[col];
+      const uint32_t r = i * 16 + (lane >> 4) * 4, c = j * 16 + (lane & 15);
+      const float dc = sh.d[c];
+      const f16x4 hi = quad_at(sh.a[0], c, r);  // A is symmetric
+      f16x4 lo = {};
+      if (SPLIT) lo = quad_at(sh.a[1], c, r);
+      float v[4];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const uint32_t row = i * 32 + g * 8 + (lane >> 5) * 4;
-        const f16x4 hi = quad_at(sh.a[0], col, row);  // A is symmetric
-        f16x4 lo = {};
-        if (SPLIT) lo = quad_at(sh.a[1], col, row);
-        float v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float a = (float)hi[k] + (float)lo[k];
-          v[k] = fmaf(fmaf(c2, sh.d[row + k] + dc, b), a, s[g * 4 + k] * (c2 / kUnit));
-          if (row + k == col) {
-            sh.e[col] = fmaf(c2, dc * dc, fmaf(b, dc, v[k] * (1.0f / kUnit)));
-            v[k] = 0.0f;
-          }
+      for (int k = 0; k < 4; ++k) {
+        v[k] = fmaf(fmaf(c2, sh.d[r + k] + dc, b), (float)hi[k] + (float)lo[k], s[k] * (c2 / kUnit));
+        if (r + k == c) {
+          sh.e[c] = fmaf(c2, dc * dc, fmaf(b, dc, v[k] * (1.0f / kUnit)));
+          v[k] = 0.0f;
         }
-        quad_at(sh.b[0], col, row) = upper_halves(v);
-        if (SPLIT) quad_at(sh.b[1], col, row) = lower_halves(v);
       }
+      quad_at(sh.b[0], c, r) = upper_halves(v);
+      if (SPLIT) quad_at(sh.b[1], c, r) = lower_halves(v);
     }
     __syncthreads();
   }
 
-  // X <- a X + B X.
+  // X <- a X + B X: every wave its own columns.
   __device__ __forceinline__ void next(float a) {
-    f16x8(*own)[64 * 8] = sh.wave[wave];
-    wave_sync();
-    quads([&](uint32_t r, uint32_t c, int i, int j, int g) {
+    if (wave * 16 >= cols) return;
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
       float v[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = x[i][j][g * 4 + k];
-      quad_at(own[0], c, r) = upper_halves(v);
-      if (SPLIT) quad_at(own[1], c, r) = lower_halves(v);
-    });
-    wave_sync();
-    f32x16 s[R][2] = {};
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      f16x8 fb[R][2], fx[2][2];
-#pragma unroll
-      for (int i = 0; i < R; ++i) read(sh.b, i * 32 + (lane & 31), ks * 2 + (lane >> 5), fb[i]);
-#pragma unroll
-      for (int j = 0; j < 2; ++j) read(own, j * 32 + (lane & 31), ks * 2 + (lane >> 5), fx[j]);
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) s[i][j] = product(s[i][j], fb[i], fx[j]);
+      for (int k = 0; k < 4; ++k) v[k] = x[i][k];
+      quad_at(sh.cols[0], col(), row(i)) = upper_halves(v);
+      if (SPLIT) quad_at(sh.cols[1], col(), row(i)) = lower_halves(v);
     }
-    quads([&](uint32_t r, uint32_t, int i, int j, int g) {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    f32x4 s[F] = {};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int e = g * 4 + k;
-        x[i][j][e] = fmaf(a + sh.e[r + k], x[i][j][e], s[i][j][e] * (1.0f / kUnit));
+    for (int ks = 0; ks < P / 32; ++ks) {
+      f16x8 fx[2];
+#pragma unroll
+      for (int p = 0; p < planes; ++p) fx[p] = sh.cols[p][slim(col(), ks * 4 + (lane >> 4))];
+#pragma unroll
+      for (int i = 0; i < F; ++i) {
+        f16x8 fb[2];
+#pragma unroll
+        for (int p = 0; p < planes; ++p) fb[p] = sh.b[p][slim(i * 16 + (lane & 15), ks * 4 + (lane >> 4))];
+        s[i] = product(s[i], fb, fx);
       }
-    });
+    }
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[i][k] = fmaf(a + sh.e[row(i) + k], x[i][k], s[i][k] * (1.0f / kUnit));
   }
 
   // The result, to the matrix or into the weights.
-  __device__ __forceinline__ void write(const NarrowItem& it) {
+  template <typename T>
+  __device__ __forceinline__ void write_to(const NarrowItem& it, T* out) const {
     const PolarMatrix& m = it.m;
-    f32x16 old[R][2];
-    if (m.momentum) gather_kind(m.out, m.out_kind, m.out_stride, m, it.flip, old);
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float o = x[i][j][k] * (1.0f / kUnit);
-          x[i][j][k] = m.momentum ? (float)(m.keep * (double)old[i][j][k] + m.step * (double)o) : o;
-        }
-    if (m.out_kind == kF32)
-      scatter(static_cast<float*>(m.out), m.out_stride, m, it.flip, x);
-    else if (m.out_kind == kBF16)
-      scatter(static_cast<__bf16*>(m.out), m.out_stride, m, it.flip, x);
+    if (m.momentum)
+      cells(m, it.flip, [&](uint64_t row, uint32_t col, uint32_t at) {
+        T* w = out + row * m.out_stride + col;
+        *w = (T)(float)(m.keep * (double)(float)*w + m.step * (double)(sh.cells[at] * (1.0f / kUnit)));
+      });
     else
-      scatter(static_cast<_Float16*>(m.out), m.out_stride, m, it.flip, x);
+      cells(m, it.flip, [&](uint64_t row, uint32_t col, uint32_t at) {
+        out[row * m.out_stride + col] = (T)(sh.cells[at] * (1.0f / kUnit));
+      });
   }
 
-  __device__ __forceinline__ u32x4* image(const NarrowItem& it, uint32_t block) const {
-    return reinterpret_cast<u32x4*>(it.image) + ((uint64_t)block * 4 + wave) * (R * 2 * 4 * 64) + lane;
-  }
-  __device__ __forceinline__ void keep(const NarrowItem& it, uint32_t block) const {
-    u32x4* to = image(it, block);
-    quads([&](uint32_t, uint32_t, int i, int j, int g) {
-      u32x4 v;
+  __device__ __forceinline__ void write(const NarrowItem& it) const {
+    __syncthreads();
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = __builtin_bit_cast(uint32_t, (float)x[i][j][g * 4 + k]);
-      to[((i * 2 + j) * 4 + g) * 64] = v;
-    });
-  }
-  __device__ __forceinline__ void recall(const NarrowItem& it, uint32_t block) {
-    const u32x4* from = image(it, block);
-    quads([&](uint32_t, uint32_t, int i, int j, int g) {
-      const u32x4 v = from[((i * 2 + j) * 4 + g) * 64];
+    for (int i = 0; i < F; ++i)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[i][j][g * 4 + k] = as_float(v[k]);
-    });
+      for (int k = 0; k < 4; ++k) sh.cells[cell(row(i) + k, col())] = x[i][k];
+    __syncthreads();
+    if (it.m.out_kind == kF32)
+      write_to(it, static_cast<float*>(it.m.out));
+    else if (it.m.out_kind == kBF16)
+      write_to(it, static_cast<__bf16*>(it.m.out));
+    else
+      write_to(it, static_cast<_Float16*>(it.m.out));
   }
+
+  __device__ __forceinline__ f32x4* image(const NarrowItem& it) const {
+    return reinterpret_cast<f32x4*>(it.image) + (uint64_t)block * F * kNarrowThreads + threadIdx.x;
+  }
+  __device__ __forceinline__ void keep(const NarrowItem& it) const {
+#pragma unroll
+    for (int i = 0; i < F; ++i) image(it)[i * kNarrowThreads] = x[i];
+  }
+  __device__ __forceinline__ void recall(const NarrowItem& it) {
+#pragma unroll
+    for (int i = 0; i < F; ++i) x[i] = image(it)[i * kNarrowThreads];
+  }
+  // Where the wave's fragment of a block's part of A lies.
+  __device__ __forceinline__ uint32_t fragment() const { return wave * 64 + lane; }
 };
 
 // All steps of matrices of one block.
-template <int R, bool SPLIT, typename List>
-__global__ __launch_bounds__(kPolarThreads) void narrow_whole_kernel(const List list, const PolarRule r, const NarrowSteps c) {
-  using N = Narrow<R, SPLIT>;
+template <int F, bool SPLIT, typename List>
+__global__ __launch_bounds__(kNarrowThreads) void narrow_whole_kernel(const List list, const PolarRule r, const NarrowSteps c) {
+  using N = Narrow<F, SPLIT>;
   __shared__ typename N::Shared sh;
   const NarrowItem it = list.at(blockIdx.x);
-  N w(sh, 0);
+  N w(sh, it, 0);
   const double sum = w.template update<true>(it, r);
-  w.scale(block_sum<kPolarThreads>(sum, sh.sum), r.eps);
+  w.scale(block_sum<kNarrowThreads>(sum, sh.sum), r.eps);
   for (uint32_t k = 0; k < c.steps; ++k) {
-    w.gram();
-    w.join([&](uint32_t row, uint32_t col, float v) { w.take(row, col, v); });
+    w.take(w.gram());
     w.square(c.c[3 * k + 1], c.c[3 * k + 2]);
     w.next(c.c[3 * k]);
   }
@@ -433,65 +409,60 @@ __global__ __launch_bounds__(kPolarThreads) void narrow_whole_kernel(const List 
 }
 
 // The beginning of the first step: X, and the blocks' parts of A.
-template <int R, bool SPLIT>
-__global__ __launch_bounds__(kPolarThreads) void narrow_first_kernel(const NarrowItem* items, uint32_t n, const PolarRule r) {
-  using N = Narrow<R, SPLIT>;
+template <int F, bool SPLIT>
+__global__ __launch_bounds__(kNarrowThreads) void narrow_first_kernel(const NarrowItem* items, uint32_t n, const PolarRule r) {
+  using N = Narrow<F, SPLIT>;
   __shared__ typename N::Shared sh;
   const NarrowItem& it = find_item(items, n, blockIdx.x, &NarrowItem::first_block);
   const uint32_t block = blockIdx.x - it.first_block;
-  N w(sh, block);
+  N w(sh, it, block);
   w.template update<false>(it, r);
   double sum = 0.0;
-  for (uint32_t i = threadIdx.x; i < it.parts; i += kPolarThreads) sum += it.partial[i];
-  w.scale(block_sum<kPolarThreads>(sum, sh.sum), r.eps);
-  w.keep(it, block);
-  w.gram();
-  float* to = it.sums + (uint64_t)block * kElems;
-  w.join([&](uint32_t row, uint32_t col, float v) { to[row * N::P + col] = v; });
+  for (uint32_t i = threadIdx.x; i < it.parts; i += kNarrowThreads) sum += it.partial[i];
+  w.scale(block_sum<kNarrowThreads>(sum, sh.sum), r.eps);
+  w.keep(it);
+  const f32x4 s = w.gram();
+  if (w.wave < N::kUpper) it.sums[(uint64_t)block * kFragments + w.fragment()] = s;
 }
 
-// A of matrices of many blocks, from the blocks' parts for a step: 256 elements a
-// workgroup.
-__global__ __launch_bounds__(kPolarThreads) void narrow_join_kernel(const NarrowItem* items, uint32_t elems, uint32_t step) {
+// A of matrices of many blocks, from the blocks' parts for a step: a fragment a
+// wave.
+__global__ __launch_bounds__(64) void narrow_join_kernel(const NarrowItem* items, uint32_t step) {
   const NarrowItem& it = items[blockIdx.y];
-  const uint32_t e = blockIdx.x * kPolarThreads + threadIdx.x;
-  if (e >= elems) return;
-  const float* from = it.sums + (uint64_t)(step & 1) * it.blocks * kElems + e;
-  float v = 0.0f;
+  const uint32_t at = blockIdx.x * 64 + threadIdx.x;
+  const f32x4* from = it.sums + (uint64_t)(step & 1) * it.blocks * kFragments + at;
+  f32x4 v = {};
 #pragma unroll 8
-  for (uint32_t b = 0; b < it.blocks; ++b) v += from[(uint64_t)b * kElems];
-  it.joined[e] = v;
+  for (uint32_t b = 0; b < it.blocks; ++b) v += from[(uint64_t)b * kFragments];
+  it.joined[at] = v;
 }
 
 // The end of a step, and the beginning of the next unless it is the last.
 // `joined`: A is there whole.
-template <int R, bool SPLIT>
-__global__ __launch_bounds__(kPolarThreads) void narrow_step_kernel(const NarrowItem* items, uint32_t n, float a, float b,
-                                                                    float c, uint32_t step, bool joined, bool last) {
-  using N = Narrow<R, SPLIT>;
+template <int F, bool SPLIT>
+__global__ __launch_bounds__(kNarrowThreads) void narrow_step_kernel(const NarrowItem* items, uint32_t n, float a, float b,
+                                                                     float c, uint32_t step, bool joined, bool last) {
+  using N = Narrow<F, SPLIT>;
   __shared__ typename N::Shared sh;
   const NarrowItem& it = find_item(items, n, blockIdx.x, &NarrowItem::first_block);
   const uint32_t block = blockIdx.x - it.first_block;
-  N w(sh, block);
-  w.recall(it, block);
-  const float* from = joined ? it.joined : it.sums + (uint64_t)(step & 1) * it.blocks * kElems;
-  const uint32_t parts = joined ? 1 : it.blocks;
-#pragma unroll 4
-  for (uint32_t e = threadIdx.x; e < N::P * N::P; e += kPolarThreads) {
-    float v = 0.0f;
-    for (uint32_t k = 0; k < parts; ++k) v += from[(uint64_t)k * kElems + e];
-    w.take(e / N::P, e % N::P, v);
+  N w(sh, it, block);
+  w.recall(it);
+  f32x4 s = {};
+  if (w.wave < N::kUpper) {
+    const f32x4* from = joined ? it.joined : it.sums + (uint64_t)(step & 1) * it.blocks * kFragments;
+    for (uint32_t k = 0; k < (joined ? 1 : it.blocks); ++k) s += from[(uint64_t)k * kFragments + w.fragment()];
   }
+  w.take(s);
   w.square(b, c);
   w.next(a);
   if (last) {
     w.write(it);
     return;
   }
-  w.keep(it, block);
-  w.gram();
-  float* to = it.sums + ((uint64_t)(~step & 1) * it.blocks + block) * kElems;
-  w.join([&](uint32_t row, uint32_t col, float v) { to[row * N::P + col] = v; });
+  w.keep(it);
+  s = w.gram();
+  if (w.wave < N::kUpper) it.sums[((uint64_t)(~step & 1) * it.blocks + block) * kFragments + w.fragment()] = s;
 }
 
 // The matrices of a launch: of one precision, number of fragments, and one block
@@ -522,9 +493,9 @@ uint64_t lay_out(const PolarMatrix& m, int fragments, char* at, NarrowItem* it) 
   it->blocks = blocks_of(m);
   norm_parts(m, &it->parts, &it->part_tiles);
   if (it->blocks == 1) return 0;
-  it->image = reinterpret_cast<float*>(take((uint64_t)it->blocks * kBlockCols * fragments * 32 * 4));
-  it->sums = reinterpret_cast<float*>(take((uint64_t)it->blocks * kElems * 4 * 2));
-  it->joined = reinterpret_cast<float*>(take(kElems * 4));
+  it->image = reinterpret_cast<float*>(take((uint64_t)it->blocks * kBlockCols * fragments * 16 * 4));
+  it->sums = reinterpret_cast<f32x4*>(take((uint64_t)it->blocks * kFragments * 16 * 2));
+  it->joined = reinterpret_cast<f32x4*>(take(kFragments * 16));
   it->partial = reinterpret_cast<double*>(take(it->parts * 8ull));
   return used;
 }
@@ -534,7 +505,7 @@ std::vector<NarrowGroup> make_groups(const PolarMatrix* m, uint32_t n) {
   for (int kind = 0; kind < 12; ++kind) {
     NarrowGroup g;
     g.split = kind & 1;
-    g.fragments = kind & 2 ? 2 : 1;
+    g.fragments = kind & 2 ? 4 : 2;
     g.one = kind / 4 == 0;
     g.many = kind / 4 == 2;
     uint64_t blocks = 0;
@@ -544,7 +515,7 @@ std::vector<NarrowGroup> make_groups(const PolarMatrix* m, uint32_t n) {
       g.bytes = blocks = 0;
     };
     for (uint32_t i = 0; i < n; ++i) {
-      const uint32_t b = blocks_of(m[i]), fragments = std::min(m[i].rows, m[i].cols) > 32 ? 2 : 1;
+      const uint32_t b = blocks_of(m[i]), fragments = std::min(m[i].rows, m[i].cols) > 32 ? 4 : 2;
       if (splits(m[i]) != g.split || (int)fragments != g.fragments || (b == 1) != g.one || (b > kManyBlocks) != g.many) continue;
       NarrowItem it;
       const uint64_t bytes = lay_out(m[i], g.fragments, nullptr, &it) + sizeof(NarrowItem);
@@ -558,7 +529,7 @@ std::vector<NarrowGroup> make_groups(const PolarMatrix* m, uint32_t n) {
   return groups;
 }
 
-template <int R, bool SPLIT>
+template <int F, bool SPLIT>
 hipError_t run_group(const PolarMatrix* m, const NarrowGroup& g, const PolarRule& r, const double* c, uint32_t steps,
                      char* ws, hipStream_t s) {
   const uint32_t n = (uint32_t)g.list.size();
@@ -586,22 +557,21 @@ hipError_t run_group(const PolarMatrix* m, const NarrowGroup& g, const PolarRule
     all.steps = steps;
     for (uint32_t k = 0; k < 3 * steps; ++k) all.c[k] = (float)c[k];
     if (n <= kDirectItems)
-      narrow_whole_kernel<R, SPLIT><<<n, kPolarThreads, 0, s>>>(direct, r, all);
+      narrow_whole_kernel<F, SPLIT><<<n, kNarrowThreads, 0, s>>>(direct, r, all);
     else
-      narrow_whole_kernel<R, SPLIT><<<n, kPolarThreads, 0, s>>>(StoredItems{stored}, r, all);
+      narrow_whole_kernel<F, SPLIT><<<n, kNarrowThreads, 0, s>>>(StoredItems{stored}, r, all);
     return hipGetLastError();
   }
   polar_norm_kernel<<<parts, kPolarThreads, 0, s>>>(stored, n, r);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  narrow_first_kernel<R, SPLIT><<<blocks, kPolarThreads, 0, s>>>(stored, n, r);
+  narrow_first_kernel<F, SPLIT><<<blocks, kNarrowThreads, 0, s>>>(stored, n, r);
   if ((e = hipGetLastError()) != hipSuccess) return e;
   for (uint32_t k = 0; k < steps; ++k, c += 3) {
     if (g.many) {
-      constexpr uint32_t elems = R * 32 * R * 32;
-      narrow_join_kernel<<<dim3(elems / kPolarThreads, n), kPolarThreads, 0, s>>>(stored, elems, k);
+      narrow_join_kernel<<<dim3(F * (F + 1) / 2, n), 64, 0, s>>>(stored, k);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    narrow_step_kernel<R, SPLIT><<<blocks, kPolarThreads, 0, s>>>(stored, n, (float)c[0], (float)c[1], (float)c[2], k, g.many,
+    narrow_step_kernel<F, SPLIT><<<blocks, kNarrowThreads, 0, s>>>(stored, n, (float)c[0], (float)c[1], (float)c[2], k, g.many,
                                                                    k + 1 == steps);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
@@ -623,10 +593,10 @@ hipError_t launch_narrow(const PolarMatrix* m, uint32_t n, const PolarRule& r, c
   char* at = static_cast<char*>(ws);
   for (const NarrowGroup& g : make_groups(m, n)) {
     hipError_t e;
-    if (g.fragments == 1)
-      e = g.split ? run_group<1, true>(m, g, r, coefficients, steps, at, s) : run_group<1, false>(m, g, r, coefficients, steps, at, s);
-    else
+    if (g.fragments == 2)
       e = g.split ? run_group<2, true>(m, g, r, coefficients, steps, at, s) : run_group<2, false>(m, g, r, coefficients, steps, at, s);
+    else
+      e = g.split ? run_group<4, true>(m, g, r, coefficients, steps, at, s) : run_group<4, false>(m, g, r, coefficients, steps, at, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
