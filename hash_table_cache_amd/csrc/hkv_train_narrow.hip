@@ -28,7 +28,6 @@ constexpr uint32_t kMostBlocks = 256;
 constexpr uint32_t kDirectItems = 16;
 constexpr int kNarrowThreads = 1024;
 constexpr uint32_t kFragments = 10 * 64;  // A's fragments on and above the diagonal, four elements a lane
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 struct NarrowItem {
   PolarMatrix m;

@@ -36,7 +36,7 @@
 namespace hkvt {
 namespace {
 
-constexpr uint32_t kUploads = 16;
+constexpr uint32_t kUploads = 15;
 constexpr uint32_t kDies = 8;
 
 // 16 bytes a lane from memory to LDS, to where the wave's first lane points and on.
@@ -56,19 +56,22 @@ struct PolarItem {
   float* d;        // [p]: diagonal of A
   float* e;        // [p]: diagonal of B
   double* partial;
+  f32x4* cut;           // [cuts][tiles on and above A's diagonal][1024]
   uint32_t p, q;        // padded to the tile
   uint32_t flip;        // rows > cols: X is the transpose
   uint32_t parts;       // partial sums
   uint32_t part_tiles;  // tiles that each has
   uint32_t first_part, first_pack;  // numbers among all items' workgroups
-  uint32_t first_gram, first_next;  // among a die's tiles
-  uint32_t each_gram, each_next;    // tiles that a die has at most
+  uint32_t first_sum;
+  uint32_t first_gram, first_cut, first_next;  // among a die's tiles
+  uint32_t each_gram, each_cut, each_next;     // tiles that a die has at most
+  uint32_t cuts;                               // workgroups that share a tile of A
 };
 
 struct PolarUpload {
   PolarItem item[kUploads];
 };
-static_assert(sizeof(PolarUpload) <= 4000, "kernel arguments");
+static_assert(sizeof(PolarUpload) <= 4064, "kernel arguments");
 
 __global__ void polar_upload_kernel(const PolarUpload u, PolarItem* to, uint32_t n) {
   const uint32_t words = n * sizeof(PolarItem) / 4;
@@ -374,18 +377,10 @@ __device__ __forceinline__ void store_both(Product<T>& m, _Float16* to, uint64_t
   if (ti != tj) m.store_rows(to + (uint64_t)ti * T * p + tj * T, p, sh, lower_halves);
 }
 
-// A without its diagonal, and D.
+// A without its diagonal, and D, from a tile of X X^T.
 template <int T, bool SPLIT>
-__global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar_gram_kernel(const PolarItem* items, uint32_t n) {
-  __shared__ typename Product<T>::Shared sh;
-  const DieTile found = find_tile(items, n, &PolarItem::first_gram, &PolarItem::each_gram);
-  const PolarItem& it = found.item;
-  uint32_t ti, tj;
-  upper_tile(found.tile, &ti, &tj);
-  if (tj >= it.p / T) return;
-  const uint64_t p = it.p, q = it.q;
-  Product<T> m;
-  m.template run<SPLIT>(it.x + ti * T * q, it.x + tj * T * q, it.q, it.q, p * q, p * q, sh);
+__device__ __forceinline__ void write_gram(Product<T>& m, const PolarItem& it, uint32_t ti, uint32_t tj,
+                                           typename Product<T>::Shared& sh) {
   m.each([&](uint32_t r, uint32_t c, float* v) {
     const uint32_t row = ti * T + r, col = tj * T + c;
 #pragma unroll
@@ -397,7 +392,67 @@ __global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar
       }
     }
   });
-  store_both<T, SPLIT>(m, it.a, p, ti, tj, sh);
+  store_both<T, SPLIT>(m, it.a, it.p, ti, tj, sh);
+}
+
+template <int T, bool SPLIT>
+__global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar_gram_kernel(const PolarItem* items, uint32_t n) {
+  __shared__ typename Product<T>::Shared sh;
+  const DieTile found = find_tile(items, n, &PolarItem::first_gram, &PolarItem::each_gram);
+  const PolarItem& it = found.item;
+  uint32_t ti, tj;
+  upper_tile(found.tile, &ti, &tj);
+  if (tj >= it.p / T) return;
+  const uint64_t p = it.p, q = it.q;
+  Product<T> m;
+  m.template run<SPLIT>(it.x + ti * T * q, it.x + tj * T * q, it.q, it.q, p * q, p * q, sh);
+  write_gram<T, SPLIT>(m, it, ti, tj, sh);
+}
+
+// Few tiles of long rows: a tile is shared by `cuts` workgroups, each a range of
+// the inner elements; what they have is added in a fixed order by a launch of its
+// own (two of 10007 x 321 bf16: 42 us a step by 21 tiles, 9 us by 240 workgroups and
+// the sums; 200 x 60000: 590 us against 26 us).
+template <bool SPLIT>
+__global__ __launch_bounds__(Product<64>::kThreads, Shape<64>::kBlocks) void polar_cut_kernel(const PolarItem* items, uint32_t n) {
+  using M = Product<64>;
+  __shared__ M::Shared sh;
+  const DieTile found = find_tile(items, n, &PolarItem::first_cut, &PolarItem::each_cut);
+  const PolarItem& it = found.item;
+  const uint32_t across = it.p / 64, tiles = across * (across + 1) / 2, cut = found.tile / tiles, tile = found.tile % tiles;
+  if (cut >= it.cuts) return;
+  uint32_t ti, tj;
+  upper_tile(tile, &ti, &tj);
+  const uint64_t p = it.p, q = it.q;
+  const uint32_t blocks = it.q / 64, begin = cut * blocks / it.cuts, end = (cut + 1) * blocks / it.cuts;
+  M m;
+  m.template run<SPLIT>(it.x + ti * 64 * q + begin * 64, it.x + tj * 64 * q + begin * 64, it.q, (end - begin) * 64, p * q, p * q, sh);
+  f32x4* to = it.cut + ((uint64_t)cut * tiles + tile) * 1024 + threadIdx.x;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    to[g * 256] = f32x4{m.acc[0][0][4 * g], m.acc[0][0][4 * g + 1], m.acc[0][0][4 * g + 2], m.acc[0][0][4 * g + 3]};
+}
+
+template <bool SPLIT>
+__global__ __launch_bounds__(Product<64>::kThreads) void polar_sum_kernel(const PolarItem* items, uint32_t n) {
+  using M = Product<64>;
+  __shared__ M::Shared sh;
+  const PolarItem& it = find_item(items, n, blockIdx.x, &PolarItem::first_sum);
+  const uint32_t across = it.p / 64, tiles = across * (across + 1) / 2, tile = blockIdx.x - it.first_sum;
+  uint32_t ti, tj;
+  upper_tile(tile, &ti, &tj);
+  M m;
+  m.acc[0][0] = f32x16{};
+  const f32x4* from = it.cut + (uint64_t)tile * 1024 + threadIdx.x;
+#pragma unroll 4
+  for (uint32_t cut = 0; cut < it.cuts; ++cut, from += (uint64_t)tiles * 1024)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const f32x4 v = from[g * 256];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m.acc[0][0][4 * g + k] += v[k];
+    }
+  write_gram<64, SPLIT>(m, it, ti, tj, sh);
 }
 
 // B without its diagonal, and E.
@@ -524,15 +579,16 @@ constexpr uint32_t kGroupTiles = 1u << 22;
 
 struct Group {
   uint32_t begin, end;  // of the order
-  uint32_t tile;
+  uint32_t tile, gram_tile;  // of the third product, whose sides X is padded to; of the other two
   bool split;
+  uint32_t cuts;  // workgroups that may share a tile of A
   uint64_t bytes;
 };
 
 uint64_t up(uint64_t v, uint64_t to) { return (v + to - 1) / to * to; }
 
 // Takes an item's scratch, from `at` on where that is memory; returns its bytes.
-uint64_t lay_out(const PolarMatrix& m, uint32_t tile, bool split, char* at, PolarItem* it) {
+uint64_t lay_out(const PolarMatrix& m, uint32_t tile, bool split, uint32_t cuts, char* at, PolarItem* it) {
   uint64_t used = 0;
   auto take = [&](uint64_t bytes) {
     char* p = at ? at + used : nullptr;
@@ -548,6 +604,10 @@ uint64_t lay_out(const PolarMatrix& m, uint32_t tile, bool split, char* at, Pola
   it->e = reinterpret_cast<float*>(take(p * 4));
   norm_parts(m, &it->parts, &it->part_tiles);
   it->partial = reinterpret_cast<double*>(take(it->parts * 8));
+  // more cuts make sums longer: 0.25 us a round of 64 inner elements against 0.2 us a cut
+  const uint32_t rounds = (uint32_t)(q / 64) * (split ? 3 : 1), best = (uint32_t)std::sqrt(1.25 * rounds);
+  it->cuts = std::max(1u, std::min({cuts, best, (uint32_t)(q / 64)}));
+  it->cut = cuts > 1 ? reinterpret_cast<f32x4*>(take(p / 64 * (p / 64 + 1) / 2 * it->cuts * 64 * 64 * 4)) : nullptr;
   it->p = (uint32_t)p;
   it->q = (uint32_t)q;
   it->flip = m.rows > m.cols;
@@ -555,9 +615,14 @@ uint64_t lay_out(const PolarMatrix& m, uint32_t tile, bool split, char* at, Pola
   return used;
 }
 
-// A tile of 128 feeds the matrix cores better, one of 64 gives twice to four
-// times as many workgroups.
-constexpr uint64_t kManyTiles = 512;
+// Large tiles feed the matrix cores better, small ones are more workgroups and less
+// padding. A third product of 512 tiles of 256 has them (16 matrices of 2048 x 4096:
+// 797 us against 1041 us with 128); of 512 tiles of 128, those (4 of 1024 x 2048
+// float32: 71 us against 114 us with 64) unless its rounds are few and its ends most
+// of it (12 of 500 x 1300: 40 and 39 us). A's half of the tiles is smaller: 256 tiles
+// or more are taken of that size (582 of 256: 390 us against 410 us with 128), others
+// of 64 (12 of 500 x 1300: 23 us against 29 us with 128).
+constexpr uint64_t kManyTiles = 512, kManyUpper = 256;
 
 struct Plan {
   std::vector<uint32_t> order;
@@ -574,26 +639,38 @@ Plan make_plan(const PolarMatrix* m, uint32_t n) {
   plan.bytes = narrow_workspace_bytes(plan.narrow.data(), (uint32_t)plan.narrow.size());
   for (int kind = 0; kind < 4; ++kind) {  // precision, and whether the shorter side fits a tile of 64
     const uint32_t begin = (uint32_t)plan.order.size();
-    uint64_t tiles = 0, big = 0;
+    uint64_t tiles = 0, big = 0, upper[3] = {}, rounds = 0;  // upper: of 64, 128 and 256
+    uint32_t longest = 0;
     const bool split = kind & 1, small = kind & 2;
     for (uint32_t i = 0; i < n; ++i) {
       if (is_narrow(m[i]) || splits(m[i]) != split || (std::min(m[i].rows, m[i].cols) <= 64) != small) continue;
       plan.order.push_back(i);
       tiles += up(m[i].rows, 128) / 128 * (up(m[i].cols, 128) / 128);
       big += up(m[i].rows, 256) / 256 * (up(m[i].cols, 256) / 256);
+      for (int k = 0; k < 3; ++k) {
+        const uint64_t side = up(std::min(m[i].rows, m[i].cols), 64 << k) / (64 << k);
+        upper[k] += side * (side + 1) / 2;
+      }
+      rounds += up(std::min(m[i].rows, m[i].cols), 64) / 64 * (split ? 3 : 1);
+      longest = std::max({longest, m[i].rows, m[i].cols});
     }
     // long products first, so that the last ones to end are short
     std::stable_sort(plan.order.begin() + begin, plan.order.end(), [&](uint32_t a, uint32_t b) {
       return std::min(m[a].rows, m[a].cols) > std::min(m[b].rows, m[b].cols);
     });
-    const uint32_t tile = small ? 64 : big >= kManyTiles ? 256 : tiles >= kManyTiles ? 128 : 64;
+    const uint64_t many = plan.order.size() - begin;
+    const uint32_t tile = small ? 64 : big >= kManyTiles ? 256 : tiles >= kManyTiles && rounds >= 12 * many ? 128 : 64;
+    const uint32_t gram_tile = tile == 256 && upper[2] >= kManyUpper ? 256 : tile >= 128 && upper[1] >= kManyUpper ? 128 : 64;
+    // A's few tiles are shared where rows are long enough to pay for the sums
+    const bool shared = gram_tile == 64 && upper[0] <= 256 && up(longest, 64) / 64 * (split ? 3 : 1) >= 32;
+    const uint32_t cuts = shared ? (uint32_t)(512 / std::max<uint64_t>(upper[0], 1)) : 1;
     for (uint32_t at = begin; at < plan.order.size();) {
-      Group g{at, at, tile, split, 0};
+      Group g{at, at, tile, gram_tile, split, cuts, 0};
       uint64_t count = 0;
       while (g.end < plan.order.size()) {
         PolarItem it;
         const PolarMatrix& x = m[plan.order[g.end]];
-        const uint64_t bytes = lay_out(x, tile, split, nullptr, &it) + up256(sizeof(PolarItem));
+        const uint64_t bytes = lay_out(x, tile, split, cuts, nullptr, &it) + up256(sizeof(PolarItem));
         const uint64_t more = (uint64_t)(it.p / 64) * (it.q / 64);
         if (g.end > at && (g.bytes + bytes > kGroupBytes || count + more > kGroupTiles)) break;
         g.bytes += bytes;
@@ -608,20 +685,64 @@ Plan make_plan(const PolarMatrix* m, uint32_t n) {
   return plan;
 }
 
-template <int T, bool SPLIT>
-hipError_t steps_t(const PolarItem* items, uint32_t n, uint32_t gram, uint32_t next, const double* c,
-                   uint32_t steps, hipStream_t s) {
-  for (uint32_t k = 0; k < steps; ++k, c += 3) {
-    polar_gram_kernel<T, SPLIT><<<gram * kDies, Product<T>::kThreads, 0, s>>>(items, n);
-    hipError_t e = hipGetLastError();
+// Workgroups of a group's launches, an eighth of them where tiles go by dies.
+struct Launches {
+  uint32_t parts, packs, sums, cut, gram, next;
+};
+
+template <bool SPLIT>
+hipError_t gram_t(const PolarItem* items, uint32_t n, const Launches& l, uint32_t tile, hipStream_t s) {
+  if (l.cut) {
+    polar_cut_kernel<SPLIT><<<l.cut * kDies, Product<64>::kThreads, 0, s>>>(items, n);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    polar_square_kernel<T, SPLIT><<<gram * kDies, Product<T>::kThreads, 0, s>>>(items, n, (float)c[1], (float)c[2]);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (k + 1 < steps)
-      polar_next_kernel<T, SPLIT, false><<<next * kDies, Product<T>::kThreads, 0, s>>>(items, n, (float)c[0], k);
+    polar_sum_kernel<SPLIT><<<l.sums, Product<64>::kThreads, 0, s>>>(items, n);
+  } else if (tile == 64) {
+    polar_gram_kernel<64, SPLIT><<<l.gram * kDies, Product<64>::kThreads, 0, s>>>(items, n);
+  } else if (tile == 128) {
+    polar_gram_kernel<128, SPLIT><<<l.gram * kDies, Product<128>::kThreads, 0, s>>>(items, n);
+  } else {
+    polar_gram_kernel<256, SPLIT><<<l.gram * kDies, Product<256>::kThreads, 0, s>>>(items, n);
+  }
+  return hipGetLastError();
+}
+
+template <bool SPLIT>
+hipError_t square_t(const PolarItem* items, uint32_t n, const Launches& l, uint32_t tile, float b, float c, hipStream_t s) {
+  if (tile == 64)
+    polar_square_kernel<64, SPLIT><<<l.gram * kDies, Product<64>::kThreads, 0, s>>>(items, n, b, c);
+  else if (tile == 128)
+    polar_square_kernel<128, SPLIT><<<l.gram * kDies, Product<128>::kThreads, 0, s>>>(items, n, b, c);
+  else
+    polar_square_kernel<256, SPLIT><<<l.gram * kDies, Product<256>::kThreads, 0, s>>>(items, n, b, c);
+  return hipGetLastError();
+}
+
+template <int T, bool SPLIT>
+hipError_t next_t(const PolarItem* items, uint32_t n, const Launches& l, float a, uint32_t step, bool last, hipStream_t s) {
+  if (last)
+    polar_next_kernel<T, SPLIT, true><<<l.next * kDies, Product<T>::kThreads, 0, s>>>(items, n, a, step);
+  else
+    polar_next_kernel<T, SPLIT, false><<<l.next * kDies, Product<T>::kThreads, 0, s>>>(items, n, a, step);
+  return hipGetLastError();
+}
+
+template <bool SPLIT>
+hipError_t steps_t(const PolarItem* items, uint32_t n, const Launches& l, const Group& g, const double* c, uint32_t steps,
+                   hipStream_t s) {
+  for (uint32_t k = 0; k < steps; ++k, c += 3) {
+    hipError_t e = gram_t<SPLIT>(items, n, l, g.gram_tile, s);
+    if (e != hipSuccess) return e;
+    if ((e = square_t<SPLIT>(items, n, l, g.gram_tile, (float)c[1], (float)c[2], s)) != hipSuccess) return e;
+    const float a = (float)c[0];
+    const bool last = k + 1 == steps;
+    if (g.tile == 256)
+      e = next_t<256, SPLIT>(items, n, l, a, k, last, s);
+    else if (g.tile == 128)
+      e = next_t<128, SPLIT>(items, n, l, a, k, last, s);
     else
-      polar_next_kernel<T, SPLIT, true><<<next * kDies, Product<T>::kThreads, 0, s>>>(items, n, (float)c[0], k);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+      e = next_t<64, SPLIT>(items, n, l, a, k, last, s);
+    if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
@@ -631,45 +752,43 @@ hipError_t run_group(const PolarMatrix* m, const uint32_t* order, const Group& g
   const uint32_t n = g.end - g.begin;
   PolarItem* items = reinterpret_cast<PolarItem*>(ws);
   char* at = ws + up256((uint64_t)n * sizeof(PolarItem));
-  uint32_t parts = 0, packs = 0, gram = 0, next = 0;
+  Launches l{};
   for (uint32_t i = 0; i < n; i += kUploads) {
     PolarUpload u;
     const uint32_t many = std::min(kUploads, n - i);
     for (uint32_t j = 0; j < many; ++j) {
       PolarItem& it = u.item[j];
-      at += lay_out(m[order[g.begin + i + j]], g.tile, g.split, at, &it);
-      it.first_part = parts;
-      it.first_pack = packs;
-      it.first_gram = gram;
-      it.first_next = next;
-      parts += it.parts;
-      packs += it.p / 64 * (it.q / 64);
-      const uint32_t pt = it.p / g.tile, qt = it.q / g.tile;
-      it.each_gram = (pt * (pt + 1) / 2 - 1) / kDies + 1;
+      at += lay_out(m[order[g.begin + i + j]], g.tile, g.split, g.cuts, at, &it);
+      const uint32_t pt = it.p / g.tile, qt = it.q / g.tile, side = it.p / g.gram_tile, upper = side * (side + 1) / 2;
+      it.first_part = l.parts;
+      it.first_pack = l.packs;
+      it.first_sum = l.sums;
+      it.first_gram = l.gram;
+      it.first_cut = l.cut;
+      it.first_next = l.next;
+      it.each_gram = (upper - 1) / kDies + 1;
+      it.each_cut = (upper * it.cuts - 1) / kDies + 1;
       it.each_next = (pt * qt - 1) / kDies + 1;
-      gram += it.each_gram;
-      next += it.each_next;
+      l.parts += it.parts;
+      l.packs += it.p / 64 * (it.q / 64);
+      l.sums += upper;
+      l.gram += it.each_gram;
+      l.next += it.each_next;
+      if (g.cuts > 1) l.cut += it.each_cut;
     }
     polar_upload_kernel<<<1, kPolarThreads, 0, s>>>(u, items + i, many);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  polar_norm_kernel<<<parts, kPolarThreads, 0, s>>>(items, n, r);
+  polar_norm_kernel<<<l.parts, kPolarThreads, 0, s>>>(items, n, r);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (g.split)
-    polar_pack_kernel<true><<<packs, kPolarThreads, 0, s>>>(items, n, r);
+    polar_pack_kernel<true><<<l.packs, kPolarThreads, 0, s>>>(items, n, r);
   else
-    polar_pack_kernel<false><<<packs, kPolarThreads, 0, s>>>(items, n, r);
+    polar_pack_kernel<false><<<l.packs, kPolarThreads, 0, s>>>(items, n, r);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  if (g.tile == 256)
-    return g.split ? steps_t<256, true>(items, n, gram, next, c, steps, s)
-                   : steps_t<256, false>(items, n, gram, next, c, steps, s);
-  if (g.tile == 128)
-    return g.split ? steps_t<128, true>(items, n, gram, next, c, steps, s)
-                   : steps_t<128, false>(items, n, gram, next, c, steps, s);
-  return g.split ? steps_t<64, true>(items, n, gram, next, c, steps, s)
-                 : steps_t<64, false>(items, n, gram, next, c, steps, s);
+  return g.split ? steps_t<true>(items, n, l, g, c, steps, s) : steps_t<false>(items, n, l, g, c, steps, s);
 }
 
 }  // namespace
