@@ -134,20 +134,35 @@ __global__ __launch_bounds__(kPolarThreads) void polar_pack_kernel(const PolarIt
 }
 
 // A tile of T x T of a product of rows, acc[i][j] = sum over k of a[i][k] b[j][k],
-// by WM x WN waves of FM x FN fragments of 32 x 32 each.
-template <int T>
+// by WM x WN waves of FM x FN fragments of 32 x 32 each. BOTH: both halves of a
+// number come together and meet in three products; where two buffers of them do
+// not fit (T = 256), the halves' products are three passes, one after the other.
+template <int T, bool SPLIT>
 struct Shape;
 template <>
-struct Shape<64> {
+struct Shape<64, false> {
   static constexpr int WM = 2, WN = 2, FM = 1, FN = 1, kBuffers = 4, kBlocks = 2;
+  static constexpr bool BOTH = false;
 };
 template <>
-struct Shape<128> {
+struct Shape<64, true> {
+  static constexpr int WM = 2, WN = 2, FM = 1, FN = 1, kBuffers = 2, kBlocks = 2;
+  static constexpr bool BOTH = true;
+};
+template <>
+struct Shape<128, false> {
   static constexpr int WM = 2, WN = 2, FM = 2, FN = 2, kBuffers = 2, kBlocks = 2;
+  static constexpr bool BOTH = false;
 };
 template <>
-struct Shape<256> {
+struct Shape<128, true> {
+  static constexpr int WM = 2, WN = 4, FM = 2, FN = 1, kBuffers = 2, kBlocks = 2;
+  static constexpr bool BOTH = true;
+};
+template <bool SPLIT>
+struct Shape<256, SPLIT> {
   static constexpr int WM = 2, WN = 4, FM = 4, FN = 2, kBuffers = 2, kBlocks = 2;
+  static constexpr bool BOTH = false;
 };
 
 // 64 inner elements at a time go through LDS, in buffers that memory itself
@@ -160,54 +175,64 @@ struct Shape<256> {
 // as half of the products take (4096 x 4096 x 2048, T = 256: 1008 TFLOP/s against
 // 950; T = 128: 854 against 830; more buffers, or fragments read one step ahead,
 // were no faster).
-template <int T>
+template <int T, bool SPLIT>
 struct Product {
-  using S = Shape<T>;
-  static constexpr int FM = S::FM, FN = S::FN;
+  using S = Shape<T, SPLIT>;
+  static constexpr int FM = S::FM, FN = S::FN, B = S::kBuffers, H = S::BOTH ? 2 : 1;
   static constexpr int kThreads = S::WM * S::WN * 64;
-  static constexpr int L = T * 8 / kThreads;  // pieces that a thread brings, of each side
-  static constexpr int kStage = 2 * T * 8;
-  static constexpr int B = S::kBuffers;
+  static constexpr int L = T * 8 / kThreads;  // pieces that a thread brings, of each side and half
+  static constexpr int kPlane = T * 8;
+  static constexpr int kStage = 2 * H * kPlane;
   typedef f16x8 Shared[B * kStage];
   f32x16 acc[FM][FN];
+
+  // The i-th piece that a thread brings of a round: first side a's halves, then b's.
+  static __device__ __forceinline__ void bring_piece(int i, const _Float16* a, const _Float16* b, uint64_t plane_a,
+                                                     uint64_t plane_b, uint32_t off, uint64_t hop, f16x8* to, uint32_t wave) {
+    const int side = i / (H * L), half = i / L % H, k = i % L;
+    const _Float16* from = side ? b + half * plane_b : a + half * plane_a;
+    bring(from + k * hop + off, to + (side * H + half) * kPlane + k * kThreads + wave * 64);
+  }
 
   // `to` and `from` are buffers apart, which the compiler has to know: it would
   // otherwise wait for the loads before it reads.
   __device__ __forceinline__ void stage(f16x8* __restrict to, const f16x8* __restrict from, const _Float16* a,
-                                        const _Float16* b, uint32_t off, uint64_t hop, bool more, uint32_t wave,
-                                        uint32_t ar, uint32_t br, uint32_t key) {
+                                        const _Float16* b, uint64_t plane_a, uint64_t plane_b, uint32_t off, uint64_t hop,
+                                        bool more, uint32_t wave, uint32_t ar, uint32_t br, uint32_t key) {
+    constexpr int N = 2 * H * L;
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
-      f16x8 fa[FM], fb[FN];
+      f16x8 fa[H][FM], fb[H][FN];
       const uint32_t pc = (ks * 2) ^ key;
 #pragma unroll
-      for (int i = 0; i < FM; ++i) fa[i] = from[ar + i * 256 + pc];
+      for (int h = 0; h < H; ++h) {
 #pragma unroll
-      for (int i = 0; i < FN; ++i) fb[i] = from[T * 8 + br + i * 256 + pc];
+        for (int i = 0; i < FM; ++i) fa[h][i] = from[h * kPlane + ar + i * 256 + pc];
+#pragma unroll
+        for (int i = 0; i < FN; ++i) fb[h][i] = from[(H + h) * kPlane + br + i * 256 + pc];
+      }
       if (more) {
 #pragma unroll
-        for (int i = ks * L / 2; i < (ks + 1) * L / 2; ++i) {
-          if (i < L)
-            bring(a + i * hop + off, to + i * kThreads + wave * 64);
-          else
-            bring(b + (i - L) * hop + off, to + T * 8 + (i - L) * kThreads + wave * 64);
-        }
+        for (int i = ks * N / 4; i < (ks + 1) * N / 4; ++i) bring_piece(i, a, b, plane_a, plane_b, off, hop, to, wave);
       }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < FM; ++i)
+      for (int pass = H == 2 ? 0 : 2; pass < 3; ++pass)  // lower x upper, upper x lower, upper x upper
 #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[pass == 0 ? H - 1 : 0][i], fb[pass == 1 ? H - 1 : 0][j],
+                                                               acc[i][j], 0, 0, 0);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 
-  // Rows K apart, K inner elements from the first one. SPLIT: lower x upper,
-  // upper x lower and upper x upper halves, one after the other, whose planes are
-  // plane_a and plane_b elements apart.
-  template <bool SPLIT>
+  // Rows `stride` apart, K inner elements from the first one; the lower halves lie
+  // plane_a and plane_b elements behind the upper ones.
   __device__ __forceinline__ void run(const _Float16* a, const _Float16* b, uint32_t stride, uint32_t K, uint64_t plane_a,
                                       uint64_t plane_b, Shared& sh) {
+    constexpr bool kPasses = SPLIT && H == 1;
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -217,16 +242,16 @@ struct Product {
     const uint64_t hop = (uint64_t)(kThreads / 8) * stride;
     const uint32_t fr = lane & 31, key = (lane >> 5) ^ ((fr >> 1) & 7);
     const uint32_t ar = (wave / S::WN * FM * 32 + fr) * 8, br = (wave % S::WN * FN * 32 + fr) * 8;
-    const uint32_t blocks = K / 64, rounds = SPLIT ? 3 * blocks : blocks;
-    const _Float16 *pa = SPLIT ? a + plane_a : a, *pb = b;
-    uint32_t left = blocks, seg = 0;
+    const uint32_t blocks = K / 64, rounds = kPasses ? 3 * blocks : blocks;
+    const _Float16 *pa = kPasses ? a + plane_a : a, *pb = b;
+    uint32_t left = blocks, pass = 0;
     auto advance = [&]() {
       pa += 64;
       pb += 64;
-      if (SPLIT && --left == 0) {
+      if (kPasses && --left == 0) {
         pa = a;
-        pb = seg == 0 ? b + plane_b : b;
-        ++seg;
+        pb = pass == 0 ? b + plane_b : b;
+        ++pass;
         left = blocks;
       }
     };
@@ -234,9 +259,7 @@ struct Product {
     for (int s = 0; s < B - 1; ++s) {
       if ((uint32_t)s < rounds) {
 #pragma unroll
-        for (int i = 0; i < L; ++i) bring(pa + i * hop + off, sh + s * kStage + i * kThreads + wave * 64);
-#pragma unroll
-        for (int i = 0; i < L; ++i) bring(pb + i * hop + off, sh + s * kStage + T * 8 + i * kThreads + wave * 64);
+        for (int i = 0; i < 2 * H * L; ++i) bring_piece(i, pa, pb, plane_a, plane_b, off, hop, sh + s * kStage, wave);
         advance();
       }
     }
@@ -247,12 +270,12 @@ struct Product {
       // be on their way; behind the barrier the others' are there too, and nobody
       // reads the buffer of the round before any more.
       if (r + B - 2 < rounds)
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((B - 2) * 2 * L) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((B - 2) * 2 * H * L) : "memory");
       else
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
-      stage(sh + to * kStage, sh + at * kStage, pa, pb, off, hop, r + B - 1 < rounds, wave, ar, br, key);
+      stage(sh + to * kStage, sh + at * kStage, pa, pb, plane_a, plane_b, off, hop, r + B - 1 < rounds, wave, ar, br, key);
       advance();
       at = at + 1 == B ? 0 : at + 1;
       to = to + 1 == B ? 0 : to + 1;
@@ -367,8 +390,8 @@ __device__ __forceinline__ void upper_tile(uint32_t tile, uint32_t* i, uint32_t*
 
 // Writes a tile of a symmetric matrix at both its places, as halves.
 template <int T, bool SPLIT>
-__device__ __forceinline__ void store_both(Product<T>& m, _Float16* to, uint64_t p, uint32_t ti, uint32_t tj,
-                                           typename Product<T>::Shared& sh) {
+__device__ __forceinline__ void store_both(Product<T, SPLIT>& m, _Float16* to, uint64_t p, uint32_t ti, uint32_t tj,
+                                           typename Product<T, SPLIT>::Shared& sh) {
   m.store_tile(to + (uint64_t)tj * T * p + ti * T, p, sh, upper_halves);
   if (ti != tj) m.store_rows(to + (uint64_t)ti * T * p + tj * T, p, sh, upper_halves);
   if (!SPLIT) return;
@@ -379,8 +402,8 @@ __device__ __forceinline__ void store_both(Product<T>& m, _Float16* to, uint64_t
 
 // A without its diagonal, and D, from a tile of X X^T.
 template <int T, bool SPLIT>
-__device__ __forceinline__ void write_gram(Product<T>& m, const PolarItem& it, uint32_t ti, uint32_t tj,
-                                           typename Product<T>::Shared& sh) {
+__device__ __forceinline__ void write_gram(Product<T, SPLIT>& m, const PolarItem& it, uint32_t ti, uint32_t tj,
+                                           typename Product<T, SPLIT>::Shared& sh) {
   m.each([&](uint32_t r, uint32_t c, float* v) {
     const uint32_t row = ti * T + r, col = tj * T + c;
 #pragma unroll
@@ -396,16 +419,16 @@ __device__ __forceinline__ void write_gram(Product<T>& m, const PolarItem& it, u
 }
 
 template <int T, bool SPLIT>
-__global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar_gram_kernel(const PolarItem* items, uint32_t n) {
-  __shared__ typename Product<T>::Shared sh;
+__global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kBlocks)) void polar_gram_kernel(const PolarItem* items, uint32_t n) {
+  __shared__ typename Product<T, SPLIT>::Shared sh;
   const DieTile found = find_tile(items, n, &PolarItem::first_gram, &PolarItem::each_gram);
   const PolarItem& it = found.item;
   uint32_t ti, tj;
   upper_tile(found.tile, &ti, &tj);
   if (tj >= it.p / T) return;
   const uint64_t p = it.p, q = it.q;
-  Product<T> m;
-  m.template run<SPLIT>(it.x + ti * T * q, it.x + tj * T * q, it.q, it.q, p * q, p * q, sh);
+  Product<T, SPLIT> m;
+  m.run(it.x + ti * T * q, it.x + tj * T * q, it.q, it.q, p * q, p * q, sh);
   write_gram<T, SPLIT>(m, it, ti, tj, sh);
 }
 
@@ -414,9 +437,9 @@ __global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar
 // own (two of 10007 x 321 bf16: 42 us a step by 21 tiles, 9 us by 240 workgroups and
 // the sums; 200 x 60000: 590 us against 26 us).
 template <bool SPLIT>
-__global__ __launch_bounds__(Product<64>::kThreads, Shape<64>::kBlocks) void polar_cut_kernel(const PolarItem* items, uint32_t n) {
-  using M = Product<64>;
-  __shared__ M::Shared sh;
+__global__ __launch_bounds__((Product<64, SPLIT>::kThreads), (Shape<64, SPLIT>::kBlocks)) void polar_cut_kernel(const PolarItem* items, uint32_t n) {
+  using M = Product<64, SPLIT>;
+  __shared__ typename M::Shared sh;
   const DieTile found = find_tile(items, n, &PolarItem::first_cut, &PolarItem::each_cut);
   const PolarItem& it = found.item;
   const uint32_t across = it.p / 64, tiles = across * (across + 1) / 2, cut = found.tile / tiles, tile = found.tile % tiles;
@@ -426,7 +449,7 @@ __global__ __launch_bounds__(Product<64>::kThreads, Shape<64>::kBlocks) void pol
   const uint64_t p = it.p, q = it.q;
   const uint32_t blocks = it.q / 64, begin = cut * blocks / it.cuts, end = (cut + 1) * blocks / it.cuts;
   M m;
-  m.template run<SPLIT>(it.x + ti * 64 * q + begin * 64, it.x + tj * 64 * q + begin * 64, it.q, (end - begin) * 64, p * q, p * q, sh);
+  m.run(it.x + ti * 64 * q + begin * 64, it.x + tj * 64 * q + begin * 64, it.q, (end - begin) * 64, p * q, p * q, sh);
   f32x4* to = it.cut + ((uint64_t)cut * tiles + tile) * 1024 + threadIdx.x;
 #pragma unroll
   for (int g = 0; g < 4; ++g)
@@ -434,9 +457,9 @@ __global__ __launch_bounds__(Product<64>::kThreads, Shape<64>::kBlocks) void pol
 }
 
 template <bool SPLIT>
-__global__ __launch_bounds__(Product<64>::kThreads) void polar_sum_kernel(const PolarItem* items, uint32_t n) {
-  using M = Product<64>;
-  __shared__ M::Shared sh;
+__global__ __launch_bounds__((Product<64, SPLIT>::kThreads)) void polar_sum_kernel(const PolarItem* items, uint32_t n) {
+  using M = Product<64, SPLIT>;
+  __shared__ typename M::Shared sh;
   const PolarItem& it = find_item(items, n, blockIdx.x, &PolarItem::first_sum);
   const uint32_t across = it.p / 64, tiles = across * (across + 1) / 2, tile = blockIdx.x - it.first_sum;
   uint32_t ti, tj;
@@ -457,17 +480,17 @@ __global__ __launch_bounds__(Product<64>::kThreads) void polar_sum_kernel(const 
 
 // B without its diagonal, and E.
 template <int T, bool SPLIT>
-__global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar_square_kernel(const PolarItem* items, uint32_t n,
+__global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kBlocks)) void polar_square_kernel(const PolarItem* items, uint32_t n,
                                                                                            float b, float c2) {
-  __shared__ typename Product<T>::Shared sh;
+  __shared__ typename Product<T, SPLIT>::Shared sh;
   const DieTile found = find_tile(items, n, &PolarItem::first_gram, &PolarItem::each_gram);
   const PolarItem& it = found.item;
   uint32_t ti, tj;
   upper_tile(found.tile, &ti, &tj);
   if (tj >= it.p / T) return;
   const uint64_t p = it.p;
-  Product<T> m;
-  m.template run<SPLIT>(it.a + ti * T * p, it.a + tj * T * p, it.p, it.p, p * p, p * p, sh);
+  Product<T, SPLIT> m;
+  m.run(it.a + ti * T * p, it.a + tj * T * p, it.p, it.p, p * p, p * p, sh);
   const _Float16* tile = it.a + (uint64_t)tj * T * p + ti * T;  // A is symmetric
   const float *dr = it.d + ti * T, *dc = it.d + tj * T;
   for (int plane = SPLIT ? 1 : 0; plane >= 0; --plane) {
@@ -497,10 +520,10 @@ __global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar
 // The tile (ti, tj) of the result, to the matrix or into the weights: by way of
 // LDS, 32 columns of every wave at a time, so that lanes lie next to each other
 // in memory.
-template <int T>
-__device__ __forceinline__ void write_out(Product<T>& m, const PolarItem& it, uint32_t ti, uint32_t tj,
-                                          typename Product<T>::Shared& sh) {
-  using S = Shape<T>;
+template <int T, bool SPLIT>
+__device__ __forceinline__ void write_out(Product<T, SPLIT>& m, const PolarItem& it, uint32_t ti, uint32_t tj,
+                                          typename Product<T, SPLIT>::Shared& sh) {
+  using S = Shape<T, SPLIT>;
   constexpr uint32_t W = S::WN * 32;  // columns at a time
   float* lds = reinterpret_cast<float*>(sh);
   const PolarMatrix w = it.m;
@@ -515,7 +538,7 @@ __device__ __forceinline__ void write_out(Product<T>& m, const PolarItem& it, ui
       for (int k = 0; k < 4; ++k) lds[flip ? cc * T + ((r + k) ^ (cc * 4 % T)) : (r + k) * W + cc] = v[k];
     });
     __syncthreads();
-    for (uint32_t i = threadIdx.x * 4; i < T * W; i += Product<T>::kThreads * 4) {
+    for (uint32_t i = threadIdx.x * 4; i < T * W; i += Product<T, SPLIT>::kThreads * 4) {
       const uint32_t cc = flip ? i / T : i % W, r = flip ? (i % T) ^ (cc * 4 % T) : i / W;
       const uint32_t row = ti * T + r, col = tj * T + (cc / 32 * S::FN + j) * 32 + cc % 32;  // of X
       const uint32_t wr = flip ? col : row, wc = flip ? row : col;
@@ -539,17 +562,17 @@ __device__ __forceinline__ void write_out(Product<T>& m, const PolarItem& it, ui
 // a X + B X of step `k`; the last one's goes to its destination. Columns of the
 // tile are rows of X^T.
 template <int T, bool SPLIT, bool LAST>
-__global__ __launch_bounds__(Product<T>::kThreads, Shape<T>::kBlocks) void polar_next_kernel(const PolarItem* items, uint32_t n,
+__global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kBlocks)) void polar_next_kernel(const PolarItem* items, uint32_t n,
                                                                                          float a, uint32_t step) {
-  __shared__ typename Product<T>::Shared sh;
+  __shared__ typename Product<T, SPLIT>::Shared sh;
   const DieTile found = find_tile(items, n, &PolarItem::first_next, &PolarItem::each_next);
   const PolarItem& it = found.item;
   const uint64_t p = it.p, q = it.q;
   const uint32_t across = it.p / T, ti = found.tile % across, tj = found.tile / across;
   if (tj >= it.q / T) return;
   const _Float16* from = it.t[step & 1];
-  Product<T> m;
-  m.template run<SPLIT>(it.b + ti * T * p, from + tj * T * p, it.p, it.p, p * p, p * q, sh);
+  Product<T, SPLIT> m;
+  m.run(it.b + ti * T * p, from + tj * T * p, it.p, it.p, p * p, p * q, sh);
   const uint64_t at = (uint64_t)tj * T * p + ti * T;
   const float* e = it.e + ti * T;
   for (int plane = 1; plane >= 0; --plane) {
@@ -693,16 +716,16 @@ struct Launches {
 template <bool SPLIT>
 hipError_t gram_t(const PolarItem* items, uint32_t n, const Launches& l, uint32_t tile, hipStream_t s) {
   if (l.cut) {
-    polar_cut_kernel<SPLIT><<<l.cut * kDies, Product<64>::kThreads, 0, s>>>(items, n);
+    polar_cut_kernel<SPLIT><<<l.cut * kDies, Product<64, SPLIT>::kThreads, 0, s>>>(items, n);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    polar_sum_kernel<SPLIT><<<l.sums, Product<64>::kThreads, 0, s>>>(items, n);
+    polar_sum_kernel<SPLIT><<<l.sums, Product<64, SPLIT>::kThreads, 0, s>>>(items, n);
   } else if (tile == 64) {
-    polar_gram_kernel<64, SPLIT><<<l.gram * kDies, Product<64>::kThreads, 0, s>>>(items, n);
+    polar_gram_kernel<64, SPLIT><<<l.gram * kDies, Product<64, SPLIT>::kThreads, 0, s>>>(items, n);
   } else if (tile == 128) {
-    polar_gram_kernel<128, SPLIT><<<l.gram * kDies, Product<128>::kThreads, 0, s>>>(items, n);
+    polar_gram_kernel<128, SPLIT><<<l.gram * kDies, Product<128, SPLIT>::kThreads, 0, s>>>(items, n);
   } else {
-    polar_gram_kernel<256, SPLIT><<<l.gram * kDies, Product<256>::kThreads, 0, s>>>(items, n);
+    polar_gram_kernel<256, SPLIT><<<l.gram * kDies, Product<256, SPLIT>::kThreads, 0, s>>>(items, n);
   }
   return hipGetLastError();
 }
@@ -710,20 +733,20 @@ hipError_t gram_t(const PolarItem* items, uint32_t n, const Launches& l, uint32_
 template <bool SPLIT>
 hipError_t square_t(const PolarItem* items, uint32_t n, const Launches& l, uint32_t tile, float b, float c, hipStream_t s) {
   if (tile == 64)
-    polar_square_kernel<64, SPLIT><<<l.gram * kDies, Product<64>::kThreads, 0, s>>>(items, n, b, c);
+    polar_square_kernel<64, SPLIT><<<l.gram * kDies, Product<64, SPLIT>::kThreads, 0, s>>>(items, n, b, c);
   else if (tile == 128)
-    polar_square_kernel<128, SPLIT><<<l.gram * kDies, Product<128>::kThreads, 0, s>>>(items, n, b, c);
+    polar_square_kernel<128, SPLIT><<<l.gram * kDies, Product<128, SPLIT>::kThreads, 0, s>>>(items, n, b, c);
   else
-    polar_square_kernel<256, SPLIT><<<l.gram * kDies, Product<256>::kThreads, 0, s>>>(items, n, b, c);
+    polar_square_kernel<256, SPLIT><<<l.gram * kDies, Product<256, SPLIT>::kThreads, 0, s>>>(items, n, b, c);
   return hipGetLastError();
 }
 
 template <int T, bool SPLIT>
 hipError_t next_t(const PolarItem* items, uint32_t n, const Launches& l, float a, uint32_t step, bool last, hipStream_t s) {
   if (last)
-    polar_next_kernel<T, SPLIT, true><<<l.next * kDies, Product<T>::kThreads, 0, s>>>(items, n, a, step);
+    polar_next_kernel<T, SPLIT, true><<<l.next * kDies, Product<T, SPLIT>::kThreads, 0, s>>>(items, n, a, step);
   else
-    polar_next_kernel<T, SPLIT, false><<<l.next * kDies, Product<T>::kThreads, 0, s>>>(items, n, a, step);
+    polar_next_kernel<T, SPLIT, false><<<l.next * kDies, Product<T, SPLIT>::kThreads, 0, s>>>(items, n, a, step);
   return hipGetLastError();
 }
 
