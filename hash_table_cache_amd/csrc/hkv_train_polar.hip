@@ -141,7 +141,7 @@ template <int T, bool SPLIT>
 struct Shape;
 template <>
 struct Shape<64, false> {
-  static constexpr int WM = 2, WN = 2, FM = 1, FN = 1, kBuffers = 4, kBlocks = 2;
+  static constexpr int WM = 2, WN = 2, FM = 1, FN = 1, kBuffers = 3, kBlocks = 3;
   static constexpr bool BOTH = false;
 };
 template <>
@@ -282,8 +282,8 @@ struct Product {
     }
   }
 
-  // use(row, column, four values of rows row .. row + 3) for each of a thread's
-  // quads, few of them at a time: registers are full.
+  // use(row, column, four values of rows row .. row + 3, number of the quad if it is
+  // asked for) for each of a thread's quads, few of them at a time: registers are full.
   template <typename Use>
   __device__ __forceinline__ void each(Use&& use) {
     uint32_t lane = threadIdx.x & 63;
@@ -303,62 +303,91 @@ struct Product {
           float v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[k] = acc[i][j][g * 4 + k];
-          use(wave / S::WN * FM * 32 + i * 32 + g * 8 + (lane >> 5) * 4, wave % S::WN * FN * 32 + j * 32 + (lane & 31), v);
+          const uint32_t r = wave / S::WN * FM * 32 + i * 32 + g * 8 + (lane >> 5) * 4;
+          const uint32_t c = wave % S::WN * FN * 32 + j * 32 + (lane & 31);
+          if constexpr (std::is_invocable_v<Use, uint32_t, uint32_t, float*, int>)
+            use(r, c, v, (i * FN + j) * 4 + g);
+          else
+            use(r, c, v);
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[i][j][g * 4 + k] = v[k];
         }
   }
 
-  // A tile of halves in LDS, T columns of T, on its way from or to memory by 16
-  // bytes a lane; a quad of a column is 8 bytes of it. Pieces are shuffled by the
-  // column as above.
-  static __device__ __forceinline__ uint32_t place(uint32_t r, uint32_t c) {
-    return c * T + (((r >> 3) ^ c) % (T / 8)) * 8 + (r & 7);
-  }
-  static __device__ __forceinline__ f16x4& quad(Shared& sh, uint32_t r, uint32_t c) {
-    return *reinterpret_cast<f16x4*>(reinterpret_cast<_Float16*>(sh) + place(r, c));
+  // use(row, column, number) for a thread's quads where nothing is held yet.
+  template <typename Use>
+  static __device__ __forceinline__ void places(Use&& use) {
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int n = 0; n < FM * FN * 4; ++n)
+      use(wave / S::WN * FM * 32 + n / 4 / FN * 32 + n % 4 * 8 + (lane >> 5) * 4, wave % S::WN * FN * 32 + n / 4 % FN * 32 + (lane & 31), n);
   }
 
-  // Brings a tile, columns `stride` apart in memory.
-  static __device__ __forceinline__ void load_tile(const _Float16* from, uint64_t stride, Shared& sh) {
+  // Tiles of halves in LDS, T columns of T, on their way from or to memory by 16
+  // bytes a lane; a quad of a column is 8 bytes of it. Pieces are shuffled by the
+  // column as above. kFit of them have room at a time.
+  static constexpr int kTile = T * T / 8, kFit = B * kStage / kTile;
+
+  static __device__ __forceinline__ f16x4& quad(f16x8* tile, uint32_t r, uint32_t c) {
+    return *reinterpret_cast<f16x4*>(reinterpret_cast<_Float16*>(tile) + c * T + (((r >> 3) ^ c) % (T / 8)) * 8 + (r & 7));
+  }
+
+  // Brings N tiles `plane` apart, of columns `stride` apart in memory.
+  template <int N>
+  static __device__ __forceinline__ void load_tiles(const _Float16* from, uint64_t stride, uint64_t plane, Shared& sh) {
+    static_assert(N <= kFit, "LDS");
     const uint32_t tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     __syncthreads();
 #pragma unroll
-    for (uint32_t i = 0; i < T * T / 8 / kThreads; ++i) {
-      const uint32_t at = i * kThreads + tid, c = at / (T / 8), piece = (at ^ c) % (T / 8);
-      bring(from + c * stride + piece * 8, sh + i * kThreads + wave * 64);
-    }
-    __syncthreads();
-  }
-
-  // value(quad) is written to a tile of columns `stride` apart.
-  template <typename Value>
-  __device__ __forceinline__ void store_tile(_Float16* to, uint64_t stride, Shared& sh, Value&& value) {
-    __syncthreads();
-    each([&](uint32_t r, uint32_t c, float* v) { quad(sh, r, c) = value(v); });
-    __syncthreads();
-#pragma unroll 4
-    for (uint32_t i = 0; i < T * T / 8 / kThreads; ++i) {
-      const uint32_t at = i * kThreads + threadIdx.x, c = at / (T / 8), piece = (at ^ c) % (T / 8);
-      *reinterpret_cast<f16x8*>(to + c * stride + piece * 8) = sh[at];
-    }
-  }
-
-  // The same as rows, `stride` apart.
-  template <typename Value>
-  __device__ __forceinline__ void store_rows(_Float16* to, uint64_t stride, Shared& sh, Value&& value) {
-    _Float16* lds = reinterpret_cast<_Float16*>(sh);
-    __syncthreads();
-    each([&](uint32_t r, uint32_t c, float* v) {
-      const f16x4 h = value(v);
+    for (int n = 0; n < N; ++n)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) lds[(r + k) * T + c] = h[k];
-    });
+      for (uint32_t i = 0; i < kTile / kThreads; ++i) {
+        const uint32_t at = i * kThreads + tid, c = at / (T / 8), piece = (at ^ c) % (T / 8);
+        bring(from + n * plane + c * stride + piece * 8, sh + n * kTile + i * kThreads + wave * 64);
+      }
     __syncthreads();
+  }
+
+  // A tile that is written: upper or lower halves, by columns or, `rows`, by rows,
+  // which are `stride` apart in memory; not where to is NULL.
+  struct Out {
+    _Float16* to;
+    uint64_t stride;
+    bool rows, lower;
+  };
+
+  template <int N>
+  __device__ __forceinline__ void store_tiles(const Out (&out)[N], Shared& sh) {
+#pragma unroll
+    for (int first = 0; first < N; first += kFit) {
+      __syncthreads();
+#pragma unroll
+      for (int n = first; n < first + kFit && n < N; ++n) {
+        const Out& o = out[n];
+        f16x8* tile = sh + (n - first) * kTile;
+        if (!o.to) continue;
+        each([&](uint32_t r, uint32_t c, float* v) {
+          const f16x4 h = o.lower ? lower_halves(v) : upper_halves(v);
+          if (o.rows) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) reinterpret_cast<_Float16*>(tile)[(r + k) * T + c] = h[k];
+          } else {
+            quad(tile, r, c) = h;
+          }
+        });
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = first; n < first + kFit && n < N; ++n) {
+        const Out& o = out[n];
+        const f16x8* tile = sh + (n - first) * kTile;
+        if (!o.to) continue;
 #pragma unroll 4
-    for (uint32_t i = 0; i < T * T / 8 / kThreads; ++i) {
-      const uint32_t at = i * kThreads + threadIdx.x, r = at / (T / 8), piece = at % (T / 8);
-      *reinterpret_cast<f16x8*>(to + r * stride + piece * 8) = sh[at];
+        for (uint32_t i = 0; i < kTile / kThreads; ++i) {
+          const uint32_t at = i * kThreads + threadIdx.x, line = at / (T / 8), piece = (o.rows ? at : at ^ line) % (T / 8);
+          *reinterpret_cast<f16x8*>(o.to + line * o.stride + piece * 8) = tile[at];
+        }
+      }
     }
   }
 };
@@ -392,12 +421,16 @@ __device__ __forceinline__ void upper_tile(uint32_t tile, uint32_t* i, uint32_t*
 template <int T, bool SPLIT>
 __device__ __forceinline__ void store_both(Product<T, SPLIT>& m, _Float16* to, uint64_t p, uint32_t ti, uint32_t tj,
                                            typename Product<T, SPLIT>::Shared& sh) {
-  m.store_tile(to + (uint64_t)tj * T * p + ti * T, p, sh, upper_halves);
-  if (ti != tj) m.store_rows(to + (uint64_t)ti * T * p + tj * T, p, sh, upper_halves);
-  if (!SPLIT) return;
-  to += p * p;
-  m.store_tile(to + (uint64_t)tj * T * p + ti * T, p, sh, lower_halves);
-  if (ti != tj) m.store_rows(to + (uint64_t)ti * T * p + tj * T, p, sh, lower_halves);
+  using Out = typename Product<T, SPLIT>::Out;
+  _Float16* col = to + (uint64_t)tj * T * p + ti * T;
+  _Float16* row = ti == tj ? nullptr : to + (uint64_t)ti * T * p + tj * T;
+  if constexpr (SPLIT) {
+    const Out out[4] = {{col, p, false, false}, {row, p, true, false}, {col + p * p, p, false, true}, {row ? row + p * p : nullptr, p, true, true}};
+    m.store_tiles(out, sh);
+  } else {
+    const Out out[2] = {{col, p, false, false}, {row, p, true, false}};
+    m.store_tiles(out, sh);
+  }
 }
 
 // A without its diagonal, and D, from a tile of X X^T.
@@ -489,20 +522,41 @@ __global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kB
   upper_tile(found.tile, &ti, &tj);
   if (tj >= it.p / T) return;
   const uint64_t p = it.p;
-  Product<T, SPLIT> m;
-  m.run(it.a + ti * T * p, it.a + tj * T * p, it.p, it.p, p * p, p * p, sh);
+  using M = Product<T, SPLIT>;
+  M m;
   const _Float16* tile = it.a + (uint64_t)tj * T * p + ti * T;  // A is symmetric
   const float *dr = it.d + ti * T, *dc = it.d + tj * T;
-  for (int plane = SPLIT ? 1 : 0; plane >= 0; --plane) {
-    m.load_tile(tile + plane * p * p, p, sh);
-    m.each([&](uint32_t r, uint32_t c, float* v) {
-      const f16x4 a = m.quad(sh, r, c);
+  constexpr int H = SPLIT ? 2 : 1;
+  auto add = [&](float* v, f32x4 d, float dcol, f16x4 x, bool first) {  // what A - D adds
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float f = fmaf(c2, dr[r + k] + dc[c], b);  // of A - D
-        v[k] = fmaf(f, (float)a[k], plane == (SPLIT ? 1 : 0) ? v[k] * (c2 / kUnit) : v[k]);
-      }
+    for (int k = 0; k < 4; ++k) v[k] = fmaf(fmaf(c2, d[k] + dcol, b), (float)x[k], first ? v[k] * (c2 / kUnit) : v[k]);
+  };
+  if constexpr (T == 64) {  // few enough to be on their way during the product
+    f16x4 x[H][4];
+    f32x4 d[4];
+    float dcol[4];
+    m.places([&](uint32_t r, uint32_t c, int n) {
+#pragma unroll
+      for (int h = 0; h < H; ++h) x[h][n] = *reinterpret_cast<const f16x4*>(tile + h * p * p + c * p + r);
+      d[n] = *reinterpret_cast<const f32x4*>(dr + r);
+      dcol[n] = dc[c];
     });
+    m.run(it.a + ti * T * p, it.a + tj * T * p, it.p, it.p, p * p, p * p, sh);
+    m.each([&](uint32_t, uint32_t, float* v, int n) {
+#pragma unroll
+      for (int h = H - 1; h >= 0; --h) add(v, d[n], dcol[n], x[h][n], h == H - 1);
+    });
+  } else {
+    m.run(it.a + ti * T * p, it.a + tj * T * p, it.p, it.p, p * p, p * p, sh);
+    constexpr int N = H <= M::kFit ? H : 1;
+    for (int plane = H - N; plane >= 0; plane -= N) {
+      m.template load_tiles<N>(tile + plane * p * p, p, p * p, sh);
+      m.each([&](uint32_t r, uint32_t c, float* v) {
+        const f32x4 d = *reinterpret_cast<const f32x4*>(dr + r);
+#pragma unroll
+        for (int h = N - 1; h >= 0; --h) add(v, d, dc[c], m.quad(sh + h * M::kTile, r, c), plane + h == H - 1);
+      });
+    }
   }
   m.each([&](uint32_t r, uint32_t c, float* v) {
 #pragma unroll
@@ -571,28 +625,52 @@ __global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kB
   const uint32_t across = it.p / T, ti = found.tile % across, tj = found.tile / across;
   if (tj >= it.q / T) return;
   const _Float16* from = it.t[step & 1];
-  Product<T, SPLIT> m;
-  m.run(it.b + ti * T * p, from + tj * T * p, it.p, it.p, p * p, p * q, sh);
+  using M = Product<T, SPLIT>;
+  M m;
   const uint64_t at = (uint64_t)tj * T * p + ti * T;
   const float* e = it.e + ti * T;
-  for (int plane = 1; plane >= 0; --plane) {
-    m.load_tile(from + plane * p * q + at, p, sh);
-    m.each([&](uint32_t r, uint32_t c, float* v) {
-      const f16x4 x = m.quad(sh, r, c);
+  auto add = [&](float* v, f32x4 d, f16x4 x, bool first) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = fmaf(a + e[r + k], (float)x[k], plane ? v[k] * (1.0f / kUnit) : v[k]);
+    for (int k = 0; k < 4; ++k) v[k] = fmaf(a + d[k], (float)x[k], first ? v[k] * (1.0f / kUnit) : v[k]);
+  };
+  if constexpr (T == 64) {
+    f16x4 x[2][4];
+    f32x4 d[4];
+    m.places([&](uint32_t r, uint32_t c, int n) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) x[h][n] = *reinterpret_cast<const f16x4*>(from + h * p * q + at + c * p + r);
+      d[n] = *reinterpret_cast<const f32x4*>(e + r);
     });
+    m.run(it.b + ti * T * p, from + tj * T * p, it.p, it.p, p * p, p * q, sh);
+    m.each([&](uint32_t, uint32_t, float* v, int n) {
+      add(v, d[n], x[1][n], true);
+      add(v, d[n], x[0][n], false);
+    });
+  } else {
+    m.run(it.b + ti * T * p, from + tj * T * p, it.p, it.p, p * p, p * q, sh);
+    constexpr int N = M::kFit >= 2 ? 2 : 1;
+    for (int plane = 2 - N; plane >= 0; plane -= N) {
+      m.template load_tiles<N>(from + plane * p * q + at, p, p * q, sh);
+      m.each([&](uint32_t r, uint32_t c, float* v) {
+        const f32x4 d = *reinterpret_cast<const f32x4*>(e + r);
+#pragma unroll
+        for (int h = N - 1; h >= 0; --h) add(v, d, m.quad(sh + h * M::kTile, r, c), plane + h == 1);
+      });
+    }
   }
   if (LAST) {
     write_out(m, it, ti, tj, sh);
     return;
   }
-  _Float16* to = it.t[~step & 1];
-  m.store_tile(to + at, p, sh, upper_halves);
-  m.store_tile(to + p * q + at, p, sh, lower_halves);
-  _Float16* x = it.x + (uint64_t)ti * T * q + tj * T;
-  m.store_rows(x, q, sh, upper_halves);
-  if (SPLIT) m.store_rows(x + p * q, q, sh, lower_halves);
+  _Float16 *to = it.t[~step & 1] + at, *x = it.x + (uint64_t)ti * T * q + tj * T;
+  using Out = typename M::Out;
+  if constexpr (SPLIT) {
+    const Out out[4] = {{to, p, false, false}, {to + p * q, p, false, true}, {x, q, true, false}, {x + p * q, q, true, true}};
+    m.store_tiles(out, sh);
+  } else {
+    const Out out[3] = {{to, p, false, false}, {to + p * q, p, false, true}, {x, q, true, false}};
+    m.store_tiles(out, sh);
+  }
 }
 
 // How a call's matrices are worked on: in groups whose scratch fits into
@@ -639,13 +717,16 @@ uint64_t lay_out(const PolarMatrix& m, uint32_t tile, bool split, uint32_t cuts,
 }
 
 // Large tiles feed the matrix cores better, small ones are more workgroups and less
-// padding. A third product of 512 tiles of 256 has them (16 matrices of 2048 x 4096:
-// 797 us against 1041 us with 128); of 512 tiles of 128, those (4 of 1024 x 2048
-// float32: 71 us against 114 us with 64) unless its rounds are few and its ends most
-// of it (12 of 500 x 1300: 40 and 39 us). A's half of the tiles is smaller: 256 tiles
-// or more are taken of that size (582 of 256: 390 us against 410 us with 128), others
-// of 64 (12 of 500 x 1300: 23 us against 29 us with 128).
-constexpr uint64_t kManyTiles = 512, kManyUpper = 256;
+// padding. A third product of 256 tiles of 256 has them (16 matrices of 2048 x 4096:
+// 797 us against 1041 us with 128; 4096 x 4096, all steps: 1910 against 2030 us); of
+// 512 tiles of 128, or 256 where both halves meet in them, those (4 of 1024 x 2048
+// float32: 71 us against 114 us with 64; 2048 x 2048 float32, all steps: 853 against
+// 948 us, but bf16 466 against 432) unless its rounds are few and its ends most of it
+// (12 of 500 x 1300: 40 and 39 us). A has half as many tiles: they are taken of that size
+// from 256 tiles on, or 128 of 256 or where both halves meet (4 of 1024 x 2048
+// float32, all steps: 787 us against 846, but bf16 467 against 407; 12 of 500 x 1300
+// bf16: 23 us with 64 against 29 us with 128).
+constexpr uint64_t kManyBig = 256, kManyTiles = 512, kManyPairs = 256, kManyUpper = 256, kManyUpperPairs = 128;
 
 struct Plan {
   std::vector<uint32_t> order;
@@ -682,8 +763,9 @@ Plan make_plan(const PolarMatrix* m, uint32_t n) {
       return std::min(m[a].rows, m[a].cols) > std::min(m[b].rows, m[b].cols);
     });
     const uint64_t many = plan.order.size() - begin;
-    const uint32_t tile = small ? 64 : big >= kManyTiles ? 256 : tiles >= kManyTiles && rounds >= 12 * many ? 128 : 64;
-    const uint32_t gram_tile = tile == 256 && upper[2] >= kManyUpper ? 256 : tile >= 128 && upper[1] >= kManyUpper ? 128 : 64;
+    const uint32_t tile = small ? 64 : big >= kManyBig ? 256 : tiles >= (split ? kManyPairs : kManyTiles) && rounds >= 12 * many ? 128 : 64;
+    const uint64_t most = split ? kManyUpperPairs : kManyUpper;
+    const uint32_t gram_tile = tile == 256 && upper[2] >= kManyUpperPairs ? 256 : tile >= 128 && upper[1] >= most ? 128 : 64;
     // A's few tiles are shared where rows are long enough to pay for the sums
     const bool shared = gram_tile == 64 && upper[0] <= 256 && up(longest, 64) / 64 * (split ? 3 : 1) >= 32;
     const uint32_t cuts = shared ? (uint32_t)(512 / std::max<uint64_t>(upper[0], 1)) : 1;
