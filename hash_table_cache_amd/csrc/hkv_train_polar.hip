@@ -58,6 +58,7 @@ struct PolarItem {
   double* partial;
   f32x4* cut;           // [cuts][tiles on and above A's diagonal][1024]
   uint32_t p, q;        // padded to the tile
+  uint32_t rows, cols;  // of X itself, not padded
   uint32_t flip;        // rows > cols: X is the transpose
   uint32_t parts;       // partial sums
   uint32_t part_tiles;  // tiles that each has
@@ -242,7 +243,7 @@ struct Product {
     const uint64_t hop = (uint64_t)(kThreads / 8) * stride;
     const uint32_t fr = lane & 31, key = (lane >> 5) ^ ((fr >> 1) & 7);
     const uint32_t ar = (wave / S::WN * FM * 32 + fr) * 8, br = (wave % S::WN * FN * 32 + fr) * 8;
-    const uint32_t blocks = K / 64, rounds = kPasses ? 3 * blocks : blocks;
+    const uint32_t blocks = (K + 63) / 64, rounds = kPasses ? 3 * blocks : blocks;
     const _Float16 *pa = kPasses ? a + plane_a : a, *pb = b;
     uint32_t left = blocks, pass = 0;
     auto advance = [&]() {
@@ -282,8 +283,8 @@ struct Product {
     }
   }
 
-  // use(row, column, four values of rows row .. row + 3, number of the quad if it is
-  // asked for) for each of a thread's quads, few of them at a time: registers are full.
+  // use(row, column, four values of rows row .. row + 3) for each of a thread's
+  // quads, few of them at a time: registers are full.
   template <typename Use>
   __device__ __forceinline__ void each(Use&& use) {
     uint32_t lane = threadIdx.x & 63;
@@ -305,22 +306,10 @@ struct Product {
           for (int k = 0; k < 4; ++k) v[k] = acc[i][j][g * 4 + k];
           const uint32_t r = wave / S::WN * FM * 32 + i * 32 + g * 8 + (lane >> 5) * 4;
           const uint32_t c = wave % S::WN * FN * 32 + j * 32 + (lane & 31);
-          if constexpr (std::is_invocable_v<Use, uint32_t, uint32_t, float*, int>)
-            use(r, c, v, (i * FN + j) * 4 + g);
-          else
-            use(r, c, v);
+          use(r, c, v);
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[i][j][g * 4 + k] = v[k];
         }
-  }
-
-  // use(row, column, number) for a thread's quads where nothing is held yet.
-  template <typename Use>
-  static __device__ __forceinline__ void places(Use&& use) {
-    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-#pragma unroll
-    for (int n = 0; n < FM * FN * 4; ++n)
-      use(wave / S::WN * FM * 32 + n / 4 / FN * 32 + n % 4 * 8 + (lane >> 5) * 4, wave % S::WN * FN * 32 + n / 4 % FN * 32 + (lane & 31), n);
   }
 
   // Tiles of halves in LDS, T columns of T, on their way from or to memory by 16
@@ -461,7 +450,7 @@ __global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kB
   if (tj >= it.p / T) return;
   const uint64_t p = it.p, q = it.q;
   Product<T, SPLIT> m;
-  m.run(it.x + ti * T * q, it.x + tj * T * q, it.q, it.q, p * q, p * q, sh);
+  m.run(it.x + ti * T * q, it.x + tj * T * q, it.q, it.cols, p * q, p * q, sh);
   write_gram<T, SPLIT>(m, it, ti, tj, sh);
 }
 
@@ -480,7 +469,7 @@ __global__ __launch_bounds__((Product<64, SPLIT>::kThreads), (Shape<64, SPLIT>::
   uint32_t ti, tj;
   upper_tile(tile, &ti, &tj);
   const uint64_t p = it.p, q = it.q;
-  const uint32_t blocks = it.q / 64, begin = cut * blocks / it.cuts, end = (cut + 1) * blocks / it.cuts;
+  const uint32_t blocks = (it.cols + 63) / 64, begin = cut * blocks / it.cuts, end = (cut + 1) * blocks / it.cuts;
   M m;
   m.run(it.x + ti * 64 * q + begin * 64, it.x + tj * 64 * q + begin * 64, it.q, (end - begin) * 64, p * q, p * q, sh);
   f32x4* to = it.cut + ((uint64_t)cut * tiles + tile) * 1024 + threadIdx.x;
@@ -531,32 +520,15 @@ __global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kB
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = fmaf(fmaf(c2, d[k] + dcol, b), (float)x[k], first ? v[k] * (c2 / kUnit) : v[k]);
   };
-  if constexpr (T == 64) {  // few enough to be on their way during the product
-    f16x4 x[H][4];
-    f32x4 d[4];
-    float dcol[4];
-    m.places([&](uint32_t r, uint32_t c, int n) {
+  m.run(it.a + ti * T * p, it.a + tj * T * p, it.p, it.rows, p * p, p * p, sh);
+  constexpr int N = H <= M::kFit ? H : 1;
+  for (int plane = H - N; plane >= 0; plane -= N) {
+    m.template load_tiles<N>(tile + plane * p * p, p, p * p, sh);
+    m.each([&](uint32_t r, uint32_t c, float* v) {
+      const f32x4 d = *reinterpret_cast<const f32x4*>(dr + r);
 #pragma unroll
-      for (int h = 0; h < H; ++h) x[h][n] = *reinterpret_cast<const f16x4*>(tile + h * p * p + c * p + r);
-      d[n] = *reinterpret_cast<const f32x4*>(dr + r);
-      dcol[n] = dc[c];
+      for (int h = N - 1; h >= 0; --h) add(v, d, dc[c], m.quad(sh + h * M::kTile, r, c), plane + h == H - 1);
     });
-    m.run(it.a + ti * T * p, it.a + tj * T * p, it.p, it.p, p * p, p * p, sh);
-    m.each([&](uint32_t, uint32_t, float* v, int n) {
-#pragma unroll
-      for (int h = H - 1; h >= 0; --h) add(v, d[n], dcol[n], x[h][n], h == H - 1);
-    });
-  } else {
-    m.run(it.a + ti * T * p, it.a + tj * T * p, it.p, it.p, p * p, p * p, sh);
-    constexpr int N = H <= M::kFit ? H : 1;
-    for (int plane = H - N; plane >= 0; plane -= N) {
-      m.template load_tiles<N>(tile + plane * p * p, p, p * p, sh);
-      m.each([&](uint32_t r, uint32_t c, float* v) {
-        const f32x4 d = *reinterpret_cast<const f32x4*>(dr + r);
-#pragma unroll
-        for (int h = N - 1; h >= 0; --h) add(v, d, dc[c], m.quad(sh + h * M::kTile, r, c), plane + h == H - 1);
-      });
-    }
   }
   m.each([&](uint32_t r, uint32_t c, float* v) {
 #pragma unroll
@@ -633,30 +605,15 @@ __global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kB
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = fmaf(a + d[k], (float)x[k], first ? v[k] * (1.0f / kUnit) : v[k]);
   };
-  if constexpr (T == 64) {
-    f16x4 x[2][4];
-    f32x4 d[4];
-    m.places([&](uint32_t r, uint32_t c, int n) {
+  m.run(it.b + ti * T * p, from + tj * T * p, it.p, it.rows, p * p, p * q, sh);
+  constexpr int N = M::kFit >= 2 ? 2 : 1;
+  for (int plane = 2 - N; plane >= 0; plane -= N) {
+    m.template load_tiles<N>(from + plane * p * q + at, p, p * q, sh);
+    m.each([&](uint32_t r, uint32_t c, float* v) {
+      const f32x4 d = *reinterpret_cast<const f32x4*>(e + r);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) x[h][n] = *reinterpret_cast<const f16x4*>(from + h * p * q + at + c * p + r);
-      d[n] = *reinterpret_cast<const f32x4*>(e + r);
+      for (int h = N - 1; h >= 0; --h) add(v, d, m.quad(sh + h * M::kTile, r, c), plane + h == 1);
     });
-    m.run(it.b + ti * T * p, from + tj * T * p, it.p, it.p, p * p, p * q, sh);
-    m.each([&](uint32_t, uint32_t, float* v, int n) {
-      add(v, d[n], x[1][n], true);
-      add(v, d[n], x[0][n], false);
-    });
-  } else {
-    m.run(it.b + ti * T * p, from + tj * T * p, it.p, it.p, p * p, p * q, sh);
-    constexpr int N = M::kFit >= 2 ? 2 : 1;
-    for (int plane = 2 - N; plane >= 0; plane -= N) {
-      m.template load_tiles<N>(from + plane * p * q + at, p, p * q, sh);
-      m.each([&](uint32_t r, uint32_t c, float* v) {
-        const f32x4 d = *reinterpret_cast<const f32x4*>(e + r);
-#pragma unroll
-        for (int h = N - 1; h >= 0; --h) add(v, d, m.quad(sh + h * M::kTile, r, c), plane + h == 1);
-      });
-    }
   }
   if (LAST) {
     write_out(m, it, ti, tj, sh);
@@ -711,6 +668,8 @@ uint64_t lay_out(const PolarMatrix& m, uint32_t tile, bool split, uint32_t cuts,
   it->cut = cuts > 1 ? reinterpret_cast<f32x4*>(take(p / 64 * (p / 64 + 1) / 2 * it->cuts * 64 * 64 * 4)) : nullptr;
   it->p = (uint32_t)p;
   it->q = (uint32_t)q;
+  it->rows = std::min(m.rows, m.cols);
+  it->cols = std::max(m.rows, m.cols);
   it->flip = m.rows > m.cols;
   it->m = m;
   return used;
