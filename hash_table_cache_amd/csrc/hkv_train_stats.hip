@@ -78,14 +78,23 @@ struct Spread {
     }
   }
 
-  // N elements, none above m. Up to F of them are added in 32 bits.
+  // What distances are taken from.
+  __device__ __forceinline__ float base() const { return m == -kInf ? 0.0f : m; }
+
+  // Up to F elements are added in 32 bits before 64, in es and as.
+  __device__ __forceinline__ void flush(float* es, float* as) {
+    s += (double)*es;
+    w += (double)*as;
+    *es = *as = 0.0f;
+  }
+
+  // N elements' distances from base(), none above it.
   template <int N, int F>
-  __device__ __forceinline__ void sum(const float* f, const Scale& c) {
-    const float base = m == -kInf ? 0.0f : m;
+  __device__ __forceinline__ void add(const float* t, const Scale& c, float* es, float* as) {
     float e[N], a[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float t = f[i] - base, z = fmaf(t, c.k_hi, t * c.k_lo);
+      const float z = fmaf(t[i], c.k_hi, t[i] * c.k_lo);
       e[i] = exp2_fast(z);
       a[i] = e[i] * fminf(-z, 1024.0f);  // a masked element has no weight, nor an infinite distance
     }
@@ -99,11 +108,30 @@ struct Spread {
           e[i + j] += e[i + j + w];
           a[i + j] += a[i + j + w];
         }
-      s += (double)e[i];
-      w += (double)a[i];
+      *es += e[i];
+      *as += a[i];
+      if (N >= F) flush(es, as);
     }
   }
 };
+
+// The elements of a vector less `base`. Halves are subtracted as they are: their
+// conversion takes as long as four subtractions (4096 x 131072 fp16: 195 us
+// against 245 us, with four vectors' sums in 32 bits before 64 and no alternatives).
+template <typename T>
+__device__ __forceinline__ void distances(u32x4 raw, float base, float* t) {
+  constexpr int K = Io<T>::K;
+  if constexpr (std::is_same_v<T, _Float16>) {
+    float one = 1.0f;
+    asm("" : "+s"(one));  // a multiplication by it would be left out, and with it the mixed instruction
+#pragma unroll
+    for (int i = 0; i < K; ++i) t[i] = fmaf((float)as_halves(raw[i / 2])[i % 2], one, -base);
+  } else {
+    Io<T>::unpack(raw, t);
+#pragma unroll
+    for (int i = 0; i < K; ++i) t[i] -= base;
+  }
+}
 
 template <typename V>
 __device__ __forceinline__ V sum_lanes(V v) {
@@ -412,20 +440,23 @@ __device__ __forceinline__ void scan_row(const T* row, const Cut<T, NT>& cut, ui
     }
     r.raise(most, c);
     if (TOP) tops.expect(most);
+    const float base = r.base();
+    float es = 0.0f, as = 0.0f;  // of up to kFloats elements
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       opaque(raw[i]);
       const uint32_t v = c0 + i * NT + tid;
       if (c0 + i * NT < cut.end) {
-        float f[K];
-        Io<T>::unpack(raw[i], f);
+        float t[K];
+        distances<T>(raw[i], base, t);
         if (__any(v == yv)) {
 #pragma unroll
           for (int j = 0; j < K; ++j)
-            if (v == yv && el == (uint32_t)j) f[j] = -kInf;
+            if (v == yv && el == (uint32_t)j) t[j] = -kInf;
         }
-        r.sum<K, Io<T>::kFloats>(f, c);
+        r.template add<K, Io<T>::kFloats>(t, c, &es, &as);
       }
+      if (K < Io<T>::kFloats && ((i + 1) * K % Io<T>::kFloats == 0 || i + 1 == NV)) r.flush(&es, &as);
     }
     if (TOP) {
       // vectors in which some lane's maximum may pass; the bound only rises
@@ -465,7 +496,9 @@ __device__ __forceinline__ void scan_row(const T* row, const Cut<T, NT>& cut, ui
     }
     if (i == y) f = -kInf;
     r.raise(f, c);
-    r.sum<1, 1>(&f, c);
+    f -= r.base();
+    float es = 0.0f, as = 0.0f;
+    r.template add<1, 1>(&f, c, &es, &as);
   }
   if (TOP) tops.join();
 }
