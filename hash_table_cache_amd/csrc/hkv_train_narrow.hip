@@ -110,7 +110,7 @@ struct Narrow {
 
   template <typename Use>
   __device__ __forceinline__ void cells(const PolarMatrix& m, bool flip, Use&& use) const {
-    const uint32_t across = flip ? 64 : kBlockCols;
+    const uint32_t across = flip ? P : kBlockCols;
 #pragma unroll 8
     for (uint32_t e = threadIdx.x; e < P * kBlockCols; e += kNarrowThreads) {
       const uint32_t a = e / across, b = e % across, r = flip ? b : a, c = flip ? a : b;
