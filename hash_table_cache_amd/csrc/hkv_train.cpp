@@ -275,12 +275,15 @@ class Places {
   std::vector<Place> list_;
 };
 
-hkv_status check_layout(uint64_t cols, uint64_t stride, uint64_t dtype, const char* what, uint64_t i, uint64_t* es) {
+hkv_status check_layout(uint64_t rows, uint64_t cols, uint64_t stride, uint64_t dtype, const char* what, uint64_t i, uint64_t* es) {
   if (dtype > hkvt::kF16 || !kind_size((uint32_t)dtype, es))
     return fail(HKV_EINVAL, "%s[%llu]: dtype %llu", what, (unsigned long long)i, (unsigned long long)dtype);
   if (stride < cols || stride > (1ull << 40))
     return fail(HKV_EINVAL, "%s[%llu]: stride = %llu with %llu columns", what, (unsigned long long)i,
                 (unsigned long long)stride, (unsigned long long)cols);
+  if (too_far(rows, stride))
+    return fail(HKV_EINVAL, "%s[%llu]: stride = %llu with %llu rows reaches past any memory", what, (unsigned long long)i,
+                (unsigned long long)stride, (unsigned long long)rows);
   return HKV_OK;
 }
 
@@ -593,8 +596,8 @@ HKV_API hkv_status hkv_orthogonalize(uint64_t matrices, const hkv_matrix* list, 
       if (m.rows == 0 || m.cols == 0) continue;
       HKV_TRY(check_sides(m.rows, m.cols, i));
       uint64_t in_size = 0, out_size = 0;
-      HKV_TRY(check_layout(m.cols, m.in_stride, m.in_dtype, "in", i, &in_size));
-      HKV_TRY(check_layout(m.cols, m.out_stride, m.out_dtype, "out", i, &out_size));
+      HKV_TRY(check_layout(m.rows, m.cols, m.in_stride, m.in_dtype, "in", i, &in_size));
+      HKV_TRY(check_layout(m.rows, m.cols, m.out_stride, m.out_dtype, "out", i, &out_size));
       HKV_TRY(check_place(buffers, m.in, m.rows, m.cols, m.in_stride, in_size, "in", i));
       HKV_TRY(check_place(buffers, m.out, m.rows, m.cols, m.out_stride, out_size, "out", i));
       const bool same = m.in == m.out && m.in_stride == m.out_stride && m.in_dtype == m.out_dtype;
@@ -632,9 +635,9 @@ HKV_API hkv_status hkv_muon_update(uint64_t matrices, const hkv_muon_matrix* lis
       if (!std::isfinite(m.lr) || !std::isfinite(m.scale))
         return fail(HKV_EINVAL, "matrix %llu: lr = %g, scale = %g", (unsigned long long)i, m.lr, m.scale);
       uint64_t ws = 0, gs = 0, ms = 0;
-      HKV_TRY(check_layout(m.cols, m.weight_stride, m.weight_dtype, "weight", i, &ws));
-      HKV_TRY(check_layout(m.cols, m.grad_stride, m.grad_dtype, "grad", i, &gs));
-      HKV_TRY(check_layout(m.cols, m.momentum_stride, HKV_F32, "momentum", i, &ms));
+      HKV_TRY(check_layout(m.rows, m.cols, m.weight_stride, m.weight_dtype, "weight", i, &ws));
+      HKV_TRY(check_layout(m.rows, m.cols, m.grad_stride, m.grad_dtype, "grad", i, &gs));
+      HKV_TRY(check_layout(m.rows, m.cols, m.momentum_stride, HKV_F32, "momentum", i, &ms));
       HKV_TRY(check_place(buffers, m.weight, m.rows, m.cols, m.weight_stride, ws, "weight", i));
       HKV_TRY(check_place(buffers, m.grad, m.rows, m.cols, m.grad_stride, gs, "grad", i));
       HKV_TRY(check_place(buffers, m.momentum, m.rows, m.cols, m.momentum_stride, ms, "momentum", i));
