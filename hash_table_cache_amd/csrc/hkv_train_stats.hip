@@ -257,13 +257,31 @@ __device__ __forceinline__ void wave_sync() {
 template <int W, int H>
 struct TopsShared {
   Key held[W][H];
+  u32x4 vecs[W][H];  // vectors with elements that may pass, and the first one's index
+  uint32_t at[W][H];
   float bound[W];
   uint32_t count[W];
 };
 
+// Takes the first element off a vector.
+template <typename T>
+__device__ __forceinline__ float first_of(u32x4& x) {
+  const uint32_t w = x[0];
+  if constexpr (sizeof(T) == 4) {
+    x = u32x4{x[1], x[2], x[3], 0};
+    return as_float(w);
+  } else {
+    x = u32x4{w >> 16 | x[1] << 16, x[1] >> 16 | x[2] << 16, x[2] >> 16 | x[3] << 16, x[3] >> 16};
+    return (float)__builtin_bit_cast(T, (uint16_t)w);
+  }
+}
+
 // The k largest elements that a wave has seen, sorted, one a lane, and a bound
-// under which no element comes among the team's. Elements that pass the bound are
-// gathered in LDS and join the list 64 at a time.
+// under which no element comes among the team's. Vectors of which an element passes
+// the bound are gathered in LDS and looked through 64 at a time, a lane each, for
+// they come one or two at a time; their elements that pass are gathered again and
+// join the list 64 at a time (4096 x 131072 fp16, 64 alternatives: 211 us against
+// 283 us with vectors looked through as they come).
 // The bound: a wave knows j = ceil(k / W) lanes that have seen an element of at
 // least b_w; then k elements are at least the ceil(k / j)-th largest of the b_w. Of a row of
 // random order few more than k elements pass it (64 of 131072 by 8 waves: about
@@ -276,6 +294,7 @@ struct Tops {
   float bound = -kInf;    // an element of this value passes
   uint32_t bound_at = 0;  // if its index is lower
   uint32_t count = 0;     // gathered
+  uint32_t vecs = 0;      // vectors
   float seen = -kInf;     // by this lane
   bool first = true, taken = false;
   Shared& sh;
@@ -327,6 +346,40 @@ struct Tops {
     if (in) sh.held[wave][count + below] = key_of(f, i);
     count += __popcll(who);
     if (count >= 64) take();
+  }
+
+  // Gathers the vectors of lanes whose largest element `mx` may pass; `i` is the
+  // index of their first element.
+  template <typename T>
+  __device__ __forceinline__ void gather(u32x4 raw, float mx, uint32_t i) {
+    const bool in = mx >= fmaxf(bound, -__FLT_MAX__);
+    const uint64_t who = __ballot(in);
+    if (who == 0) return;
+    const uint32_t below = __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0));
+    if (in) {
+      sh.vecs[wave][vecs + below] = raw;
+      sh.at[wave][vecs + below] = i;
+    }
+    vecs += __popcll(who);
+    if (vecs >= 64) look<T>();
+  }
+
+  // Looks through the last 64 vectors, or all of fewer.
+  template <typename T>
+  __device__ __forceinline__ void look() {
+    constexpr int K = Io<T>::K;
+    const uint32_t n = min(vecs, 64u);
+    vecs -= n;
+    wave_sync();
+    const bool mine = (uint32_t)lane < n;
+    u32x4 x = sh.vecs[wave][vecs + (mine ? lane : 0)];
+    const uint32_t i = sh.at[wave][vecs + (mine ? lane : 0)];
+    wave_sync();
+#pragma unroll 1
+    for (int j = 0; j < K; ++j) {
+      const float f = first_of<T>(x);
+      add(f, i + j, mine && f >= -__FLT_MAX__);
+    }
   }
 
   // Joins the last 64 gathered ones, or all of fewer.
@@ -459,35 +512,12 @@ __device__ __forceinline__ void scan_row(const T* row, const Cut<T, NT>& cut, ui
       if (K < Io<T>::kFloats && ((i + 1) * K % Io<T>::kFloats == 0 || i + 1 == NV)) r.flush(&es, &as);
     }
     if (TOP) {
-      // vectors in which some lane's maximum may pass; the bound only rises
-      const float bound = fmaxf(tops.bound, -__FLT_MAX__);
-      uint32_t some = 0;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) some |= __any(mx[i] >= bound) ? 1u << i : 0u;
-      while (some) {
-        const int at = __builtin_ctz(some);
-        some &= some - 1;
-        u32x4 x = raw[0];
-#pragma unroll
-        for (int i = 1; i < NV; ++i)
-          if (at == i) x = raw[i];
-        float f[K];
-        Io<T>::unpack(x, f);
-        uint32_t may = 0;  // this lane's elements
-#pragma unroll
-        for (int j = 0; j < K; ++j) may |= f[j] >= bound ? 1u << j : 0u;
-        const uint32_t base = cut.head + (c0 + at * NT + tid) * K;
-        while (__any(may != 0)) {
-          const uint32_t j = __builtin_ctz(may | 1u << 31);
-          float one = f[0];
-#pragma unroll
-          for (int i = 1; i < K; ++i) one = j == (uint32_t)i ? f[i] : one;
-          tops.add(one, base + j, may != 0);
-          may &= may - 1;
-        }
-      }
+      for (int i = 0; i < NV; ++i) tops.template gather<T>(raw[i], mx[i], cut.head + (c0 + i * NT + tid) * K);
     }
   }
+  if (TOP)
+    while (tops.vecs) tops.template look<T>();
   for (uint32_t j0 = 0; j0 < cut.singles(); j0 += NT) {
     const uint32_t j = j0 + tid, i = cut.single(j);
     float f = j < cut.singles() ? (float)row[i] : -kInf;
@@ -748,13 +778,11 @@ hipError_t stats_t(const StatsArgs& a, void* ws, hipStream_t s) {
   if (nv <= 64 * 4) return stats_n<T, 64, 4>(a, s);
   // Small teams where rows are many, as for log-probabilities: more of them are in
   // a compute unit while others sort (20 alternatives, teams of 64 threads against
-  // 256: 30000 x 2500 bf16 77 us against 194 us, 8000 x 8000 53 against 70; of 256
-  // against 512: 4096 x 131072 fp16 250 against 300, but 300 x 131072 64 against 46).
-  if (a.l.rows >= 1024) {
-    if (nv <= 64 * 16) return stats_n<T, 64, 8>(a, s);
-    return stats_n<T, 256, 8>(a, s);
-  }
-  if (nv <= 256 * 4) return stats_n<T, 256, 4>(a, s);
+  // 256: 30000 x 2500 bf16 71 us against 219 us, 8000 x 8000 40 against 69; of 256
+  // against 512: 4096 x 131072 fp16 210 against 247, 1000 x 60000 bf16 37 against
+  // 45, but 300 x 131072 40 against 37).
+  if (nv <= 64 * 16) return a.l.rows >= 1024 ? stats_n<T, 64, 8>(a, s) : stats_n<T, 256, 4>(a, s);
+  if (a.l.rows >= 512) return stats_n<T, 256, 8>(a, s);
   if (a.l.rows < kFewRows && nv <= kOneRound) return stats_n<T, 1024, 4>(a, s);
   return stats_n<T, 512, 8>(a, s);
 }
