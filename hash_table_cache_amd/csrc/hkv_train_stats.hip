@@ -744,6 +744,7 @@ hipError_t stats_n(const StatsArgs& a, hipStream_t s) {
 // shared against not: 64 x 131072 bf16 21.5 us against 32.5 us, 100 rows 24.8
 // against 32.8, but 200 rows 34.2 against 32.6.
 constexpr uint32_t kStatsShared = 128;
+constexpr uint32_t kUnits = 256;      // compute units
 constexpr uint32_t kOneRound = 4096;  // vectors
 
 bool shared_stats(const Logits& l) {
@@ -780,9 +781,9 @@ hipError_t stats_t(const StatsArgs& a, void* ws, hipStream_t s) {
   // a compute unit while others sort (20 alternatives, teams of 64 threads against
   // 256: 30000 x 2500 bf16 71 us against 219 us, 8000 x 8000 40 against 69; of 256
   // against 512: 4096 x 131072 fp16 210 against 247, 1000 x 60000 bf16 37 against
-  // 45, but 300 x 131072 40 against 37).
+  // 45, but 512 x 131072, of which teams of 512 are all there at once, 43 against 40).
   if (nv <= 64 * 16) return a.l.rows >= 1024 ? stats_n<T, 64, 8>(a, s) : stats_n<T, 256, 4>(a, s);
-  if (a.l.rows >= 512) return stats_n<T, 256, 8>(a, s);
+  if (a.l.rows > 2 * kUnits) return stats_n<T, 256, 8>(a, s);
   if (a.l.rows < kFewRows && nv <= kOneRound) return stats_n<T, 1024, 4>(a, s);
   return stats_n<T, 512, 8>(a, s);
 }
