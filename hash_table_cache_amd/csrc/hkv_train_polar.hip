@@ -381,23 +381,38 @@ struct Product {
 };
 
 // Consecutive workgroups go to the 8 dies in turn. Each die takes an eighth of the
-// work, of tiles next to each other, so that what they share is in its cache: whole
-// matrices where there are many (16 of 2048 x 4096 bf16, all steps: 6.78 ms against
-// 7.14 ms with an eighth of each matrix's tiles to every die; 12 of 500 x 1300: 275
-// us against 310 us). `first`: each die's first tile, and their number.
+// work, of tiles next to each other, so that what they share is in its cache (16 of
+// 2048 x 4096 bf16, all steps: 6.78 ms against 7.14 ms with an eighth of each matrix's
+// tiles to every die; 12 of 500 x 1300: 275 us against 310 us). Tiles of 256 are few
+// rounds of the chip, and a die with long products alone ends late: of many matrices
+// their work is cut into `rows` times 8 pieces, about half a matrix each, which go to
+// the dies forth and back, so that each has long products and, last, short ones (16
+// of 1100 x 3400 to 3000 x 5000: 7.48 ms against 7.85 ms; smaller tiles lose by it, 40 of
+// 128 x 512: 158 us against 142 us). `first`: each piece's first tile, and their number.
+constexpr uint32_t kMostRows = 4;
+
 struct Dies {
-  uint32_t first[kDies + 1];
+  uint32_t rows;
+  uint32_t first[kMostRows * kDies + 1];
 };
 
 // The workgroup's matrix and its tile of it; false where its die has no more.
 __device__ __forceinline__ bool find_tile(const PolarItem* items, uint32_t n, const Dies& dies, uint32_t PolarItem::* first,
                                           const PolarItem** item, uint32_t* tile) {
-  const uint32_t die = blockIdx.x % kDies, at = dies.first[die] + blockIdx.x / kDies;
-  if (at >= dies.first[die + 1]) return false;
-  const PolarItem& it = find_item(items, n, at, first);
-  *item = &it;
-  *tile = at - it.*first;
-  return true;
+  const uint32_t die = blockIdx.x % kDies;
+  uint32_t at = blockIdx.x / kDies;
+  for (uint32_t r = 0; r < dies.rows; ++r) {
+    const uint32_t piece = r * kDies + (r % 2 ? kDies - 1 - die : die);
+    const uint32_t begin = dies.first[piece], tiles = dies.first[piece + 1] - begin;
+    if (at < tiles) {
+      const PolarItem& it = find_item(items, n, begin + at, first);
+      *item = &it;
+      *tile = begin + at - it.*first;
+      return true;
+    }
+    at -= tiles;
+  }
+  return false;
 }
 
 // Number of a tile on or above the diagonal -> its place: 0 (0,0), 1 (0,1), 2 (1,1), 3 (0,2) ...
@@ -732,6 +747,10 @@ Plan make_plan(const PolarMatrix* m, uint32_t n) {
     const uint32_t tile = small ? 64 : big >= kManyBig ? 256 : tiles >= (split ? kManyPairs : kManyTiles) && rounds >= 12 * many ? 128 : 64;
     const uint64_t most = split ? kManyUpperPairs : kManyUpper;
     const uint32_t gram_tile = tile == 256 && upper[2] >= kManyUpperPairs ? 256 : tile >= 128 && upper[1] >= most ? 128 : 64;
+    if (tile < 256) {  // long and short ones by turns: every die has both
+      const std::vector<uint32_t> sorted(plan.order.begin() + begin, plan.order.end());
+      for (uint64_t k = 0; k < many; ++k) plan.order[begin + k] = sorted[k % 2 ? many - 1 - k / 2 : k / 2];
+    }
     // A's few tiles are shared where rows are long enough to pay for the sums
     const bool shared = gram_tile == 64 && upper[0] <= 256 && up(longest, 64) / 64 * (split ? 3 : 1) >= 32;
     const uint32_t cuts = shared ? (uint32_t)(512 / std::max<uint64_t>(upper[0], 1)) : 1;
@@ -766,21 +785,29 @@ class Tiles {
     count_ += tiles;
     return count_ - tiles;
   }
-  // An eighth of the work to each die.
-  void share() {
+  void share(uint32_t tile) {
+    dies_.rows = tile == 256 ? std::max(1u, std::min(kMostRows, (uint32_t)list_.size() / 4)) : 1;
+    const uint32_t pieces = dies_.rows * kDies;
     uint64_t whole = 0, before = 0;
     for (const Some& s : list_) whole += (uint64_t)s.tiles * s.each;
-    uint32_t first = 0, die = 1;
+    uint32_t first = 0, piece = 1;
     for (const Some& s : list_) {
       const uint64_t after = before + (uint64_t)s.tiles * s.each;
-      for (; die < kDies && after >= whole * die / kDies; ++die)
-        dies_.first[die] = first + (uint32_t)((whole * die / kDies - before + s.each - 1) / s.each);
+      for (; piece < pieces && after >= whole * piece / pieces; ++piece)
+        dies_.first[piece] = first + (uint32_t)((whole * piece / pieces - before + s.each - 1) / s.each);
       before = after;
       first += s.tiles;
     }
-    dies_.first[kDies] = count_;
+    dies_.first[pieces] = count_;
     uint32_t most = 0;
-    for (uint32_t d = 0; d < kDies; ++d) most = std::max(most, dies_.first[d + 1] - dies_.first[d]);
+    for (uint32_t d = 0; d < kDies; ++d) {
+      uint32_t tiles = 0;
+      for (uint32_t r = 0; r < dies_.rows; ++r) {
+        const uint32_t p = r * kDies + (r % 2 ? kDies - 1 - d : d);
+        tiles += dies_.first[p + 1] - dies_.first[p];
+      }
+      most = std::max(most, tiles);
+    }
     grid_ = most * kDies;
   }
   const Dies& dies() const { return dies_; }
@@ -887,7 +914,7 @@ hipError_t run_group(const PolarMatrix* m, const uint32_t* order, const Group& g
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  for (Tiles* tiles : {&l.cut, &l.gram, &l.square, &l.next}) tiles->share();
+  for (Tiles* tiles : {&l.cut, &l.gram, &l.square, &l.next}) tiles->share(g.tile);
   polar_norm_kernel<<<l.parts, kPolarThreads, 0, s>>>(items, n, r);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
