@@ -720,7 +720,9 @@ __global__ __launch_bounds__(Team<NT>::kBlock) void stats_backward_kernel(const 
   });
   for (uint32_t j = tid; j < cut.singles(); j += NT) {
     const uint32_t i = cut.single(j);
-    out[i] = (T)back_of((float)row[i], a.c, lse, h, g, ge);
+    float d = back_of((float)row[i], a.c, lse, h, g, ge);
+    asm("" : "+v"(d));  // rounded to 32 bits first, as a vector's elements are, not once with the product
+    out[i] = (T)d;
   }
   if (tid == owner)
     out[y] = (T)(float)((double)g * rest_of_label(fy, a.c, lse) + (double)back_of(fy, a.c, lse, h, 0.0f, ge));
