@@ -311,7 +311,9 @@ struct Narrow {
     __syncthreads();
   }
 
-  // X <- a X + B X: every wave its own columns.
+  // X <- a X + B X: every wave its own columns. Both halves of X in either precision
+  // (with the upper one alone directions that X does not have would come in), here in
+  // the last steps too: 64 x 64 bf16 19.5 us, with the upper half alone 18.3 us.
   __device__ __forceinline__ void next(float a) {
     if (wave * 16 >= cols) return;
 #pragma unroll
@@ -320,7 +322,7 @@ struct Narrow {
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = x[i][k];
       quad_at(sh.cols[0], col(), row(i)) = upper_halves(v);
-      if (SPLIT) quad_at(sh.cols[1], col(), row(i)) = lower_halves(v);
+      quad_at(sh.cols[1], col(), row(i)) = lower_halves(v);
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -330,12 +332,13 @@ struct Narrow {
     for (int ks = 0; ks < P / 32; ++ks) {
       f16x8 fx[2];
 #pragma unroll
-      for (int p = 0; p < planes; ++p) fx[p] = sh.cols[p][slim(col(), ks * 4 + (lane >> 4))];
+      for (int p = 0; p < 2; ++p) fx[p] = sh.cols[p][slim(col(), ks * 4 + (lane >> 4))];
 #pragma unroll
       for (int i = 0; i < F; ++i) {
         f16x8 fb[2];
 #pragma unroll
         for (int p = 0; p < planes; ++p) fb[p] = sh.b[p][slim(i * 16 + (lane & 15), ks * 4 + (lane >> 4))];
+        if (!SPLIT) s[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[0], fx[1], s[i], 0, 0, 0);
         s[i] = product(s[i], fb, fx);
       }
     }

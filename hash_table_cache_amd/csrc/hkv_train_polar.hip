@@ -16,14 +16,24 @@
 //   - split: a number is the sum of two halves, and a product three products of
 //     halves (what is left out is 2^-22 of it): as precise as float32.
 //   - single: one product of halves. Rounding would still cost most where it
-//     counts: a X, which alone carries the small singular values, and the
+//     counts: in X, whose small singular values a X carries, and on the
 //     diagonals of A and B, which near the end are nearly all of them. So X
-//     keeps both halves for a X, the diagonals are kept out of the halves in 32
-//     bits, D = diag A, E = diag B:
+//     keeps both halves, the diagonals are kept out of the halves in 32 bits,
+//     D = diag A, E = diag B:
 //       B X = E X + (B - E) X,  A A = (A - D)(A - D) + D (A - D) + (A - D) D + D D.
-//     Results are off by 4e-4 to 9e-4 of their size (2-norm), less than their
-//     rounding to bf16 (1.7e-3); with A, B and X rounded as they are, by 1.3e-3
-//     for a full spectrum and by 4e-2 for one of 8 directions among 512.
+//     (B - E) X takes both halves of X too, in two products. Then a step is a
+//     product M X of the X that is held, and what A's and B's roundings do to M
+//     turns X's directions without adding any. With the upper half alone, E times
+//     its rounding stays behind in directions that X does not have, where only a
+//     and E act, and every step multiplies it by a: 64 x 64 of rank 1, 5 steps,
+//     would be off by 7e-3, of rank 16 after 10 steps by 1.2 (2-norm). In the last
+//     two steps, after which it is multiplied once at most, the upper half is
+//     enough: 16 of about 2048 x 4096 9.0 ms (7.5 ms with it alone throughout, 10.0
+//     ms with both throughout), 2048 x 2048 534 us (422, 601), two of 10007 x 321
+//     275 us (247, 291). Results are off by 2e-4 to 1.6e-3, less than their rounding
+//     to bf16 (1.7e-3), for full, decaying and low-rank spectra and up to 6 steps. A
+//     has X's rounding in 2^-12 of itself; where all elements are rounded alike (a
+//     multiple of the identity) that moves all singular values alike, by up to 7e-3.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -229,10 +239,13 @@ struct Product {
   }
 
   // Rows `stride` apart, K inner elements from the first one; the lower halves lie
-  // plane_a and plane_b elements behind the upper ones.
+  // plane_a and plane_b elements behind the upper ones. PRODUCTS of halves: upper x
+  // upper, before it (2) upper x lower, before that (3) lower x upper.
+  template <int PRODUCTS = SPLIT ? 3 : 1>
   __device__ __forceinline__ void run(const _Float16* a, const _Float16* b, uint32_t stride, uint32_t K, uint64_t plane_a,
                                       uint64_t plane_b, Shared& sh) {
-    constexpr bool kPasses = SPLIT && H == 1;
+    constexpr uint32_t kPasses = H == 2 ? 1 : PRODUCTS;
+    static_assert(H == 1 || PRODUCTS == 3, "stage() takes both halves");
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 #pragma unroll
     for (int i = 0; i < FM; ++i)
@@ -242,16 +255,16 @@ struct Product {
     const uint64_t hop = (uint64_t)(kThreads / 8) * stride;
     const uint32_t fr = lane & 31, key = (lane >> 5) ^ ((fr >> 1) & 7);
     const uint32_t ar = (wave / S::WN * FM * 32 + fr) * 8, br = (wave % S::WN * FN * 32 + fr) * 8;
-    const uint32_t blocks = (K + 63) / 64, rounds = kPasses ? 3 * blocks : blocks;
-    const _Float16 *pa = kPasses ? a + plane_a : a, *pb = b;
-    uint32_t left = blocks, pass = 0;
+    const uint32_t blocks = (K + 63) / 64, rounds = kPasses * blocks;
+    const _Float16 *pa = kPasses == 3 ? a + plane_a : a, *pb = kPasses == 2 ? b + plane_b : b;
+    uint32_t left = blocks, passes = kPasses;  // this one included
     auto advance = [&]() {
       pa += 64;
       pb += 64;
-      if (kPasses && --left == 0) {
+      if (kPasses > 1 && --left == 0) {
+        --passes;
         pa = a;
-        pb = pass == 0 ? b + plane_b : b;
-        ++pass;
+        pb = passes == 2 ? b + plane_b : b;
         left = blocks;
       }
     };
@@ -607,8 +620,8 @@ __device__ __forceinline__ void write_out(Product<T, SPLIT>& m, const PolarItem&
 }
 
 // a X + B X of step `k`; the last one's goes to its destination. Columns of the
-// tile are rows of X^T.
-template <int T, bool SPLIT, bool LAST>
+// tile are rows of X^T. PRODUCTS of halves make B X.
+template <int T, bool SPLIT, bool LAST, int PRODUCTS>
 __global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kBlocks)) void polar_next_kernel(const PolarItem* items, uint32_t n,
                                                                                          const Dies dies, float a, uint32_t step) {
   __shared__ typename Product<T, SPLIT>::Shared sh;
@@ -627,7 +640,7 @@ __global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kB
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = fmaf(a + d[k], (float)x[k], first ? v[k] * (1.0f / kUnit) : v[k]);
   };
-  m.run(it.b + ti * T * p, from + tj * T * p, it.p, it.rows, p * p, p * q, sh);
+  m.template run<PRODUCTS>(it.b + ti * T * p, from + tj * T * p, it.p, it.rows, p * p, p * q, sh);
   constexpr int N = M::kFit >= 2 ? 2 : 1;
   for (int plane = 2 - N; plane >= 0; plane -= N) {
     m.template load_tiles<N>(from + plane * p * q + at, p, p * q, sh);
@@ -857,12 +870,26 @@ hipError_t square_t(const PolarItem* items, uint32_t n, const Launches& l, uint3
   return hipGetLastError();
 }
 
+template <int T, bool SPLIT, bool LAST, int PRODUCTS>
+void launch_next(const PolarItem* items, uint32_t n, const Launches& l, float a, uint32_t step, hipStream_t s) {
+  polar_next_kernel<T, SPLIT, LAST, PRODUCTS><<<l.next.grid(), Product<T, SPLIT>::kThreads, 0, s>>>(items, n, l.next.dies(), a, step);
+}
+
 template <int T, bool SPLIT>
-hipError_t next_t(const PolarItem* items, uint32_t n, const Launches& l, float a, uint32_t step, bool last, hipStream_t s) {
-  if (last)
-    polar_next_kernel<T, SPLIT, true><<<l.next.grid(), Product<T, SPLIT>::kThreads, 0, s>>>(items, n, l.next.dies(), a, step);
-  else
-    polar_next_kernel<T, SPLIT, false><<<l.next.grid(), Product<T, SPLIT>::kThreads, 0, s>>>(items, n, l.next.dies(), a, step);
+hipError_t next_t(const PolarItem* items, uint32_t n, const Launches& l, float a, uint32_t step, uint32_t steps, hipStream_t s) {
+  if constexpr (SPLIT) {
+    if (step + 1 == steps)
+      launch_next<T, true, true, 3>(items, n, l, a, step, s);
+    else
+      launch_next<T, true, false, 3>(items, n, l, a, step, s);
+  } else {
+    if (step + 1 == steps)
+      launch_next<T, false, true, 1>(items, n, l, a, step, s);
+    else if (step + 2 == steps)  // what X's rounding leaves is multiplied by `a` once more
+      launch_next<T, false, false, 1>(items, n, l, a, step, s);
+    else
+      launch_next<T, false, false, 2>(items, n, l, a, step, s);
+  }
   return hipGetLastError();
 }
 
@@ -874,13 +901,12 @@ hipError_t steps_t(const PolarItem* items, uint32_t n, const Launches& l, const 
     if (e != hipSuccess) return e;
     if ((e = square_t<SPLIT>(items, n, l, g.gram_tile, (float)c[1], (float)c[2], s)) != hipSuccess) return e;
     const float a = (float)c[0];
-    const bool last = k + 1 == steps;
     if (g.tile == 256)
-      e = next_t<256, SPLIT>(items, n, l, a, k, last, s);
+      e = next_t<256, SPLIT>(items, n, l, a, k, steps, s);
     else if (g.tile == 128)
-      e = next_t<128, SPLIT>(items, n, l, a, k, last, s);
+      e = next_t<128, SPLIT>(items, n, l, a, k, steps, s);
     else
-      e = next_t<64, SPLIT>(items, n, l, a, k, last, s);
+      e = next_t<64, SPLIT>(items, n, l, a, k, steps, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;

@@ -498,7 +498,8 @@ def orthogonalize(matrices, *, steps: int = 5, coefficients=NEWTON_SCHULZ, eps: 
     coefficients: a, b, c, or a sequence of `steps` such triples. out: tensors of
     the matrices' shapes that take the results (they may be the matrices); their
     types decide the precision, float32 and float16 being computed as precisely
-    as float32 is, bfloat16 to less than its rounding."""
+    as float32 is, bfloat16 to less than its rounding with the coefficients and up
+    to 6 steps (include/hkv_train.h has the exceptions)."""
     matrices = list(matrices)
     if not matrices:
         raise ValueError("orthogonalize needs at least one matrix")
@@ -539,8 +540,9 @@ def muon_update(weights, grads, momenta, lr, *, momentum: float = 0.95, nesterov
     momenta: float32, kept by the caller (zeros at first), in place too. lr: a
     number, or one for each matrix. scale multiplies lr by the matrix's shape:
     "shape" by sqrt(max(1, rows / cols)), "rms" by 0.2 sqrt(max(rows, cols)),
-    which gives updates the size of an adaptive optimiser's, None by 1. Weights of
-    float32 and float16 are computed as precisely as float32 is."""
+    which gives updates the size of an adaptive optimiser's, None by 1. The weights'
+    types decide the precision as out's do in orthogonalize: a program to which
+    bfloat16's is not enough keeps its weights in float32."""
     weights, grads, momenta = list(weights), list(grads), list(momenta)
     n = len(weights)
     if not weights:
