@@ -6,6 +6,7 @@
 #include <cstdio>
 #include <cstring>
 #include <exception>
+#include <numeric>
 #include <string>
 #include <vector>
 
@@ -235,12 +236,13 @@ hkv_status check_coefficients(uint32_t steps, const double* c) {
 }
 
 // The memory of matrices: no written one may share an element with another. Two
-// whose ranges overlap may lie in different columns of the same wider rows.
+// whose ranges overlap may lie in different columns of the same wider rows, and one
+// of them have only some of the rows, or a single one.
 class Places {
  public:
   void add(const void* p, uint64_t rows, uint64_t cols, uint64_t stride, uint64_t es, bool written) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    list_.push_back({a, a + ((rows - 1) * stride + cols) * es, stride * es, cols * es, written});
+    list_.push_back({a, a + ((rows - 1) * stride + cols) * es, rows > 1 ? stride * es : 0, cols * es, written});
   }
   bool clash() {
     std::sort(list_.begin(), list_.end(), [](const Place& a, const Place& b) { return a.begin < b.begin; });
@@ -263,14 +265,16 @@ class Places {
  private:
   struct Place {
     uintptr_t begin, end;
-    uint64_t stride, width;
+    uint64_t stride, width;  // stride: 0 of a single row
     bool written;
   };
-  // o begins first and reaches past p's beginning.
+  // o begins first and reaches past p's beginning. Rows of both are a multiple of
+  // their strides' common divisor apart.
   static bool apart(const Place& o, const Place& p) {
-    if (o.stride != p.stride) return false;
-    const uint64_t column = (p.begin - o.begin) % o.stride;
-    return column >= o.width && column + p.width <= o.stride;
+    const uint64_t line = std::gcd(o.stride, p.stride);
+    if (line == 0) return false;
+    const uint64_t column = (p.begin - o.begin) % line;
+    return column >= o.width && column + p.width <= line;
   }
   std::vector<Place> list_;
 };

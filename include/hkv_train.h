@@ -227,8 +227,9 @@ hkv_status hkv_clip_grad_norm(uint64_t tensors, void* const* grads, void* const*
  *                (up to 3.9, |b s^2 + c s^4| up to 15.5).
  *   steps 1 .. 64, eps > 0
  * A matrix's rows are *_stride elements apart. out may be the matrix itself (same
- * address, stride and type); no other written matrix may share an element with
- * another one of the list (columns of the same wider rows are separate matrices).
+ * address, stride and type). No other written matrix may share an element with
+ * another one of the list, nor lie among its rows in another way than in other
+ * columns of the same wider rows, of which each may have all, some or a single one.
  * Sides up to 2^24, the shorter one up to 2^15, up to 2^32 elements.
  * workspace: hkv_orthogonalize_workspace_bytes(...) of the same matrices (in hkv_muon_update the
  * weights' types).
