@@ -11,7 +11,9 @@ float16 whose rows may lie inside wider ones (stride(0) >= vocab, stride(1) ==
 ``stream`` (a ``torch.cuda.Stream`` or a handle; torch's current stream by
 default), and what a call allocates belongs to that stream. Gradients are
 returned, not recorded: pass one on with ``logits.backward(grad)``. A gradient
-written over its logits (``grad_out=logits``) is written behind autograd's back.
+written over its logits (``grad_out=logits``) is written behind autograd's back;
+what ``orthogonalize`` and ``muon_update`` write in place counts as modified, so that
+a backward pass that saved it fails instead of taking the new values.
 """
 
 from __future__ import annotations
@@ -470,6 +472,9 @@ def _matrix(t, name, i):
     return KINDS[t.dtype], s0 if rows > 1 else cols
 
 
+_modified = torch.autograd.graph.increment_version  # tensors that were written by address
+
+
 @functools.lru_cache(maxsize=64)
 def _steps(steps, coefficients):
     """a, b, c of every step, for a triple or a sequence of them."""
@@ -529,6 +534,7 @@ def orthogonalize(matrices, *, steps: int = 5, coefficients=NEWTON_SCHULZ, eps: 
     ws = _workspace(nb, dev)
     _check(load().hkv_orthogonalize(len(matrices), table.buffer_info()[0], steps, c.buffer_info()[0], eps,
                                     ws.data_ptr(), nb, _current_stream(dev)))
+    _modified(out)
     return out
 
 
@@ -585,3 +591,4 @@ def muon_update(weights, grads, momenta, lr, *, momentum: float = 0.95, nesterov
     ws = _workspace(nb, dev)
     _check(load().hkv_muon_update(n, bytes(table), momentum, bool(nesterov), weight_decay, steps, c.buffer_info()[0],
                                   eps, ws.data_ptr(), nb, _current_stream(dev)))
+    _modified(weights + momenta)
