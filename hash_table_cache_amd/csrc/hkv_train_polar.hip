@@ -720,6 +720,16 @@ uint64_t lay_out(const PolarMatrix& m, uint32_t tile, bool split, uint32_t cuts,
 // from 256 tiles on, or 128 of 256 or where both halves meet (4 of 1024 x 2048
 // float32, all steps: 787 us against 846, but bf16 467 against 407; 12 of 500 x 1300
 // bf16: 23 us with 64 against 29 us with 128).
+//
+// Tiles of 256 have to be worth their padding and their last round of the chip. A
+// matrix counts for them if they pad it to at most 5/4 of what tiles of 64 do (32 of
+// 192 x 4096 bf16: 761 us, 571 us with 64; 16 of 300 x 8192: 1689 and 1163; 640 x
+// 4096, padded to 6/5, still 1670 against 1696), and they are taken where their
+// rounds of 256 take no longer than those of 512 tiles of 128, two of which a compute
+// unit has at a time, at 23/20 of the rate (16 of 1024 x 4096, 4 rounds each: 2641 us
+// against 2955 us with 128; 8 of 1500 x 1500, 2 rounds against 3: 1461 against 1348 us;
+// 11 of 1100 x 1100: 1199 against 782 us). What does not count goes apart from what
+// does: 4096 x 4096 with 100 of 70 x 70 2478 us, 3157 us in one group of 256.
 constexpr uint64_t kManyBig = 256, kManyTiles = 512, kManyPairs = 256, kManyUpper = 256, kManyUpperPairs = 128;
 
 struct Plan {
@@ -735,16 +745,15 @@ Plan make_plan(const PolarMatrix* m, uint32_t n) {
   for (uint32_t i = 0; i < n; ++i)
     if (is_narrow(m[i])) plan.narrow.push_back(m[i]);
   plan.bytes = narrow_workspace_bytes(plan.narrow.data(), (uint32_t)plan.narrow.size());
-  for (int kind = 0; kind < 4; ++kind) {  // precision, and whether the shorter side fits a tile of 64
+  const auto area = [&](uint32_t i, uint64_t tile) { return up(m[i].rows, tile) * up(m[i].cols, tile); };
+  // Adds the groups of matrices of one precision, in tiles of 256 or of what they are enough for.
+  const auto add = [&](const std::vector<uint32_t>& list, bool split, bool small, bool whole) {
     const uint32_t begin = (uint32_t)plan.order.size();
-    uint64_t tiles = 0, big = 0, upper[3] = {}, rounds = 0;  // upper: of 64, 128 and 256
+    uint64_t tiles = 0, upper[3] = {}, rounds = 0;  // upper: of 64, 128 and 256
     uint32_t longest = 0;
-    const bool split = kind & 1, small = kind & 2;
-    for (uint32_t i = 0; i < n; ++i) {
-      if (is_narrow(m[i]) || splits(m[i]) != split || (std::min(m[i].rows, m[i].cols) <= 64) != small) continue;
+    for (const uint32_t i : list) {
       plan.order.push_back(i);
-      tiles += up(m[i].rows, 128) / 128 * (up(m[i].cols, 128) / 128);
-      big += up(m[i].rows, 256) / 256 * (up(m[i].cols, 256) / 256);
+      tiles += area(i, 128) / (128 * 128);
       for (int k = 0; k < 3; ++k) {
         const uint64_t side = up(std::min(m[i].rows, m[i].cols), 64 << k) / (64 << k);
         upper[k] += side * (side + 1) / 2;
@@ -757,7 +766,7 @@ Plan make_plan(const PolarMatrix* m, uint32_t n) {
       return std::min(m[a].rows, m[a].cols) > std::min(m[b].rows, m[b].cols);
     });
     const uint64_t many = plan.order.size() - begin;
-    const uint32_t tile = small ? 64 : big >= kManyBig ? 256 : tiles >= (split ? kManyPairs : kManyTiles) && rounds >= 12 * many ? 128 : 64;
+    const uint32_t tile = whole ? 256 : !small && tiles >= (split ? kManyPairs : kManyTiles) && rounds >= 12 * many ? 128 : 64;
     const uint64_t most = split ? kManyUpperPairs : kManyUpper;
     const uint32_t gram_tile = tile == 256 && upper[2] >= kManyUpperPairs ? 256 : tile >= 128 && upper[1] >= most ? 128 : 64;
     if (tile < 256) {  // long and short ones by turns: every die has both
@@ -784,6 +793,31 @@ Plan make_plan(const PolarMatrix* m, uint32_t n) {
       plan.groups.push_back(g);
       at = g.end;
     }
+  };
+  for (const bool split : {false, true}) {
+    std::vector<uint32_t> small, large, others;
+    uint64_t big = 0, tiles = 0;  // large's tiles of 256 and of 128
+    for (uint32_t i = 0; i < n; ++i) {
+      if (is_narrow(m[i]) || splits(m[i]) != split) continue;
+      if (std::min(m[i].rows, m[i].cols) <= 64) {
+        small.push_back(i);
+      } else if (4 * area(i, 256) <= 5 * area(i, 64)) {
+        large.push_back(i);
+        big += area(i, 256) / (256 * 256);
+        tiles += area(i, 128) / (128 * 128);
+      } else {
+        others.push_back(i);
+      }
+    }
+    const bool whole = big >= kManyBig && 40 * up(big, 256) / 256 <= 23 * up(tiles, 512) / 512;
+    if (!whole) {
+      large.insert(large.end(), others.begin(), others.end());
+      std::sort(large.begin(), large.end());
+      others.clear();
+    }
+    add(large, split, false, whole);
+    add(others, split, false, false);
+    add(small, split, true, false);
   }
   return plan;
 }

@@ -30,7 +30,7 @@ def test_few_directions(shape, steps):
         D.assert_rounded(o, P.polar(u.double(), steps), steps, f"{kind} {rank} of {shape}")
 
 
-@pytest.mark.parametrize("shape,count", [((300, 500), 12), ((800, 1600), 6), ((1100, 2300), 6)])
+@pytest.mark.parametrize("shape,count", [((300, 500), 12), ((800, 1600), 6), ((1100, 2300), 6), ((1000, 2000), 8)])
 def test_tiles(shape, count):
     """Tiles of 64, 128 and 256."""
     import hash_table_cache_amd as H
