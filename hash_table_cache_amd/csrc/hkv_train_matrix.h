@@ -97,6 +97,18 @@ __device__ __forceinline__ void store_kind(void* p, uint32_t kind, uint64_t i, u
     store_few(static_cast<_Float16*>(p) + i, n, v);
 }
 
+// The float next to v, of two the odd one, where v is none: rounded to 16 bits it gives
+// what v would at once. (By way of the nearest float, what lies within 2^-25 of the
+// middle between two of 16 bits would be taken for the middle.)
+__device__ __forceinline__ float odd_float(double v) {
+  const float f = (float)v;
+  const double g = (double)f;
+  uint32_t bits = __builtin_bit_cast(uint32_t, f);
+  if (fabs(g) > fabs(v)) --bits;
+  if (g < v || g > v) bits |= 1;
+  return as_float(bits);
+}
+
 // The update that is orthogonalised, n elements of a row, in 64 bits. MOVE: the
 // momentum takes the gradient in first.
 template <bool MOVE>

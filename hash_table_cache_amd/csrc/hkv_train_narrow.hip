@@ -355,7 +355,8 @@ struct Narrow {
     if (m.momentum)
       cells(m, it.flip, [&](uint64_t row, uint32_t col, uint32_t at) {
         T* w = out + row * m.out_stride + col;
-        *w = (T)(float)(m.keep * (double)(float)*w + m.step * (double)(sh.cells[at] * (1.0f / kUnit)));
+        const double v = m.keep * (double)(float)*w + m.step * (double)(sh.cells[at] * (1.0f / kUnit));
+        *w = (T)(sizeof(T) == 4 ? (float)v : odd_float(v));
       });
     else
       cells(m, it.flip, [&](uint64_t row, uint32_t col, uint32_t at) {

@@ -612,7 +612,10 @@ __device__ __forceinline__ void write_out(Product<T, SPLIT>& m, const PolarItem&
         float old[4];
         load_kind(w.out, w.out_kind, at, few, old);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = (float)(w.keep * (double)old[k] + w.step * (double)o[k]);
+        for (int k = 0; k < 4; ++k) {
+          const double v = w.keep * (double)old[k] + w.step * (double)o[k];
+          o[k] = w.out_kind == kF32 ? (float)v : odd_float(v);
+        }
       }
       store_kind(w.out, w.out_kind, at, few, o);
     }
