@@ -306,6 +306,10 @@ hkv_status check_sides(uint64_t rows, uint64_t cols, uint64_t i) {
   return HKV_OK;
 }
 
+// Norms are 0 or far above it: no float's square comes near, nor do the momentum's
+// shares of one. The kernels divide by eps, which for a smaller one would overflow.
+constexpr double kLeastEps = 1e-200;
+
 hkv_status run_polar(Buffers& buffers, const std::vector<hkvt::PolarMatrix>& list, const hkvt::PolarRule& rule,
                      uint32_t steps, const double* coefficients, void* workspace, uint64_t workspace_bytes,
                      hipStream_t stream, const char* what) {
@@ -611,7 +615,7 @@ HKV_API hkv_status hkv_orthogonalize(uint64_t matrices, const hkv_matrix* list, 
                       (uint32_t)m.in_dtype, (uint32_t)m.out_dtype});
     }
     if (places.clash()) return fail(HKV_EINVAL, "two matrices overlap, and one of them is written");
-    return run_polar(buffers, todo, hkvt::PolarRule{0.0, eps, 0}, steps, coefficients, workspace, workspace_bytes,
+    return run_polar(buffers, todo, hkvt::PolarRule{0.0, std::max(eps, kLeastEps), 0}, steps, coefficients, workspace, workspace_bytes,
                      stream, "hkv_orthogonalize launch");
   });
 }
@@ -653,7 +657,7 @@ HKV_API hkv_status hkv_muon_update(uint64_t matrices, const hkv_muon_matrix* lis
                       (uint32_t)m.grad_dtype, (uint32_t)m.weight_dtype});
     }
     if (places.clash()) return fail(HKV_EINVAL, "two matrices overlap, and one of them is written");
-    return run_polar(buffers, todo, hkvt::PolarRule{momentum, eps, nesterov}, steps, coefficients, workspace,
+    return run_polar(buffers, todo, hkvt::PolarRule{momentum, std::max(eps, kLeastEps), nesterov}, steps, coefficients, workspace,
                      workspace_bytes, stream, "hkv_muon_update launch");
   });
 }
