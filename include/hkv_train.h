@@ -218,8 +218,9 @@ hkv_status hkv_clip_grad_norm(uint64_t tensors, void* const* grads, void* const*
  * constant). Further steps, and coefficients that move singular values apart,
  * multiply that, as they do a rounding of the matrix itself: by less than 2 a step.
  * In both precisions a direction without a singular value comes in at 2^-23 of X
- * and grows by a each step. A matrix of zeros gives zeros, one that holds NaN or
- * infinities NaN throughout.
+ * and grows by a each step. Halves hold X to 2^-37 at best: where a matrix's norm is
+ * f times below eps, results are off by 5e-12 sqrt(rows cols) f of their size besides.
+ * A matrix of zeros gives zeros, one that holds NaN or infinities NaN throughout.
  *   list         array of `matrices` entries in HOST memory, read during the call;
  *                matrices without an element are passed over
  *   coefficients [3 * steps] in HOST memory: a, b, c of each step. Refused where
@@ -232,7 +233,11 @@ hkv_status hkv_clip_grad_norm(uint64_t tensors, void* const* grads, void* const*
  * columns of the same wider rows, of which each may have all, some or a single one.
  * Sides up to 2^24, the shorter one up to 2^15, up to 2^32 elements.
  * workspace: hkv_orthogonalize_workspace_bytes(...) of the same matrices (in hkv_muon_update the
- * weights' types).
+ * weights' types). It is of the matrices that are worked on at a time, as many as fit into 4 GiB
+ * or a single one: 10 bytes an element (12 for float32 and float16 results) and 4 (8) for each of
+ * the shorter side's square, of sides padded to 64, 128 or 256. A matrix of up to 64 rows or
+ * columns and up to 65536 of the others takes 340 bytes for each of those instead; a longer one is
+ * padded to 64 like the others, 640 (768) bytes an element if it is a single row.
  */
 typedef struct hkv_matrix {
   const void* in;
