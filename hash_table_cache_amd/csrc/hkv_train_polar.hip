@@ -146,32 +146,34 @@ __global__ __launch_bounds__(kPolarThreads) void polar_pack_kernel(const PolarIt
 // A tile of T x T of a product of rows, acc[i][j] = sum over k of a[i][k] b[j][k],
 // by WM x WN waves of FM x FN fragments of 32 x 32 each. BOTH: both halves of a
 // number come together and meet in three products; where two buffers of them do
-// not fit (T = 256), the halves' products are three passes, one after the other.
+// not fit (T = 256), the halves' products are passes, one after the other. kWaves: on
+// a SIMD, which registers have to leave room for; with 256 threads that is as many
+// workgroups, with 512 half as many.
 template <int T, bool SPLIT>
 struct Shape;
 template <>
 struct Shape<64, false> {
-  static constexpr int WM = 2, WN = 2, FM = 1, FN = 1, kBuffers = 3, kBlocks = 3;
+  static constexpr int WM = 2, WN = 2, FM = 1, FN = 1, kBuffers = 3, kWaves = 3;
   static constexpr bool BOTH = false;
 };
 template <>
 struct Shape<64, true> {
-  static constexpr int WM = 2, WN = 2, FM = 1, FN = 1, kBuffers = 2, kBlocks = 2;
+  static constexpr int WM = 2, WN = 2, FM = 1, FN = 1, kBuffers = 2, kWaves = 2;
   static constexpr bool BOTH = true;
 };
 template <>
 struct Shape<128, false> {
-  static constexpr int WM = 2, WN = 2, FM = 2, FN = 2, kBuffers = 2, kBlocks = 2;
+  static constexpr int WM = 2, WN = 2, FM = 2, FN = 2, kBuffers = 2, kWaves = 2;
   static constexpr bool BOTH = false;
 };
 template <>
 struct Shape<128, true> {
-  static constexpr int WM = 2, WN = 4, FM = 2, FN = 1, kBuffers = 2, kBlocks = 2;
+  static constexpr int WM = 2, WN = 4, FM = 2, FN = 1, kBuffers = 2, kWaves = 2;
   static constexpr bool BOTH = true;
 };
 template <bool SPLIT>
 struct Shape<256, SPLIT> {
-  static constexpr int WM = 2, WN = 4, FM = 4, FN = 2, kBuffers = 2, kBlocks = 2;
+  static constexpr int WM = 2, WN = 4, FM = 4, FN = 2, kBuffers = 2, kWaves = 2;
   static constexpr bool BOTH = false;
 };
 
@@ -472,7 +474,7 @@ __device__ __forceinline__ void write_gram(Product<T, SPLIT>& m, const PolarItem
 }
 
 template <int T, bool SPLIT>
-__global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kBlocks)) void polar_gram_kernel(const PolarItem* items, uint32_t n,
+__global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kWaves)) void polar_gram_kernel(const PolarItem* items, uint32_t n,
                                                                                          const Dies dies) {
   __shared__ typename Product<T, SPLIT>::Shared sh;
   const PolarItem* item;
@@ -491,7 +493,7 @@ __global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kB
 // own (two of 10007 x 321 bf16: 42 us a step by 21 tiles, 9 us by 240 workgroups and
 // the sums; 200 x 60000: 590 us against 26 us).
 template <bool SPLIT>
-__global__ __launch_bounds__((Product<64, SPLIT>::kThreads), (Shape<64, SPLIT>::kBlocks)) void polar_cut_kernel(const PolarItem* items, uint32_t n,
+__global__ __launch_bounds__((Product<64, SPLIT>::kThreads), (Shape<64, SPLIT>::kWaves)) void polar_cut_kernel(const PolarItem* items, uint32_t n,
                                                                                         const Dies dies) {
   using M = Product<64, SPLIT>;
   __shared__ typename M::Shared sh;
@@ -536,7 +538,7 @@ __global__ __launch_bounds__((Product<64, SPLIT>::kThreads)) void polar_sum_kern
 
 // B without its diagonal, and E.
 template <int T, bool SPLIT>
-__global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kBlocks)) void polar_square_kernel(const PolarItem* items, uint32_t n,
+__global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kWaves)) void polar_square_kernel(const PolarItem* items, uint32_t n,
                                                                                            const Dies dies, float b, float c2) {
   __shared__ typename Product<T, SPLIT>::Shared sh;
   const PolarItem* item;
@@ -625,7 +627,7 @@ __device__ __forceinline__ void write_out(Product<T, SPLIT>& m, const PolarItem&
 // a X + B X of step `k`; the last one's goes to its destination. Columns of the
 // tile are rows of X^T. PRODUCTS of halves make B X.
 template <int T, bool SPLIT, bool LAST, int PRODUCTS>
-__global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kBlocks)) void polar_next_kernel(const PolarItem* items, uint32_t n,
+__global__ __launch_bounds__((Product<T, SPLIT>::kThreads), (Shape<T, SPLIT>::kWaves)) void polar_next_kernel(const PolarItem* items, uint32_t n,
                                                                                          const Dies dies, float a, uint32_t step) {
   __shared__ typename Product<T, SPLIT>::Shared sh;
   const PolarItem* item;
