@@ -29,11 +29,11 @@
 //     would be off by 7e-3, of rank 16 after 10 steps by 1.2 (2-norm). In the last
 //     two steps, after which it is multiplied once at most, the upper half is
 //     enough: 16 of about 2048 x 4096 9.0 ms (7.5 ms with it alone throughout, 10.0
-//     ms with both throughout), 2048 x 2048 534 us (422, 601), two of 10007 x 321
-//     275 us (247, 291). Results are off by 2e-4 to 1.6e-3, less than their rounding
-//     to bf16 (1.7e-3), for full, decaying and low-rank spectra and up to 6 steps. A
-//     has X's rounding in 2^-12 of itself; where all elements are rounded alike (a
-//     multiple of the identity) that moves all singular values alike, by up to 7e-3.
+//     ms with both throughout), two of 10007 x 321 275 us (247, 291). Results are off
+//     by 2e-4 to 1.6e-3, less than their rounding to bf16 (1.7e-3), for full,
+//     decaying and low-rank spectra and up to 6 steps. A is off by X's rounding, 2^-12
+//     of it; where all elements are rounded alike (a multiple of the identity) that
+//     moves all singular values alike, by up to 7e-3.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -398,12 +398,13 @@ struct Product {
 // Consecutive workgroups go to the 8 dies in turn. Each die takes an eighth of the
 // work, of tiles next to each other, so that what they share is in its cache (16 of
 // 2048 x 4096 bf16, all steps: 6.78 ms against 7.14 ms with an eighth of each matrix's
-// tiles to every die; 12 of 500 x 1300: 275 us against 310 us). Tiles of 256 are few
-// rounds of the chip, and a die with long products alone ends late: of many matrices
-// their work is cut into `rows` times 8 pieces, about half a matrix each, which go to
-// the dies forth and back, so that each has long products and, last, short ones (16
-// of 1100 x 3400 to 3000 x 5000: 7.48 ms against 7.85 ms; smaller tiles lose by it, 40 of
-// 128 x 512: 158 us against 142 us). `first`: each piece's first tile, and their number.
+// tiles to every die; 12 of 500 x 1300: 275 us against 310 us; both with one product for
+// B X in every step). Tiles of 256 are few rounds of the chip, and a die with long
+// products alone ends late: of many matrices their work is cut into `rows` times 8
+// pieces, about half a matrix each, which go to the dies forth and back, so that each
+// has long products and, last, short ones (16 of 1100 x 3400 to 3005 x 5005: 9.89 ms
+// against 10.20 ms; smaller tiles lose by it, 40 of 128 x 512: 178 us against 169 us).
+// `first`: each piece's first tile, and their number.
 constexpr uint32_t kMostRows = 4;
 
 struct Dies {
@@ -717,14 +718,14 @@ uint64_t lay_out(const PolarMatrix& m, uint32_t tile, bool split, uint32_t cuts,
 
 // Large tiles feed the matrix cores better, small ones are more workgroups and less
 // padding. A third product of 256 tiles of 256 has them (16 matrices of 2048 x 4096:
-// 797 us against 1041 us with 128; 4096 x 4096, all steps: 1910 against 2030 us); of
-// 512 tiles of 128, or 256 where both halves meet in them, those (4 of 1024 x 2048
-// float32: 71 us against 114 us with 64; 2048 x 2048 float32, all steps: 853 against
-// 948 us, but bf16 466 against 432) unless its rounds are few and its ends most of it
-// (12 of 500 x 1300: 40 and 39 us). A has half as many tiles: they are taken of that size
-// from 256 tiles on, or 128 of 256 or where both halves meet (4 of 1024 x 2048
-// float32, all steps: 787 us against 846, but bf16 467 against 407; 12 of 500 x 1300
-// bf16: 23 us with 64 against 29 us with 128).
+// 797 us against 1041 us with 128; 4096 x 4096, all steps: 2129 against 2445 us); of
+// 256 tiles of 128 those (all steps: 2500 x 2500 bf16 814 us against 1088 us with 64,
+// 2048 x 2048 501 and 535 us, of float32 761 and 916 us; 800 x 5000 bf16 302 and 279 us)
+// unless its rounds are few and its ends most of it (12 of 500 x 1300: 361 and 309 us).
+// A has half as many tiles: they are taken of that size from 256 tiles on, or 128 of
+// 256 or where both halves meet (4 of 1024 x 2048 float32, all steps: 753 us against
+// 809, but bf16 480 against 414; 12 of 500 x 1300 bf16: 23 us with 64 against 29 us
+// with 128).
 //
 // Tiles of 256 have to be worth their padding and their last round of the chip. A
 // matrix counts for them if they pad it to at most 5/4 of what tiles of 64 do (32 of
@@ -735,7 +736,7 @@ uint64_t lay_out(const PolarMatrix& m, uint32_t tile, bool split, uint32_t cuts,
 // against 2955 us with 128; 8 of 1500 x 1500, 2 rounds against 3: 1461 against 1348 us;
 // 11 of 1100 x 1100: 1199 against 782 us). What does not count goes apart from what
 // does: 4096 x 4096 with 100 of 70 x 70 2478 us, 3157 us in one group of 256.
-constexpr uint64_t kManyBig = 256, kManyTiles = 512, kManyPairs = 256, kManyUpper = 256, kManyUpperPairs = 128;
+constexpr uint64_t kManyBig = 256, kManyTiles = 256, kManyUpper = 256, kManyUpperPairs = 128;
 
 struct Plan {
   std::vector<uint32_t> order;
@@ -771,7 +772,7 @@ Plan make_plan(const PolarMatrix* m, uint32_t n) {
       return std::min(m[a].rows, m[a].cols) > std::min(m[b].rows, m[b].cols);
     });
     const uint64_t many = plan.order.size() - begin;
-    const uint32_t tile = whole ? 256 : !small && tiles >= (split ? kManyPairs : kManyTiles) && rounds >= 12 * many ? 128 : 64;
+    const uint32_t tile = whole ? 256 : !small && tiles >= kManyTiles && rounds >= 12 * many ? 128 : 64;
     const uint64_t most = split ? kManyUpperPairs : kManyUpper;
     const uint32_t gram_tile = tile == 256 && upper[2] >= kManyUpperPairs ? 256 : tile >= 128 && upper[1] >= most ? 128 : 64;
     if (tile < 256) {  // long and short ones by turns: every die has both
